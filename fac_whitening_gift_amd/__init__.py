@@ -18,4 +18,8 @@ from ._lib import (  # noqa: F401
     SCALE_TENSOR, SCALE_BLOCK128, SCALE_MXFP4, MX_BLOCK, FLAG_NONFINITE, FLAG_ZERO_AMAX, EXPORTS,
     COEF_ALPHA, COEF_BETA, COEF_LAMBDA_ISO, COEF_LAMBDA_FLOOR, COEF_TRACE, COEF_SIGMA2_TAIL,
     COEF_DW, COEF_DU, COEF_COUNT,
+    MxOperand, gift_mx_bytes, gift_mx_quantize, gift_mx_dequantize, gift_mx_matmul,
+    gift_mx_matmul_workspace_bytes, gift_mx_linear, gift_mx_linear_workspace_bytes,
+    NORM_LAYER, NORM_RMS, gift_norm_forward, gift_norm_backward,
+    gift_norm_backward_workspace_bytes,
 )

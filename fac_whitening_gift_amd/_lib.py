@@ -7,6 +7,7 @@ is not built it raises instead of falling back to anything else.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -36,6 +37,8 @@ FLAG_NONFINITE, FLAG_ZERO_AMAX = 1, 2
 OP_WHITEN_QUANTIZE, OP_DEQUANT_UNWHITEN, OP_EUCLID_ROUNDTRIP, OP_ROUNDTRIP_ERROR = 0, 1, 2, 3
 OP_UNWHITEN_F32 = 4
 
+NORM_LAYER, NORM_RMS = 0, 1
+
 COEF_ALPHA, COEF_BETA, COEF_LAMBDA_ISO, COEF_LAMBDA_FLOOR, COEF_TRACE, COEF_SIGMA2_TAIL = range(6)
 COEF_DW = 8
 COEF_DU = 8 + RANK
@@ -54,6 +57,9 @@ EXPORTS = (
     "gift_refresh_factors", "gift_refresh_group_workspace_bytes", "gift_build_hash",
     "gift_dequant_accumulate", "gift_unwhiten_f32", "gift_block_factor_pack_bytes",
     "gift_whiten_quantize_static", "gift_static_scratch_bytes", "gift_factor_pack_bytes_rank",
+    "gift_mx_bytes", "gift_mx_quantize", "gift_mx_dequantize", "gift_mx_matmul",
+    "gift_mx_matmul_workspace_bytes", "gift_mx_linear", "gift_mx_linear_workspace_bytes",
+    "gift_norm_forward", "gift_norm_backward", "gift_norm_backward_workspace_bytes",
 )
 
 
@@ -82,6 +88,10 @@ class _Layer(ctypes.Structure):
                 ("W_out", ctypes.c_void_p)]
 
 
+class _Mx(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -96,6 +106,7 @@ def load():
     P, I, I64, SZ, U64, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t,
                              ctypes.c_uint64, ctypes.c_float)
     LP = ctypes.POINTER(_Layer)
+    MP = ctypes.POINTER(_Mx)
     sig = {
         "gift_refresh_factor": (I, [P, I, I64, ctypes.POINTER(_Factor), F, I, I, I, U64, P, P, P,
                                     P, SZ, P]),
@@ -120,6 +131,16 @@ def load():
         "gift_prepare_factor": (I, [ctypes.POINTER(_Factor), P]),
         "gift_refresh_factors": (I, [ctypes.POINTER(_RefreshInput), I, F, I, I, I, P, P, SZ, P]),
         "gift_refresh_group_workspace_bytes": (SZ, [ctypes.POINTER(_RefreshInput), I, I]),
+        "gift_mx_bytes": (SZ, [I64, I64]),
+        "gift_mx_quantize": (I, [P, I, I64, I64, I64, MP, MP, P, P]),
+        "gift_mx_dequantize": (I, [MP, P, I, I64, P]),
+        "gift_mx_matmul": (I, [MP, MP, P, P, I, I64, I, P, SZ, P]),
+        "gift_mx_matmul_workspace_bytes": (SZ, [I64, I64, I64]),
+        "gift_mx_linear": (I, [P, I, I64, I64, MP, P, P, I, I64, P, P, SZ, P]),
+        "gift_mx_linear_workspace_bytes": (SZ, [I64, I64, I64]),
+        "gift_norm_forward": (I, [P, I, I64, I64, I, P, P, F, P, P, P, P]),
+        "gift_norm_backward": (I, [P, P, I, I64, I64, I, P, P, P, P, P, P, I, P, SZ, P]),
+        "gift_norm_backward_workspace_bytes": (SZ, [I64, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -545,3 +566,271 @@ def gift_draw_sketch(d_in, width=SKETCH_WIDTH, seed=0, out=None, device="cuda", 
     _check(load().gift_draw_sketch(_ptr(out), d_in, width,
                                    ctypes.c_uint64(seed & 0xFFFFFFFFFFFFFFFF), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------
+# MXFP4 operands and products, layer norm and RMS norm
+# --------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _matrix(t, name, device=None, shape=None, dtype=None):
+    """-> (pointer, dtype code, rows, cols, leading dimension) of a 2-D device
+    tensor whose rows are contiguous."""
+    code = _DTYPES.get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be %s, got %s" % (name, dtype or "bf16 or fp32", t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
+                                                           shape or "rows x columns"))
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.data_ptr(), code, rows, cols, ld
+
+
+def _vector(t, n, name, device):
+    """-> pointer of an optional contiguous fp32 device vector of n elements."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != (n,) \
+            or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be %d contiguous fp32 elements on %s" % (name, n, device))
+    return t.data_ptr()
+
+
+def _flags_ptr(flags, device):
+    if flags is None:
+        return None
+    if flags.device != device or flags.element_size() != 4 or flags.numel() < 1:
+        raise ValueError("flags must be a 4-byte word on %s" % device)
+    return flags.data_ptr()
+
+
+def _out(out, shape, dtype, device):
+    return out if out is not None else torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, ws):
+    """-> (workspace tensor, its pointer, its bytes); nothing for 0 bytes."""
+    if ws is None:
+        if nbytes == 0:
+            return None, None, 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous, on %s" % device)
+    have = ws.numel() * ws.element_size()
+    if have < nbytes:
+        raise ValueError("workspace too small: %d < %d bytes" % (have, nbytes))
+    return ws, ws.data_ptr(), have
+
+
+def _on_stream(fn):
+    """Run a call given a stream as if that were the current one, so that what
+    it allocates (outputs, workspaces) belongs to that stream too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kwargs)
+    return call
+
+
+def _enqueue(device, stream, fn, *args):
+    """Call a library function with torch's current stream of the tensors'
+    device appended."""
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != GIFT_OK:
+        _check(status)
+
+
+class MxOperand:
+    """An MXFP4 operand: a rows x k matrix quantized in blocks of 32 along k,
+    in the layout of gift_mx (include/gift.h).  data: uint8 device tensor of
+    gift_mx_bytes(rows, k), allocated when not given; gift_mx_quantize fills
+    it.  shape is (rows, k)."""
+
+    def __init__(self, rows, k, device="cuda", data=None):
+        self.rows, self.k = int(rows), int(k)
+        nbytes = int(load().gift_mx_bytes(self.rows, self.k))
+        if nbytes == 0:
+            raise ValueError("MXFP4 operand of %d x %d is out of range" % (self.rows, self.k))
+        if data is None:
+            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _dev(data, torch.uint8, (nbytes,), "data")
+        self.data = data
+        self._struct = _Mx(self.rows, self.k, data.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+    @property
+    def shape(self):
+        return (self.rows, self.k)
+
+    @property
+    def device(self):
+        return self.data.device
+
+
+def _operand(op, name, device=None):
+    if not isinstance(op, MxOperand):
+        raise ValueError("%s must be an MxOperand" % name)
+    if device is not None and op.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, op.device, device))
+    return op._ref
+
+
+def _quantize_target(want, rows, k, device, name):
+    if want is None or want is False:
+        return None
+    if want is True:
+        return MxOperand(rows, k, device)
+    _operand(want, name, device)
+    if want.shape != (rows, k):
+        raise ValueError("%s has shape %s, expected %s" % (name, want.shape, (rows, k)))
+    return want
+
+
+def gift_mx_bytes(rows, k):
+    return int(load().gift_mx_bytes(rows, k))
+
+
+@_on_stream
+def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
+    """Quantize x (rows x cols, bf16 or fp32) to MXFP4 in one read: by_row /
+    by_col True (allocate) or an MxOperand to fill, of x and of its transpose.
+    -> (by_row operand or None, by_col operand or None)."""
+    ptr, dt, rows, cols, ld = _matrix(x, "x")
+    row = _quantize_target(by_row, rows, cols, x.device, "by_row")
+    col = _quantize_target(by_col, cols, rows, x.device, "by_col")
+    _enqueue(x.device, stream, load().gift_mx_quantize, ptr, dt, rows, cols, ld,
+             row._ref if row is not None else None, col._ref if col is not None else None,
+             _flags_ptr(flags, x.device))
+    return row, col
+
+
+@_on_stream
+def gift_mx_dequantize(a, dtype=torch.float32, out=None, stream=None):
+    """-> rows x k tensor of the values the operand stands for."""
+    ref = _operand(a, "a")
+    out = _out(out, a.shape, dtype, a.device)
+    ptr, dt, _, _, ld = _matrix(out, "out", a.device, a.shape)
+    _enqueue(a.device, stream, load().gift_mx_dequantize, ref, ptr, dt, ld)
+    return out
+
+
+def gift_mx_matmul_workspace_bytes(m, n, k):
+    return int(load().gift_mx_matmul_workspace_bytes(m, n, k))
+
+
+@_on_stream
+def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=False, ws=None,
+                   stream=None):
+    """a (M x k), b (N x k) operands -> a b^T (+ bias), M x N of dtype (or out's);
+    accumulate: out (fp32) += the product."""
+    ra, rb = _operand(a, "a"), _operand(b, "b", a.device)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    dev, shape = a.device, (a.rows, b.rows)
+    out = _out(out, shape, dtype, dev)
+    ptr, dt, _, _, ld = _matrix(out, "out", dev, shape)
+    lib = load()
+    keep, wp, wb = _scratch(lib.gift_mx_matmul_workspace_bytes(a.rows, b.rows, a.k), dev, ws)
+    _enqueue(dev, stream, lib.gift_mx_matmul, ra, rb, _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
+             1 if accumulate else 0, wp, wb)
+    return out
+
+
+def gift_mx_linear_workspace_bytes(rows, n, k):
+    return int(load().gift_mx_linear_workspace_bytes(rows, n, k))
+
+
+@_on_stream
+def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, stream=None):
+    """x (rows x k, bf16 or fp32) quantized in the call, w an operand (n x k)
+    -> x w^T (+ bias), rows x n of dtype (x's when not given)."""
+    dev = x.device
+    ptr, dt, rows, _, ld = _matrix(x, "x", w.device)
+    rw = _operand(w, "w", dev)
+    if x.shape[1] != w.k:
+        raise ValueError("x has %d columns, w sums over %d" % (x.shape[1], w.k))
+    shape = (rows, w.rows)
+    out = _out(out, shape, dtype or x.dtype, dev)
+    yp, ydt, _, _, ldy = _matrix(out, "out", dev, shape)
+    lib = load()
+    keep, wp, wb = _scratch(lib.gift_mx_linear_workspace_bytes(rows, w.rows, w.k), dev, ws)
+    _enqueue(dev, stream, lib.gift_mx_linear, ptr, dt, rows, ld, rw, _vector(bias, w.rows, "bias", dev),
+             yp, ydt, ldy, _flags_ptr(flags, dev), wp, wb)
+    return out
+
+
+def _dense(t, name, device=None, shape=None, dtype=None):
+    ptr, dt, rows, cols, ld = _matrix(t, name, device, shape, dtype)
+    if ld != cols:
+        raise ValueError("%s must be contiguous" % name)
+    return ptr, dt, rows, cols
+
+
+@_on_stream
+def gift_norm_forward(x, weight=None, bias=None, eps=1e-5, kind=NORM_LAYER, out=None, mean=None,
+                      rstd=None, stream=None):
+    """Norm of every row of x (rows x d, bf16 or fp32); weight and bias: d fp32
+    or None.  -> (y, mean (None for NORM_RMS), rstd)."""
+    dev = x.device
+    ptr, dt, rows, d = _dense(x, "x")
+    out = _out(out, (rows, d), x.dtype, dev)
+    yp = _dense(out, "out", dev, (rows, d), x.dtype)[0]
+    if kind == NORM_LAYER:
+        mean = _out(mean, (rows,), torch.float32, dev)
+    elif mean is not None:
+        raise ValueError("NORM_RMS has no mean")
+    rstd = _out(rstd, (rows,), torch.float32, dev)
+    _enqueue(dev, stream, load().gift_norm_forward, ptr, dt, rows, d, kind,
+             _vector(weight, d, "weight", dev), _vector(bias, d, "bias", dev), eps, yp,
+             _vector(mean, rows, "mean", dev), _vector(rstd, rows, "rstd", dev))
+    return out, mean, rstd
+
+
+def gift_norm_backward_workspace_bytes(rows, d):
+    return int(load().gift_norm_backward_workspace_bytes(rows, d))
+
+
+@_on_stream
+def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dweight=None, dbias=None,
+                       accumulate=False, ws=None, stream=None):
+    """Gradients of gift_norm_forward for its statistics.  dx, dweight, dbias: a
+    tensor to fill, False to leave out, None to allocate (dbias None: only for
+    NORM_LAYER); accumulate adds to the given dweight and dbias.
+    -> (dx, dweight, dbias), None for what was left out."""
+    dev = x.device
+    ptr, dt, rows, d = _dense(x, "x")
+    gp = _dense(dy, "dy", dev, (rows, d), x.dtype)[0]
+    if dbias is None and kind != NORM_LAYER:
+        dbias = False
+    if accumulate and (dweight is None or dbias is None):
+        raise ValueError("accumulate adds to given gradients")
+    dx = None if dx is False else _out(dx, (rows, d), x.dtype, dev)
+    dweight = None if dweight is False else _out(dweight, (d,), torch.float32, dev)
+    dbias = None if dbias is False else _out(dbias, (d,), torch.float32, dev)
+    xp = None if dx is None else _dense(dx, "dx", dev, (rows, d), x.dtype)[0]
+    lib = load()
+    need = lib.gift_norm_backward_workspace_bytes(rows, d) \
+        if dweight is not None or dbias is not None else 0
+    keep, wp, wb = _scratch(need, dev, ws)
+    _enqueue(dev, stream, lib.gift_norm_backward, gp, ptr, dt, rows, d, kind,
+             _vector(weight, d, "weight", dev), _vector(mean, rows, "mean", dev),
+             _vector(rstd, rows, "rstd", dev), xp, _vector(dweight, d, "dweight", dev),
+             _vector(dbias, d, "dbias", dev), 1 if accumulate else 0, wp, wb)
+    return dx, dweight, dbias

@@ -24,7 +24,8 @@ PROBE_LIB = os.path.join(HERE, "libgift_probe.so")
 PROBE_HEADER = os.path.join(ROOT, "include", "gift_probe.h")
 ARCH = "gfx950"
 
-SOURCES = ["api.cpp", "roundtrip.hip", "roundtrip_rt2.hip", "refresh.hip"]
+SOURCES = ["api.cpp", "api_layer.cpp", "roundtrip.hip", "roundtrip_rt2.hip", "refresh.hip", "mx.hip",
+           "norm.hip"]
 
 # -packed-fp32-ops: keep hipcc from forming packed fp32 VALU ops (the host
 # pass does not know the feature and warns; that is expected).

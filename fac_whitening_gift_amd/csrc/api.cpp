@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "device.hpp"
+#include "host.hpp"
 
 namespace gift {
 // roundtrip.hip, built with 64-row tiles (rt4) and 32-row tiles (rt2)
@@ -93,9 +94,9 @@ gift_status refresh_factors(const gift_refresh_input* in, int n, float damp_eps,
 
 using namespace gift;
 
-namespace {
+static thread_local std::string t_err;
 
-thread_local std::string t_err;
+namespace gift {
 
 gift_status fail(gift_status s, const char* fmt, ...) {
   char buf[512];
@@ -111,13 +112,18 @@ gift_status hip_fail(hipError_t e, const char* where) {
   return fail(GIFT_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+gift_status check_ws(void* ws, size_t ws_bytes, size_t need) {
+  if (ws_bytes < need)
+    return fail(GIFT_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  if (need && !ws) return fail(GIFT_ERR_INVALID_ARG, "workspace is NULL");
+  if (ws && ((uintptr_t)ws % kAlign))
+    return fail(GIFT_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return GIFT_OK;
+}
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+}  // namespace gift
 
-constexpr int64_t kMaxDim = int64_t(1) << 24;
-constexpr int64_t kMaxElems = int64_t(1) << 36;
+namespace {
 
 enum class Op { Whiten, Dequant, Euclid, Error, Accumulate, UnwhitenF32 };
 
@@ -472,15 +478,6 @@ gift_status run_grouped(const gift_layer* layers, int n, Op op, bool block, void
 }
 
 int tiles_flat(const gift_layer& L) { return flat_tiles(L.d_out * L.d_in); }
-
-gift_status check_ws(void* ws, size_t ws_bytes, size_t need) {
-  if (ws_bytes < need)
-    return fail(GIFT_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
-  if (need && !ws) return fail(GIFT_ERR_INVALID_ARG, "workspace is NULL");
-  if (ws && ((uintptr_t)ws % kAlign))
-    return fail(GIFT_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  return GIFT_OK;
-}
 
 // Scratch of gift_whiten_quantize_static: a file-scope device array, one copy
 // per GPU, held until the process ends.  Host code never uses the array's

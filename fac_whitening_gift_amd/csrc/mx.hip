@@ -1,0 +1,752 @@
+// MXFP4 operands and their product on gfx950 (gift_mx_* of include/gift.h).
+//
+// An operand (rows x k) is cut into blocks of 64 rows x 128 k elements, 4352
+// bytes each: four 1 KB fragments of 16 rows, then 256 bytes of scales.  A
+// fragment is what one v_mfma_scale_f32_16x16x128_f8f6f4 takes from a wave:
+// lane l holds row l % 16, k elements 32 (l / 16) .. +31, i.e. exactly one
+// 32-element MX block (16 bytes of E2M1 codes) with one E8M0 scale.  The
+// scale dword of lane l holds the bytes of the block's four fragments, which
+// the instruction picks by its byte select, so neither codes nor scales need
+// any rearranging between memory and the matrix cores.
+#include <type_traits>
+
+#include "device.hpp"
+#include "mx.hpp"
+
+namespace gift {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
+
+constexpr int kFmtFp4 = 4;  // f8f6f4 operand format: E2M1
+
+// acc += (fragment a) x (fragment b)^T with byte SA of a's and SB of b's scales
+template <int SA, int SB>
+__device__ __forceinline__ f32x4 mx_mfma(const i32x4& a, int sa, const i32x4& b, int sb, f32x4 acc) {
+  const i32x8 va = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  const i32x8 vb = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, acc, kFmtFp4, kFmtFp4, SA, sa, SB, sb);
+}
+
+__device__ __forceinline__ float ld1(const float* p) { return *p; }
+__device__ __forceinline__ float ld1(const __bf16* p) { return (float)*p; }
+
+// ---------------------------------------------------------------------------
+// quantize
+// ---------------------------------------------------------------------------
+
+// One MX block: 32 values -> 16 bytes of codes and the scale byte.
+__device__ __forceinline__ uint4 mx_block(const float (&v)[32], uint32_t& code, uint32_t& flags) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t b = abs_bits(v[i]);
+    m = m > b ? m : b;
+  }
+  code = mx_scale_code(m, flags);
+  const float s = mx_scale_operand(code);
+  const bool nonfinite = code == kMxScaleNaN;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = mx_encode4(make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]), s, nonfinite) |
+           mx_encode4(make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]), s, nonfinite) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+
+constexpr int kQTile = 128;     // the tile is kQTile x kQTile: one k step of either operand
+constexpr int kQThreads = 256;
+
+// One tile of X through LDS.  By rows: a thread takes 32 consecutive columns
+// of a row, threads in fragment order, so a wave writes a whole 1 KB
+// fragment.  By columns: a thread takes two neighbouring columns of 32 rows.
+// The LDS row stride is 4 banks past a multiple of 64, so the 16 rows of a
+// fragment fall in 16 distinct groups of 4 banks.
+template <class T, bool kByRow, bool kByCol>
+__global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X, int64_t rows,
+                                                        int64_t cols, int64_t ld, uint8_t* R,
+                                                        uint8_t* C, int col_tiles, bool vec,
+                                                        uint32_t* flags) {
+  constexpr int kPer = 16 / sizeof(T);                  // elements of a 16-byte load
+  constexpr int kStride = kQTile * sizeof(T) + 16;      // bytes of an LDS row
+  constexpr int kChunks = kQTile / kPer;                // 16-byte chunks of a row
+  constexpr int kLoads = kQTile * kChunks / kQThreads;  // chunks per thread
+  __shared__ __attribute__((aligned(16))) char lds[kQTile * kStride];
+  const int t = threadIdx.x;
+  const int tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
+  const int64_t r0 = (int64_t)tr * kQTile, c0 = (int64_t)tc * kQTile;
+  if (vec && r0 + kQTile <= rows && c0 + kQTile <= cols) {
+    uint4 v[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = t + i * kQThreads, r = e / kChunks, c = e % kChunks;
+      v[i] = *reinterpret_cast<const uint4*>(X + (r0 + r) * ld + c0 + c * kPer);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = t + i * kQThreads, r = e / kChunks, c = e % kChunks;
+      *reinterpret_cast<uint4*>(lds + r * kStride + c * 16) = v[i];
+    }
+  } else {
+    for (int e = t; e < kQTile * kQTile; e += kQThreads) {
+      const int r = e / kQTile, c = e % kQTile;
+      T x = (T)0.f;
+      if (r0 + r < rows && c0 + c < cols) x = X[(r0 + r) * ld + c0 + c];
+      *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = x;
+    }
+  }
+  __syncthreads();
+  uint32_t fl = 0;
+  if constexpr (kByRow) {
+    const int64_t panels = (rows + kMxRows - 1) / kMxRows;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = t + i * kQThreads;  // fragment-major: 8 fragments x 64 lanes
+      const int f = e >> 6, lane = e & 63, b = lane >> 4, r = f * 16 + (lane & 15);
+      const int64_t panel = (r0 >> 6) + (f >> 2);
+      if (panel >= panels) break;       // wave-uniform
+      float v[32];
+      const char* src = lds + r * kStride + b * 32 * sizeof(T);
+#pragma unroll
+      for (int j = 0; j < 32 / kPer; ++j) {
+        const uint4 q = *reinterpret_cast<const uint4*>(src + 16 * j);
+        if constexpr (sizeof(T) == 2) {
+          unpack2(q.x, v[8 * j], v[8 * j + 1]);
+          unpack2(q.y, v[8 * j + 2], v[8 * j + 3]);
+          unpack2(q.z, v[8 * j + 4], v[8 * j + 5]);
+          unpack2(q.w, v[8 * j + 6], v[8 * j + 7]);
+        } else {
+          v[4 * j] = __uint_as_float(q.x);
+          v[4 * j + 1] = __uint_as_float(q.y);
+          v[4 * j + 2] = __uint_as_float(q.z);
+          v[4 * j + 3] = __uint_as_float(q.w);
+        }
+      }
+      uint32_t code, bf = 0;
+      const uint4 w = mx_block(v, code, bf);
+      if (r0 + r < rows && c0 + b * 32 < cols) fl |= bf;
+      uint8_t* out = R + (panel * col_tiles + tc) * (int64_t)kMxPanel;
+      *reinterpret_cast<uint4*>(out + (f & 3) * 1024 + lane * 16) = w;
+      out[4096 + lane * 4 + (f & 3)] = (uint8_t)code;
+    }
+  }
+  if constexpr (kByCol) {
+    const int64_t panels = (cols + kMxRows - 1) / kMxRows;
+    const int64_t steps = (rows + kMxStep - 1) / kMxStep;
+    const int b = t >> 6, p = t & 63;  // rows 32 b .. +31, columns 2 p, 2 p + 1
+    const int c = 2 * p;
+    const int64_t panel = (c0 >> 6) + (c >> 6);
+    if (panel < panels) {
+      float lo[32], hi[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const char* src = lds + (b * 32 + j) * kStride + c * sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+          unpack2(*reinterpret_cast<const uint32_t*>(src), lo[j], hi[j]);
+        } else {
+          const float2 q = *reinterpret_cast<const float2*>(src);
+          lo[j] = q.x;
+          hi[j] = q.y;
+        }
+      }
+      uint32_t code0, code1, f0 = 0, f1 = 0;
+      const uint4 w0 = mx_block(lo, code0, f0);
+      const uint4 w1 = mx_block(hi, code1, f1);
+      if (r0 + b * 32 < rows) {
+        if (c0 + c < cols) fl |= f0;
+        if (c0 + c + 1 < cols) fl |= f1;
+      }
+      uint8_t* out = C + (panel * steps + tr) * (int64_t)kMxPanel;
+      const int f = (c >> 4) & 3, lane = b * 16 + (c & 15);
+      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16) = w0;
+      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16 + 16) = w1;
+      out[4096 + lane * 4 + f] = (uint8_t)code0;
+      out[4096 + lane * 4 + 4 + f] = (uint8_t)code1;
+    }
+  }
+  if (flags && fl) atomicOr(flags, fl);
+}
+
+// One 64 x 128 block of the operand per iteration: through LDS, then a
+// thread decodes 8 consecutive elements of a row.
+template <class T>
+__global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ A, int64_t rows,
+                                                    int64_t k, int steps, T* out, int64_t ld,
+                                                    bool vec) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kMxPanel];
+  const int t = threadIdx.x;
+  const int64_t panel = blockIdx.x / steps;
+  const int s = (int)(blockIdx.x - panel * steps);
+  const uint8_t* src = A + (int64_t)blockIdx.x * kMxPanel;
+  for (int i = t; i < kMxPanel / 16; i += 256)
+    *reinterpret_cast<uint4*>(lds + 16 * i) = *reinterpret_cast<const uint4*>(src + 16 * i);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = t + 256 * i, r = e >> 4, piece = e & 15, b = piece >> 2;
+    const int64_t row = panel * kMxRows + r, col = (int64_t)s * kMxStep + piece * 8;
+    if (row >= rows || col >= k) continue;
+    const int lane = b * 16 + (r & 15), f = r >> 4;
+    const uint32_t codes = *reinterpret_cast<const uint32_t*>(lds + f * 1024 + lane * 16 + (piece & 3) * 4);
+    const uint32_t sc = lds[4096 + lane * 4 + f];
+    const float4 a = mx_decode4(codes & 0xffffu, sc), c = mx_decode4(codes >> 16, sc);
+    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    T* dst = out + row * ld + col;
+    if (vec && col + 8 <= k) {
+      T o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(o) / 16; ++j)
+        reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(o)[j];
+    } else {
+      for (int j = 0; j < 8 && col + j < k; ++j) dst[j] = (T)v[j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// product
+// ---------------------------------------------------------------------------
+
+// 16 (or 4) bytes per lane from the raw buffer (at voff) into LDS at m0 +
+// 16 (4) lane.  Written in asm so that the compiler does not make every LDS
+// read wait for all copies in flight: the kernel waits with explicit vmcnt
+// counts.  The instruction writes no VGPR.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+constexpr uint32_t kRawBufferWord3 = 0x00020000u;  // gfx9 raw buffer, 32-bit data format
+
+// s_waitcnt immediate (gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4,
+// lgkmcnt 11:8), lgkmcnt 0
+constexpr int wait_vm_lgkm0(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+  return ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+}
+
+struct MxGemm {
+  const uint8_t* A;
+  const uint8_t* B;
+  void* C;
+  const float* bias;
+  float* part;     // split-k partials, [split][M][N] fp32
+  int64_t ldc;
+  int M, N;
+  int steps;       // k steps of 128
+  int per_split;   // k steps of a split
+  int tm, tn;      // tiles
+  int n_split;
+  int mode;        // kOut*
+  bool vec;        // C takes 4-element stores
+};
+enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2, kOutPart = 3 };
+
+// Tile of a workgroup: workgroups go to the XCDs in turn, so XCD x takes the
+// x-th contiguous run of the tiles in an order that walks bands of 4 tile
+// rows column by column: the tiles running together on one XCD share operand
+// panels in its L2.
+__device__ __forceinline__ void mx_tile(int id, int tm, int tn, int& ti, int& tj) {
+  const int n = tm * tn, q = n / kXcd, rem = n % kXcd, x = id % kXcd;
+  const int u = x * q + (x < rem ? x : rem) + id / kXcd;
+  constexpr int kBand = 4;
+  const int band = u / (kBand * tn), first = band * kBand;
+  const int h = tm - first < kBand ? tm - first : kBand;
+  const int v = u - first * tn;
+  ti = first + v % h;
+  tj = v / h;
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float x) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// Four consecutive columns n .. n + 3 of row m.
+__device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v, float* part) {
+  if (m >= g.M || n >= g.N) return;
+  const bool whole = n + 4 <= g.N;
+  if (g.mode == kOutPart) {
+    float* p = part + (int64_t)m * g.N + n;
+    if (whole && (g.N & 3) == 0) *reinterpret_cast<f32x4*>(p) = v;
+    else for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = v[e];
+    return;
+  }
+  if (g.bias)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < g.N) v[e] += g.bias[n + e];
+  const int64_t at = (int64_t)m * g.ldc + n;
+  if (g.mode == kOutBf16) {
+    uint16_t* p = static_cast<uint16_t*>(g.C) + at;
+    if (whole && g.vec)
+      *reinterpret_cast<uint2*>(p) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+    else
+      for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = (uint16_t)bf16_bits(v[e]);
+    return;
+  }
+  float* p = static_cast<float*>(g.C) + at;
+  if (whole && g.vec) {
+    f32x4* q = reinterpret_cast<f32x4*>(p);
+    *q = g.mode == kOutAcc ? *q + v : v;
+  } else {
+    for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = g.mode == kOutAcc ? p[e] + v[e] : v[e];
+  }
+}
+
+// The product on tiles of (WR FA 16) x (WC FB 16): WR x WC waves, each with
+// FA x FB accumulator tiles.  The operands' blocks of a k step are copied as
+// they lie into one of kStages LDS stages by the buffer unit; the fragments
+// come out of LDS with one conflict-free 16-byte read per lane.  Per step i:
+// wait until step i + 1's copies have landed, barrier, start the copies of
+// step i + kStages into the stage that step i has left, read step i + 1's
+// fragments into the other register set, and run step i's MFMAs under all of
+// it.  Copies past the operand's end write zeros (raw buffer bounds), so the
+// loop's counts are the same in every step.
+template <int WR, int WC, int FA, int FB, int kStages>
+__global__ __launch_bounds__(64 * WR * WC, 1) void k_mx_gemm(MxGemm g) {
+  constexpr int kWaves = WR * WC;
+  constexpr int kPA = WR * FA / 4, kPB = WC * FB / 4;  // panels of the tile
+  constexpr int kPer = (kPA + kPB) / kWaves;           // panels copied by a wave
+  static_assert(kPer * kWaves == kPA + kPB && FA % 4 == 0 && FB % 4 == 0, "whole panels");
+  constexpr int kStage = (kPA + kPB) * kMxPanel;
+  constexpr int kVm = 5 * kPer;                        // copies of a wave and step
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = w / WC, wc = w % WC;
+  const int tiles = g.tm * g.tn;
+  const int split = blockIdx.x / tiles;
+  int ti, tj;
+  mx_tile((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
+  const int s0 = split * g.per_split;
+  const int steps = min(g.steps, s0 + g.per_split) - s0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+
+  // Panel `p` of the tile's kPA + kPB: panels past the operand's last repeat
+  // it (their rows and columns of C are not written).
+  __amdgpu_buffer_rsrc_t rs[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int p = w * kPer + i;
+    const bool isb = p >= kPA;
+    const int last = ((isb ? g.N : g.M) + kMxRows - 1) / kMxRows - 1;
+    const int panel = min(isb ? tj * kPB + p - kPA : ti * kPA + p, last);
+    const uint64_t base = reinterpret_cast<uint64_t>(isb ? g.B : g.A) +
+                          ((uint64_t)panel * g.steps + s0) * kMxPanel;
+    rs[i] = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>(uniform64(base)), (short)0,
+        __builtin_amdgcn_readfirstlane(steps * kMxPanel), (int)kRawBufferWord3);
+  }
+  uint32_t vo[5];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) vo[f] = f * 1024 + lane * 16;
+  vo[4] = 4096 + lane * 4;
+  auto issue = [&](int slot, int st) {
+    // the step goes into the vector offset, which the bounds check covers
+    const uint32_t off = (uint32_t)st * kMxPanel;
+    const uint32_t to = lds0 + (uint32_t)slot * kStage + (uint32_t)(w * kPer) * kMxPanel;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) dma16(rs[i], to + i * kMxPanel + f * 1024, vo[f] + off);
+      dma4(rs[i], to + i * kMxPanel + 4096, vo[4] + off);
+    }
+  };
+  struct Frags {
+    i32x4 a[FA], b[FB];
+    int sa[FA / 4], sb[FB / 4];
+  };
+  const char* ra = lds + wr * (FA / 4) * kMxPanel + lane * 16;
+  const char* rb = lds + (kPA + wc * (FB / 4)) * kMxPanel + lane * 16;
+  const char* qa = lds + wr * (FA / 4) * kMxPanel + 4096 + lane * 4;
+  const char* qb = lds + (kPA + wc * (FB / 4)) * kMxPanel + 4096 + lane * 4;
+  auto read = [&](Frags& r, int slot) {
+    const int o = slot * kStage;
+#pragma unroll
+    for (int p = 0; p < FB / 4; ++p) r.sb[p] = *reinterpret_cast<const int*>(qb + o + p * kMxPanel);
+#pragma unroll
+    for (int p = 0; p < FA / 4; ++p) r.sa[p] = *reinterpret_cast<const int*>(qa + o + p * kMxPanel);
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+      r.b[f] = *reinterpret_cast<const i32x4*>(rb + o + (f / 4) * kMxPanel + (f % 4) * 1024);
+#pragma unroll
+    for (int f = 0; f < FA; ++f)
+      r.a[f] = *reinterpret_cast<const i32x4*>(ra + o + (f / 4) * kMxPanel + (f % 4) * 1024);
+  };
+  f32x4 acc[FA][FB];
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // C^T tiles (B's fragment first): a lane ends with four consecutive
+  // columns of one row of C
+  auto mul = [&](const Frags& r) {
+#pragma unroll
+    for (int i = 0; i < FA; i += 4)
+#pragma unroll
+      for (int j = 0; j < FB; j += 4) {
+        auto row = [&](auto I) {
+          constexpr int ii = decltype(I)::value;
+          acc[i + ii][j] = mx_mfma<0, ii>(r.b[j], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j]);
+          acc[i + ii][j + 1] = mx_mfma<1, ii>(r.b[j + 1], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 1]);
+          acc[i + ii][j + 2] = mx_mfma<2, ii>(r.b[j + 2], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 2]);
+          acc[i + ii][j + 3] = mx_mfma<3, ii>(r.b[j + 3], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 3]);
+        };
+        row(std::integral_constant<int, 0>{});
+        row(std::integral_constant<int, 1>{});
+        row(std::integral_constant<int, 2>{});
+        row(std::integral_constant<int, 3>{});
+      }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue(s, s);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 1) * kVm));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags fr[2];
+  read(fr[0], 0);
+  int slot = 0;
+  auto step = [&](auto P, int i) {
+    constexpr int p = decltype(P)::value;
+    const int next = slot + 1 == kStages ? 0 : slot + 1;
+    // step i's fragments are in registers, step i + 1's copies have landed
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 2) * kVm));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(slot, i + kStages);
+    read(fr[1 - p], next);
+    mul(fr[p]);
+    slot = next;
+  };
+  for (int i = 0; i < steps; i += 2) {
+    step(std::integral_constant<int, 0>{}, i);
+    if (i + 1 < steps) step(std::integral_constant<int, 1>{}, i + 1);
+  }
+  // no copy may land in LDS that the next workgroup has been given
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+  float* part = g.part + (int64_t)split * g.M * g.N;
+  const int m0 = (ti * WR + wr) * FA * 16 + (lane & 15), n0 = (tj * WC + wc) * FB * 16 + (lane >> 4) * 4;
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) mx_store4(g, m0 + 16 * i, n0 + 16 * j, acc[i][j], part);
+}
+
+// C = the splits' partials, added in split order (+ bias, or to C).
+__global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
+  const int64_t n4 = (g.N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4 * g.M) return;
+  const int m = (int)(i / n4), n = (int)(i - m * n4) * 4;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.n_split; ++s) {
+    const float* p = g.part + ((int64_t)s * g.M + m) * g.N + n;
+    if ((g.N & 3) == 0) v += *reinterpret_cast<const f32x4*>(p);
+    else
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < g.N) v[e] += p[e];
+  }
+  mx_store4(g, m, n, v, nullptr);
+}
+
+// ---------------------------------------------------------------------------
+// few rows (M <= 64): a workgroup owns 16 columns of C (one fragment of B per
+// k step), its 8 waves take the k steps in turn, straight from memory into
+// the MFMA operands, and their sums are added in wave order through LDS.
+// kQuant: A is X itself (M <= 16 rows), quantized into LDS first.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8;
+constexpr int kFewUnroll = 4;
+
+struct MxFew {
+  MxGemm g;
+  const void* X;
+  int64_t ldx;
+  int64_t k;
+  uint32_t* flags;
+  bool xvec;
+};
+
+template <int FM, class T, bool kQuant>
+__global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
+  extern __shared__ __attribute__((aligned(16))) char dyn[];
+  __shared__ float sums[kFewWaves][FM][256];
+  const MxGemm& g = q.g;
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  // the four fragments of a panel (one scale line) on one XCD
+  const int nf = (g.N + 15) / 16, panels = (nf + 3) / 4;
+  const int id = blockIdx.x;
+  const int pq = panels / kXcd, rem = panels % kXcd;
+  int panel, frag;
+  {
+    const int x = id % kXcd, u = id / kXcd;
+    panel = x * pq + (x < rem ? x : rem) + u / 4;
+    frag = u % 4;
+    // XCDs below `rem` hold one panel more than the others
+    if (u / 4 >= pq + (x < rem ? 1 : 0)) return;
+  }
+  if (panel * 4 + frag >= nf) return;
+  const uint8_t* Bp = g.B + (int64_t)panel * g.steps * kMxPanel;
+  i32x4 b[kFewUnroll];
+  int sb[kFewUnroll];
+  auto load_b = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < kFewUnroll; ++u) {
+      const int st = min(s + u * kFewWaves, g.steps - 1);
+      const uint8_t* p = Bp + (int64_t)st * kMxPanel;
+      b[u] = *reinterpret_cast<const i32x4*>(p + frag * 1024 + lane * 16);
+      sb[u] = p[4096 + lane * 4 + frag];
+    }
+  };
+  load_b(w);
+  if constexpr (kQuant) {
+    const T* X = static_cast<const T*>(q.X);
+    const int nb = g.steps * 4, M = g.M;
+    uint8_t* sc = reinterpret_cast<uint8_t*>(dyn) + (int64_t)nb * M * 16;
+    uint32_t fl = 0;
+    for (int e = t; e < nb * M; e += 64 * kFewWaves) {
+      const int m = e / nb, kb = e - m * nb;
+      const int64_t k0 = (int64_t)kb * 32;
+      const T* src = X + m * q.ldx + k0;
+      float v[32];
+      if (q.xvec && k0 + 32 <= q.k) {
+        constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < 32 / kPer; ++j) {
+          const uint4 c = reinterpret_cast<const uint4*>(src)[j];
+          if constexpr (sizeof(T) == 2) {
+            unpack2(c.x, v[8 * j], v[8 * j + 1]);
+            unpack2(c.y, v[8 * j + 2], v[8 * j + 3]);
+            unpack2(c.z, v[8 * j + 4], v[8 * j + 5]);
+            unpack2(c.w, v[8 * j + 6], v[8 * j + 7]);
+          } else {
+            v[4 * j] = __uint_as_float(c.x);
+            v[4 * j + 1] = __uint_as_float(c.y);
+            v[4 * j + 2] = __uint_as_float(c.z);
+            v[4 * j + 3] = __uint_as_float(c.w);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = k0 + j < q.k ? ld1(src + j) : 0.f;
+      }
+      uint32_t code, bf = 0;
+      const uint4 c = mx_block(v, code, bf);
+      if (k0 < q.k) fl |= bf;
+      *reinterpret_cast<uint4*>(dyn + ((int64_t)kb * M + m) * 16) = c;
+      sc[kb * M + m] = (uint8_t)code;
+    }
+    if (q.flags && fl && id == 0) atomicOr(q.flags, fl);
+    __syncthreads();
+  }
+  f32x4 acc[FM];
+#pragma unroll
+  for (int f = 0; f < FM; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s = w; s < g.steps; s += kFewWaves * kFewUnroll) {
+    if (s != w) load_b(s);
+    i32x4 a[kFewUnroll][FM];
+    int sa[kFewUnroll];
+#pragma unroll
+    for (int u = 0; u < kFewUnroll; ++u) {
+      const int st = min(s + u * kFewWaves, g.steps - 1);
+      if constexpr (kQuant) {
+        const int r = lane & 15, at = (st * 4 + (lane >> 4)) * g.M + (r < g.M ? r : 0);
+        a[u][0] = *reinterpret_cast<const i32x4*>(dyn + at * 16);
+        sa[u] = reinterpret_cast<const uint8_t*>(dyn)[(int64_t)g.steps * 4 * g.M * 16 + at];
+      } else {
+        const uint8_t* p = g.A + (int64_t)st * kMxPanel;
+#pragma unroll
+        for (int f = 0; f < FM; ++f) a[u][f] = *reinterpret_cast<const i32x4*>(p + f * 1024 + lane * 16);
+        sa[u] = *reinterpret_cast<const int*>(p + 4096 + lane * 4);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFewUnroll; ++u) {
+      if (s + u * kFewWaves >= g.steps) break;  // wave-uniform
+      acc[0] = mx_mfma<0, 0>(b[u], sb[u], a[u][0], sa[u], acc[0]);
+      if constexpr (FM > 1) acc[1] = mx_mfma<0, 1>(b[u], sb[u], a[u][1], sa[u], acc[1]);
+      if constexpr (FM > 2) acc[2] = mx_mfma<0, 2>(b[u], sb[u], a[u][2], sa[u], acc[2]);
+      if constexpr (FM > 3) acc[3] = mx_mfma<0, 3>(b[u], sb[u], a[u][3], sa[u], acc[3]);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < FM; ++f) *reinterpret_cast<f32x4*>(&sums[w][f][lane * 4]) = acc[f];
+  __syncthreads();
+  for (int e = t; e < FM * 64; e += 64 * kFewWaves) {
+    const int f = e >> 6, l = e & 63;
+    f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][f][l * 4]);
+#pragma unroll
+    for (int u = 1; u < kFewWaves; ++u) v += *reinterpret_cast<const f32x4*>(&sums[u][f][l * 4]);
+    mx_store4(g, f * 16 + (l & 15), (panel * 4 + frag) * 16 + (l >> 4) * 4, v, nullptr);
+  }
+}
+
+hipError_t done() { return hipGetLastError(); }
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                              uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s) {
+  const int ct = (int)((cols + kQTile - 1) / kQTile);
+  const int64_t tiles = (rows + kQTile - 1) / kQTile * ct;
+  const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
+  const bool vec = ((uintptr_t)X & 15) == 0 && ld * es % 16 == 0;
+  auto go = [&](auto zero) {
+    using T = decltype(zero);
+    auto run = [&](auto kernel) {
+      kernel<<<dim3((uint32_t)tiles), dim3(kQThreads), 0, s>>>(static_cast<const T*>(X), rows, cols, ld,
+                                                               by_row, by_col, ct, vec, flags);
+    };
+    if (by_row && by_col) run(k_mx_quant<T, true, true>);
+    else if (by_row) run(k_mx_quant<T, true, false>);
+    else run(k_mx_quant<T, false, true>);
+  };
+  if (dtype == GIFT_DTYPE_BF16) go((__bf16)0.f);
+  else go(0.f);
+  return done();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void* out, int dtype,
+                                int64_t ld, hipStream_t s) {
+  const int steps = (int)((k + kMxStep - 1) / kMxStep);
+  const int64_t blocks = (rows + kMxRows - 1) / kMxRows * steps;
+  const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
+  const bool vec = ((uintptr_t)out & 15) == 0 && ld * es % 16 == 0;
+  if (dtype == GIFT_DTYPE_BF16)
+    k_mx_dequant<__bf16><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<__bf16*>(out), ld, vec);
+  else
+    k_mx_dequant<float><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<float*>(out), ld, vec);
+  return done();
+}
+
+// How a product is cut: rows and columns per tile and the number of k splits.
+MxPlan mx_plan(int64_t M, int64_t N, int64_t k) {
+  const int64_t steps = (k + kMxStep - 1) / kMxStep;
+  MxPlan p{};
+  if (M <= kMxFewRows) {
+    p.tile = 0;
+    p.n_split = 1;
+    p.per_split = (int)steps;
+    return p;
+  }
+  auto tiles = [&](int t) { return (M + t - 1) / t * ((N + t - 1) / t); };
+  p.tile = tiles(256) >= 192 ? 256 : 128;
+  const int64_t slots = p.tile == 256 ? 256 : 512;
+  int64_t want = slots / tiles(p.tile);
+  if (want > steps / 8) want = steps / 8;
+  if (want < 1) want = 1;
+  if (want > 16) want = 16;
+  p.per_split = (int)((steps + want - 1) / want);
+  p.n_split = (int)((steps + p.per_split - 1) / p.per_split);
+  return p;
+}
+
+size_t mx_matmul_ws(int64_t M, int64_t N, int64_t k) {
+  const MxPlan p = mx_plan(M, N, k);
+  return p.n_split > 1 ? (size_t)p.n_split * M * N * sizeof(float) : 0;
+}
+
+namespace {
+MxGemm gemm_args(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t k, const float* bias,
+                 void* C, int dtype, int64_t ldc, bool accumulate) {
+  MxGemm g{};
+  g.A = A;
+  g.B = B;
+  g.C = C;
+  g.bias = bias;
+  g.ldc = ldc;
+  g.M = (int)M;
+  g.N = (int)N;
+  g.steps = (int)((k + kMxStep - 1) / kMxStep);
+  g.mode = dtype == GIFT_DTYPE_BF16 ? kOutBf16 : accumulate ? kOutAcc : kOutF32;
+  const size_t bytes = dtype == GIFT_DTYPE_BF16 ? 8 : 16;
+  g.vec = ldc % 4 == 0 && (uintptr_t)C % bytes == 0;
+  return g;
+}
+
+uint32_t few_blocks(const MxGemm& g) {
+  // every XCD gets the grid of the one with the most panels
+  const int panels = (g.N + kMxRows - 1) / kMxRows;
+  return (uint32_t)((panels + kXcd - 1) / kXcd * kXcd * 4);
+}
+}  // namespace
+
+hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t k,
+                            const float* bias, void* C, int dtype, int64_t ldc, bool accumulate,
+                            void* ws, hipStream_t s) {
+  const MxPlan p = mx_plan(M, N, k);
+  MxGemm g = gemm_args(A, B, M, N, k, bias, C, dtype, ldc, accumulate);
+  if (p.tile == 0) {
+    MxFew q{};
+    q.g = g;
+    const dim3 grid(few_blocks(g)), block(64 * kFewWaves);
+    if (M <= 16) k_mx_few<1, float, false><<<grid, block, 0, s>>>(q);
+    else if (M <= 32) k_mx_few<2, float, false><<<grid, block, 0, s>>>(q);
+    else if (M <= 48) k_mx_few<3, float, false><<<grid, block, 0, s>>>(q);
+    else k_mx_few<4, float, false><<<grid, block, 0, s>>>(q);
+    return done();
+  }
+  g.tm = (int)((M + p.tile - 1) / p.tile);
+  g.tn = (int)((N + p.tile - 1) / p.tile);
+  g.per_split = p.per_split;
+  g.n_split = p.n_split;
+  MxGemm h = g;
+  if (p.n_split > 1) {
+    h.part = g.part = static_cast<float*>(ws);
+    h.mode = kOutPart;
+  }
+  const dim3 grid((uint32_t)((int64_t)g.tm * g.tn * p.n_split));
+  if (p.tile == 256) k_mx_gemm<2, 2, 8, 8, 4><<<grid, dim3(256), 0, s>>>(h);
+  else k_mx_gemm<2, 2, 4, 4, 4><<<grid, dim3(256), 0, s>>>(h);
+  hipError_t e = done();
+  if (e != hipSuccess || p.n_split == 1) return e;
+  k_mx_reduce<<<dim3((uint32_t)((M * ((N + 3) / 4) + 255) / 256)), dim3(256), 0, s>>>(g);
+  return done();
+}
+
+// Bytes of LDS that the rows' operand takes in the one-launch form.
+static size_t few_lds(int64_t M, int64_t k) {
+  return (size_t)((k + kMxStep - 1) / kMxStep * 4 * M * 17);
+}
+
+bool mx_linear_one_launch(int64_t M, int64_t k) { return M <= 16 && few_lds(M, k) <= kMxFewLds; }
+
+hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t ldx, const uint8_t* W,
+                                int64_t N, int64_t k, const float* bias, void* Y, int dtype, int64_t ldy,
+                                uint32_t* flags, hipStream_t s) {
+  MxFew q{};
+  q.g = gemm_args(nullptr, W, M, N, k, bias, Y, dtype, ldy, false);
+  q.X = X;
+  q.ldx = ldx;
+  q.k = k;
+  q.flags = flags;
+  const size_t es = x_dtype == GIFT_DTYPE_BF16 ? 2 : 4;
+  q.xvec = ((uintptr_t)X & 15) == 0 && ldx * es % 16 == 0;
+  const dim3 grid(few_blocks(q.g)), block(64 * kFewWaves);
+  const size_t lds = few_lds(M, k);
+  if (x_dtype == GIFT_DTYPE_BF16) k_mx_few<1, __bf16, true><<<grid, block, lds, s>>>(q);
+  else k_mx_few<1, float, true><<<grid, block, lds, s>>>(q);
+  return done();
+}
+
+}  // namespace gift

@@ -1,0 +1,49 @@
+// Launchers of mx.hip (MXFP4 operands and products) and norm.hip (layer and
+// RMS norm) for the entry points in api_layer.cpp.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/gift.h"
+
+namespace gift {
+
+constexpr int kMxRows = 64;                      // rows of an operand panel
+constexpr int kMxStep = 128;                     // k elements of a step
+constexpr int kMxPanel = GIFT_MX_PANEL_BYTES;    // bytes of a panel's step
+constexpr int kMxFewRows = 64;                   // products of at most this many rows: k_mx_few
+constexpr size_t kMxFewLds = 96 << 10;           // LDS for the rows quantized in front of a product
+
+struct MxPlan {
+  int tile;       // rows and columns of a tile, 0: k_mx_few
+  int n_split;    // k splits
+  int per_split;  // k steps of a split
+};
+MxPlan mx_plan(int64_t M, int64_t N, int64_t k);
+size_t mx_matmul_ws(int64_t M, int64_t N, int64_t k);
+bool mx_linear_one_launch(int64_t M, int64_t k);
+
+hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                              uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void* out, int dtype,
+                                int64_t ld, hipStream_t s);
+hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t k,
+                            const float* bias, void* C, int dtype, int64_t ldc, bool accumulate,
+                            void* ws, hipStream_t s);
+hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t ldx, const uint8_t* W,
+                                int64_t N, int64_t k, const float* bias, void* Y, int dtype,
+                                int64_t ldy, uint32_t* flags, hipStream_t s);
+
+// norm.hip
+hipError_t launch_norm_forward(const void* X, int dtype, int64_t rows, int64_t d, int kind,
+                               const float* weight, const float* bias, float eps, void* Y,
+                               float* mean, float* rstd, hipStream_t s);
+size_t norm_backward_ws(int64_t rows, int64_t d);
+hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_t rows, int64_t d,
+                                int kind, const float* weight, const float* mean, const float* rstd,
+                                void* dX, float* dweight, float* dbias, bool accumulate, void* ws,
+                                hipStream_t s);
+
+}  // namespace gift

@@ -384,6 +384,124 @@ enum { GIFT_OP_WHITEN_QUANTIZE = 0, GIFT_OP_DEQUANT_UNWHITEN = 1,
 size_t gift_group_workspace_bytes(int op, const gift_layer *layers,
                                   int n_layers, int scaling);
 
+/* ------------------------------------------------------------------------
+ * A layer's training step in MXFP4, and the norm in front of it: the
+ * operators that produce what the round trip works on.  The norm writes the
+ * layer input X (what gift_refresh_factor reads), the products form
+ * Y = X W^T, dX = dY W and the weight gradient G = dY^T X (what
+ * gift_whiten_quantize takes), each operand quantized to MXFP4 along the
+ * axis its product sums over, with the scale and rounding rules of
+ * GIFT_SCALE_MXFP4 above.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * gift_mx -- an MXFP4 operand: a rows x k matrix quantized in blocks of 32
+ * along k, stored in the order the matrix cores read it.  Row panels of 64
+ * rows and k steps of 128: the block of panel p and step s starts at byte
+ * (p * ceil(k/128) + s) * GIFT_MX_PANEL_BYTES and holds 4 x 1024 bytes of
+ * codes, then 256 bytes of scales.
+ *   codes:  row r of the panel, k element e of the step: byte
+ *           1024 (r/16) + 16 (16 (e/32) + r%16) + (e%32)/2, the even element
+ *           in the low nibble;
+ *   scales: the E8M0 byte of row r, 32-block b of the step: byte
+ *           4096 + 4 (16 b + r%16) + r/16.
+ * Rows and k elements past the matrix hold code 0 with scale 127 (2^0).
+ * data: gift_mx_bytes(rows, k) bytes, 16-byte aligned.
+ */
+#define GIFT_MX_PANEL_BYTES 4352
+typedef struct gift_mx {
+    int64_t rows;     /* 1 <= rows <= 2^24                                    */
+    int64_t k;        /* 1 <= k <= 2^24                                       */
+    void *data;       /* device                                               */
+} gift_mx;
+
+/* Bytes of gift_mx.data; 0 for sizes outside the range above (or a matrix
+ * of more than 2^36 padded elements). */
+size_t gift_mx_bytes(int64_t rows, int64_t k);
+
+/*
+ * gift_mx_quantize -- quantize X (rows x cols, x_dtype, element (i, j) at
+ * i * ld + j, ld >= cols) in one read: along its rows into *by_row
+ * (rows x cols) and/or along its columns into *by_col (cols x rows, the
+ * operand of X^T).  Either may be NULL, not both.  X needs only its element
+ * alignment; rows that start 16-byte aligned are read faster.  Per block of
+ * 32 as in GIFT_SCALE_MXFP4: the result is what gift_euclid_fp8_roundtrip
+ * gives for the same values; a block cut short by the matrix's edge is
+ * quantized as if filled with zeros.  dev_flags (optional, 4-byte aligned):
+ * NONFINITE where a block's amax is NaN or infinite, ZERO_AMAX where a block
+ * is all zero.
+ */
+gift_status gift_mx_quantize(const void *X, int x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                             const gift_mx *by_row, const gift_mx *by_col,
+                             uint32_t *dev_flags, void *stream);
+
+/*
+ * gift_mx_dequantize -- out (rows x k, out_dtype, element (i, j) at
+ * i * ld + j) = the values the operand stands for, exactly (a bf16 holds
+ * every E2M1 value times its scale; a NaN scale gives NaN).
+ */
+gift_status gift_mx_dequantize(const gift_mx *a, void *out, int out_dtype, int64_t ld,
+                               void *stream);
+
+/*
+ * gift_mx_matmul -- C = A B^T (+ bias): C[i, j] = sum_k A[i, k] B[j, k] in
+ * fp32 over the operands' exact values, A of M rows, B of N rows, equal k.
+ * C: M x N, c_dtype, element (i, j) at i * ldc + j, ldc >= N, element
+ * aligned.  bias: N fp32 or NULL.  accumulate != 0 (fp32 C, no bias): C +=
+ * the product (gradients summed over micro-batches).  A bf16 C is rounded
+ * once, to nearest even, from the fp32 sum.  The order of the sum depends
+ * on (M, N, k) alone: equal calls give equal bits.
+ */
+gift_status gift_mx_matmul(const gift_mx *A, const gift_mx *B, const float *bias, void *C,
+                           int c_dtype, int64_t ldc, int accumulate, void *ws, size_t ws_bytes,
+                           void *stream);
+size_t gift_mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t k);
+
+/*
+ * gift_mx_linear -- Y = Q(X) W^T (+ bias), X (rows x W->k, x_dtype, leading
+ * dimension ldx) quantized along its rows inside the call: the serving form.
+ * Few rows (a token, a small batch) take one launch, which quantizes X in
+ * front of the product; the result is that of gift_mx_quantize and
+ * gift_mx_matmul to the rounding of the fp32 sums.  dev_flags as in
+ * gift_mx_quantize.
+ */
+gift_status gift_mx_linear(const void *X, int x_dtype, int64_t rows, int64_t ldx,
+                           const gift_mx *W, const float *bias, void *Y, int y_dtype,
+                           int64_t ldy, uint32_t *dev_flags, void *ws, size_t ws_bytes,
+                           void *stream);
+size_t gift_mx_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k);
+
+/*
+ * Layer norm and RMS norm of every row of X (rows x d, x_dtype, dense):
+ *   LAYER: mu = mean(x), r = (mean((x - mu)^2) + eps)^-1/2, h = (x - mu) r
+ *   RMS:   r = (mean(x^2) + eps)^-1/2,                      h = x r
+ *   y = h * weight + bias
+ * weight, bias: d fp32 (NULL: 1 and 0).  Y has X's type; mean (LAYER) and
+ * rstd, fp32, one per row, may be NULL.  Statistics are fp32, the variance
+ * in a second pass over the centred values.  X and Y may be the same
+ * buffer.  X, Y, dY and dX need their element alignment only.
+ */
+enum { GIFT_NORM_LAYER = 0, GIFT_NORM_RMS = 1 };
+gift_status gift_norm_forward(const void *X, int x_dtype, int64_t rows, int64_t d, int kind,
+                              const float *weight, const float *bias, float eps, void *Y,
+                              float *mean, float *rstd, void *stream);
+
+/*
+ * gift_norm_backward -- gradients for the statistics of the forward pass:
+ *   g = dY * weight
+ *   dX = r (g - mean(g) - h mean(g h))      (RMS: without mean(g))
+ *   dweight = sum over rows of dY h,  dbias = sum over rows of dY
+ * dX (X's type), dweight and dbias (d fp32) may each be NULL, not all;
+ * mean is required for LAYER.  dX and dY may be the same buffer.
+ * accumulate != 0: dweight and dbias are added to.  The rows are summed in
+ * an order that depends on (rows, d) and alignment alone.
+ */
+gift_status gift_norm_backward(const void *dY, const void *X, int x_dtype, int64_t rows,
+                               int64_t d, int kind, const float *weight, const float *mean,
+                               const float *rstd, void *dX, float *dweight, float *dbias,
+                               int accumulate, void *ws, size_t ws_bytes, void *stream);
+size_t gift_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+
 const char *gift_status_string(int status);
 /* Thread-local detail of the last failing call on this thread. */
 const char *gift_last_error(void);
