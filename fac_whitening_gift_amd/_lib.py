@@ -585,13 +585,17 @@ def _matrix(t, name, device=None, shape=None, dtype=None):
         raise ValueError("%s must be a device tensor" % name)
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape),
+    have = t.shape
+    if len(have) != 2 or (shape is not None and have != shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(have),
                                                            shape or "rows x columns"))
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
-        raise ValueError("%s must have contiguous rows" % name)
+    rows, cols = have
+    if t.is_contiguous():
+        ld = cols
+    else:
+        ld, step = t.stride()
+        if (cols > 1 and step != 1) or ld < cols:
+            raise ValueError("%s must have contiguous rows" % name)
     return t.data_ptr(), code, rows, cols, ld
 
 
@@ -599,8 +603,7 @@ def _vector(t, n, name, device):
     """-> pointer of an optional contiguous fp32 device vector of n elements."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != (n,) \
-            or (n > 1 and t.stride(0) != 1):
+    if t.dtype != torch.float32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be %d contiguous fp32 elements on %s" % (name, n, device))
     return t.data_ptr()
 
@@ -613,17 +616,14 @@ def _flags_ptr(flags, device):
     return flags.data_ptr()
 
 
-def _out(out, shape, dtype, device):
-    return out if out is not None else torch.empty(shape, dtype=dtype, device=device)
-
-
 def _scratch(nbytes, device, ws):
     """-> (workspace tensor, its pointer, its bytes); nothing for 0 bytes."""
     if ws is None:
         if nbytes == 0:
             return None, None, 0
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        return ws, ws.data_ptr(), nbytes
+    if ws.device != device or not ws.is_contiguous():
         raise ValueError("workspace must be contiguous, on %s" % device)
     have = ws.numel() * ws.element_size()
     if have < nbytes:
@@ -648,11 +648,12 @@ def _enqueue(device, stream, fn, *args):
     device appended."""
     if stream is not None and stream.device != device:
         raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != GIFT_OK:
         _check(status)
 
@@ -663,25 +664,20 @@ class MxOperand:
     gift_mx_bytes(rows, k), allocated when not given; gift_mx_quantize fills
     it.  shape is (rows, k)."""
 
+    __slots__ = ("rows", "k", "shape", "data", "device", "_struct", "_ref")
+
     def __init__(self, rows, k, device="cuda", data=None):
-        self.rows, self.k = int(rows), int(k)
-        nbytes = int(load().gift_mx_bytes(self.rows, self.k))
+        self.rows, self.k = self.shape = (int(rows), int(k))
+        nbytes = load().gift_mx_bytes(rows, k)
         if nbytes == 0:
             raise ValueError("MXFP4 operand of %d x %d is out of range" % (self.rows, self.k))
         if data is None:
             data = torch.empty(nbytes, dtype=torch.uint8, device=device)
         _dev(data, torch.uint8, (nbytes,), "data")
         self.data = data
-        self._struct = _Mx(self.rows, self.k, data.data_ptr())
+        self.device = data.device
+        self._struct = _Mx(rows, k, data.data_ptr())
         self._ref = ctypes.byref(self._struct)
-
-    @property
-    def shape(self):
-        return (self.rows, self.k)
-
-    @property
-    def device(self):
-        return self.data.device
 
 
 def _operand(op, name, device=None):
@@ -725,7 +721,8 @@ def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
 def gift_mx_dequantize(a, dtype=torch.float32, out=None, stream=None):
     """-> rows x k tensor of the values the operand stands for."""
     ref = _operand(a, "a")
-    out = _out(out, a.shape, dtype, a.device)
+    if out is None:
+        out = torch.empty(a.shape, dtype=dtype, device=a.device)
     ptr, dt, _, _, ld = _matrix(out, "out", a.device, a.shape)
     _enqueue(a.device, stream, load().gift_mx_dequantize, ref, ptr, dt, ld)
     return out
@@ -744,7 +741,8 @@ def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=F
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     dev, shape = a.device, (a.rows, b.rows)
-    out = _out(out, shape, dtype, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
     ptr, dt, _, _, ld = _matrix(out, "out", dev, shape)
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_matmul_workspace_bytes(a.rows, b.rows, a.k), dev, ws)
@@ -767,7 +765,8 @@ def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, s
     if x.shape[1] != w.k:
         raise ValueError("x has %d columns, w sums over %d" % (x.shape[1], w.k))
     shape = (rows, w.rows)
-    out = _out(out, shape, dtype or x.dtype, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or x.dtype, device=dev)
     yp, ydt, _, _, ldy = _matrix(out, "out", dev, shape)
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_linear_workspace_bytes(rows, w.rows, w.k), dev, ws)
@@ -783,6 +782,10 @@ def _dense(t, name, device=None, shape=None, dtype=None):
     return ptr, dt, rows, cols
 
 
+def _f32(n, device):
+    return torch.empty(n, dtype=torch.float32, device=device)
+
+
 @_on_stream
 def gift_norm_forward(x, weight=None, bias=None, eps=1e-5, kind=NORM_LAYER, out=None, mean=None,
                       rstd=None, stream=None):
@@ -790,13 +793,18 @@ def gift_norm_forward(x, weight=None, bias=None, eps=1e-5, kind=NORM_LAYER, out=
     or None.  -> (y, mean (None for NORM_RMS), rstd)."""
     dev = x.device
     ptr, dt, rows, d = _dense(x, "x")
-    out = _out(out, (rows, d), x.dtype, dev)
-    yp = _dense(out, "out", dev, (rows, d), x.dtype)[0]
-    if kind == NORM_LAYER:
-        mean = _out(mean, (rows,), torch.float32, dev)
-    elif mean is not None:
-        raise ValueError("NORM_RMS has no mean")
-    rstd = _out(rstd, (rows,), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(x)
+        yp = out.data_ptr()
+    else:
+        yp = _dense(out, "out", dev, (rows, d), x.dtype)[0]
+    if kind != NORM_LAYER:
+        if mean is not None:
+            raise ValueError("NORM_RMS has no mean")
+    elif mean is None:
+        mean = _f32(rows, dev)
+    if rstd is None:
+        rstd = _f32(rows, dev)
     _enqueue(dev, stream, load().gift_norm_forward, ptr, dt, rows, d, kind,
              _vector(weight, d, "weight", dev), _vector(bias, d, "bias", dev), eps, yp,
              _vector(mean, rows, "mean", dev), _vector(rstd, rows, "rstd", dev))
@@ -821,9 +829,12 @@ def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dwei
         dbias = False
     if accumulate and (dweight is None or dbias is None):
         raise ValueError("accumulate adds to given gradients")
-    dx = None if dx is False else _out(dx, (rows, d), x.dtype, dev)
-    dweight = None if dweight is False else _out(dweight, (d,), torch.float32, dev)
-    dbias = None if dbias is False else _out(dbias, (d,), torch.float32, dev)
+    if dx is None:
+        dx = torch.empty_like(x)
+    elif dx is False:
+        dx = None
+    dweight = _f32(d, dev) if dweight is None else None if dweight is False else dweight
+    dbias = _f32(d, dev) if dbias is None else None if dbias is False else dbias
     xp = None if dx is None else _dense(dx, "dx", dev, (rows, d), x.dtype)[0]
     lib = load()
     need = lib.gift_norm_backward_workspace_bytes(rows, d) \

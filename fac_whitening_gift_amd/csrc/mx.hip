@@ -9,6 +9,7 @@
 // the instruction picks by its byte select, so neither codes nor scales need
 // any rearranging between memory and the matrix cores.
 #include <type_traits>
+#include <utility>
 
 #include "device.hpp"
 #include "mx.hpp"
@@ -82,24 +83,37 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
   const int t = threadIdx.x;
   const int tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
   const int64_t r0 = (int64_t)tr * kQTile, c0 = (int64_t)tc * kQTile;
-  if (vec && r0 + kQTile <= rows && c0 + kQTile <= cols) {
+  // Loads go out together, from addresses clamped into X; what lies outside
+  // becomes zero.
+  if (vec) {  // every 16-byte chunk lies inside X or outside
     uint4 v[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int e = t + i * kQThreads, r = e / kChunks, c = e % kChunks;
-      v[i] = *reinterpret_cast<const uint4*>(X + (r0 + r) * ld + c0 + c * kPer);
+      const int e = t + i * kQThreads;
+      const int64_t r = min(r0 + e / kChunks, rows - 1), c = min(c0 + e % kChunks * kPer, cols - kPer);
+      v[i] = *reinterpret_cast<const uint4*>(X + r * ld + c);
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int e = t + i * kQThreads, r = e / kChunks, c = e % kChunks;
+      if (r0 + r >= rows || c0 + c * kPer >= cols) v[i] = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(lds + r * kStride + c * 16) = v[i];
     }
   } else {
-    for (int e = t; e < kQTile * kQTile; e += kQThreads) {
-      const int r = e / kQTile, c = e % kQTile;
-      T x = (T)0.f;
-      if (r0 + r < rows && c0 + c < cols) x = X[(r0 + r) * ld + c0 + c];
-      *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = x;
+    constexpr int kAtOnce = 16;
+    for (int e0 = t; e0 < kQTile * kQTile; e0 += kAtOnce * kQThreads) {
+      T v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int e = e0 + i * kQThreads;
+        v[i] = X[min(r0 + e / kQTile, rows - 1) * ld + min(c0 + e % kQTile, cols - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int e = e0 + i * kQThreads, r = e / kQTile, c = e % kQTile;
+        if (r0 + r >= rows || c0 + c >= cols) v[i] = (T)0.f;
+        *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = v[i];
+      }
     }
   }
   __syncthreads();
@@ -258,7 +272,9 @@ struct MxGemm {
   int mode;        // kOut*
   bool vec;        // C takes 4-element stores
 };
-enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2, kOutPart = 3 };
+enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
+// workgroups of a launch: one (256 x 256 tiles) or two per CU
+constexpr int kMxSlots256 = 256, kMxSlots128 = 512;
 
 // Tile of a workgroup: workgroups go to the XCDs in turn, so XCD x takes the
 // x-th contiguous run of the tiles in an order that walks bands of 4 tile
@@ -280,15 +296,9 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
 }
 
 // Four consecutive columns n .. n + 3 of row m.
-__device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v, float* part) {
+__device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v) {
   if (m >= g.M || n >= g.N) return;
   const bool whole = n + 4 <= g.N;
-  if (g.mode == kOutPart) {
-    float* p = part + (int64_t)m * g.N + n;
-    if (whole && (g.N & 3) == 0) *reinterpret_cast<f32x4*>(p) = v;
-    else for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = v[e];
-    return;
-  }
   if (g.bias)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -312,143 +322,260 @@ __device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v
   }
 }
 
+template <class F, int... I>
+__device__ __forceinline__ void static_for_seq(F& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0), ..., f(N - 1) with the index as a constant
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for_seq(f, std::make_integer_sequence<int, N>{});
+}
+
 // The product on tiles of (WR FA 16) x (WC FB 16): WR x WC waves, each with
-// FA x FB accumulator tiles.  The operands' blocks of a k step are copied as
-// they lie into one of kStages LDS stages by the buffer unit; the fragments
-// come out of LDS with one conflict-free 16-byte read per lane.  Per step i:
-// wait until step i + 1's copies have landed, barrier, start the copies of
-// step i + kStages into the stage that step i has left, read step i + 1's
-// fragments into the other register set, and run step i's MFMAs under all of
-// it.  Copies past the operand's end write zeros (raw buffer bounds), so the
-// loop's counts are the same in every step.
-template <int WR, int WC, int FA, int FB, int kStages>
-__global__ __launch_bounds__(64 * WR * WC, 1) void k_mx_gemm(MxGemm g) {
-  constexpr int kWaves = WR * WC;
+// FA x FB accumulator tiles.  A workgroup takes the work items (a tile and a
+// range of k steps) blockIdx.x, blockIdx.x + gridDim.x, ... as one stream of
+// k steps.  The operands' blocks of a step are copied as they lie into one
+// of kStages LDS stages by the buffer unit; the fragments come out of LDS
+// with one conflict-free 16-byte read per lane.  Per step i: wait until step
+// i + 1's copies have landed, barrier, then run step i's MFMAs with, spread
+// between them, the copies of step i + kStages into the stage that step i has
+// left and the reads of step i + 1's fragments into the other register set.
+// The copies run ahead across items, so a tile's results leave (through a
+// wave's own corner of LDS, as whole row segments) while the next tile's
+// operands arrive.  Copies past an item's end write zeros (raw buffer
+// bounds): items are rounded up to an even number of steps, at least
+// kStages.  The loops hold no branch around a step: the compiler would sink
+// the MFMAs below it, away from the copies and reads they are spread among.
+template <int WR, int WC, int FA, int FB, int kOut, bool kBias>
+__global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(MxGemm g) {
+  constexpr int kWaves = WR * WC, kStages = 4;
   constexpr int kPA = WR * FA / 4, kPB = WC * FB / 4;  // panels of the tile
   constexpr int kPer = (kPA + kPB) / kWaves;           // panels copied by a wave
   static_assert(kPer * kWaves == kPA + kPB && FA % 4 == 0 && FB % 4 == 0, "whole panels");
   constexpr int kStage = (kPA + kPB) * kMxPanel;
   constexpr int kVm = 5 * kPer;                        // copies of a wave and step
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  constexpr int kRowData = FB * 32 > 256 ? 256 : FB * 32;  // bytes of a staged row of C
+  constexpr int kRow = kRowData + 16;  // 4 banks past a power of two: 16 rows of one column, no conflict
+  constexpr int kOutLds = 16 * kRow;
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage + kWaves * kOutLds];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = w / WC, wc = w % WC;
-  const int tiles = g.tm * g.tn;
-  const int split = blockIdx.x / tiles;
-  int ti, tj;
-  mx_tile((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
-  const int s0 = split * g.per_split;
-  const int steps = min(g.steps, s0 + g.per_split) - s0;
+  const int tiles = g.tm * g.tn, items = tiles * g.n_split;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  // Panel `p` of the tile's kPA + kPB: panels past the operand's last repeat
-  // it (their rows and columns of C are not written).
-  __amdgpu_buffer_rsrc_t rs[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int p = w * kPer + i;
-    const bool isb = p >= kPA;
-    const int last = ((isb ? g.N : g.M) + kMxRows - 1) / kMxRows - 1;
-    const int panel = min(isb ? tj * kPB + p - kPA : ti * kPA + p, last);
-    const uint64_t base = reinterpret_cast<uint64_t>(isb ? g.B : g.A) +
-                          ((uint64_t)panel * g.steps + s0) * kMxPanel;
-    rs[i] = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<void*>(uniform64(base)), (short)0,
-        __builtin_amdgcn_readfirstlane(steps * kMxPanel), (int)kRawBufferWord3);
-  }
   uint32_t vo[5];
 #pragma unroll
   for (int f = 0; f < 4; ++f) vo[f] = f * 1024 + lane * 16;
   vo[4] = 4096 + lane * 4;
-  auto issue = [&](int slot, int st) {
-    // the step goes into the vector offset, which the bounds check covers
-    const uint32_t off = (uint32_t)st * kMxPanel;
-    const uint32_t to = lds0 + (uint32_t)slot * kStage + (uint32_t)(w * kPer) * kMxPanel;
+
+  // The copies' position in the stream.  Panels past an operand's last
+  // repeat it (their rows and columns of C are not written).
+  int c_step = 0, c_slot = 0;
+  __amdgpu_buffer_rsrc_t rs[kPer];
+  auto seek = [&](int it) {
+    const bool any = it < items;
+    if (!any) it = 0;
+    const int split = it / tiles;
+    int ti, tj;
+    mx_tile(it - split * tiles, g.tm, g.tn, ti, tj);
+    const int s0 = split * g.per_split;
+    const int n = any ? min(g.steps, s0 + g.per_split) - s0 : 0;
+    c_step = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-#pragma unroll
-      for (int f = 0; f < 4; ++f) dma16(rs[i], to + i * kMxPanel + f * 1024, vo[f] + off);
-      dma4(rs[i], to + i * kMxPanel + 4096, vo[4] + off);
+      const int p = w * kPer + i;
+      const bool isb = p >= kPA;
+      const int last = ((isb ? g.N : g.M) + kMxRows - 1) / kMxRows - 1;
+      const int panel = min(isb ? tj * kPB + p - kPA : ti * kPA + p, last);
+      const uint64_t base = reinterpret_cast<uint64_t>(isb ? g.B : g.A) +
+                            ((uint64_t)panel * g.steps + s0) * kMxPanel;
+      rs[i] = __builtin_amdgcn_make_buffer_rsrc(
+          reinterpret_cast<void*>(uniform64(base)), (short)0,
+          __builtin_amdgcn_readfirstlane(n * kMxPanel), (int)kRawBufferWord3);
     }
   };
+  // copy `d` of the wave's kVm of a step
+  auto copy = [&](auto D) {
+    constexpr int d = decltype(D)::value, i = d / 5, f = d % 5;
+    const uint32_t to = lds0 + (uint32_t)c_slot * kStage + (uint32_t)(w * kPer + i) * kMxPanel;
+    // the step goes into the vector offset, which the bounds check covers
+    const uint32_t off = (uint32_t)c_step * kMxPanel;
+    if constexpr (f < 4) dma16(rs[i], to + f * 1024, vo[f] + off);
+    else dma4(rs[i], to + 4096, vo[4] + off);
+  };
+  auto copied = [&] {
+    c_slot = (c_slot + 1) % kStages;
+    ++c_step;
+  };
+
   struct Frags {
-    i32x4 a[FA], b[FB];
-    int sa[FA / 4], sb[FB / 4];
+    i32x4 f[FB + FA];  // B's, then A's
+    int s[(FB + FA) / 4];
   };
-  const char* ra = lds + wr * (FA / 4) * kMxPanel + lane * 16;
   const char* rb = lds + (kPA + wc * (FB / 4)) * kMxPanel + lane * 16;
-  const char* qa = lds + wr * (FA / 4) * kMxPanel + 4096 + lane * 4;
-  const char* qb = lds + (kPA + wc * (FB / 4)) * kMxPanel + 4096 + lane * 4;
-  auto read = [&](Frags& r, int slot) {
-    const int o = slot * kStage;
-#pragma unroll
-    for (int p = 0; p < FB / 4; ++p) r.sb[p] = *reinterpret_cast<const int*>(qb + o + p * kMxPanel);
-#pragma unroll
-    for (int p = 0; p < FA / 4; ++p) r.sa[p] = *reinterpret_cast<const int*>(qa + o + p * kMxPanel);
-#pragma unroll
-    for (int f = 0; f < FB; ++f)
-      r.b[f] = *reinterpret_cast<const i32x4*>(rb + o + (f / 4) * kMxPanel + (f % 4) * 1024);
-#pragma unroll
-    for (int f = 0; f < FA; ++f)
-      r.a[f] = *reinterpret_cast<const i32x4*>(ra + o + (f / 4) * kMxPanel + (f % 4) * 1024);
+  const char* ra = lds + wr * (FA / 4) * kMxPanel + lane * 16;
+  constexpr int kReads = (FA + FB) / 4 * 5;
+  // read `d` of a step's kReads: per panel the scales, then four fragments
+  auto read = [&](auto D, Frags& r, int o) {
+    constexpr int d = decltype(D)::value, p = d / 5, e = d % 5;
+    constexpr bool isb = p < FB / 4;
+    const char* at = (isb ? rb + p * kMxPanel : ra + (p - FB / 4) * kMxPanel) + o;
+    if constexpr (e == 0) r.s[p] = *reinterpret_cast<const int*>(at + 4096 - lane * 12);
+    else r.f[p * 4 + e - 1] = *reinterpret_cast<const i32x4*>(at + (e - 1) * 1024);
   };
+
   f32x4 acc[FA][FB];
+  auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < FA; ++i)
+    for (int i = 0; i < FA; ++i)
 #pragma unroll
-    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // C^T tiles (B's fragment first): a lane ends with four consecutive
-  // columns of one row of C
-  auto mul = [&](const Frags& r) {
-#pragma unroll
-    for (int i = 0; i < FA; i += 4)
-#pragma unroll
-      for (int j = 0; j < FB; j += 4) {
-        auto row = [&](auto I) {
-          constexpr int ii = decltype(I)::value;
-          acc[i + ii][j] = mx_mfma<0, ii>(r.b[j], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j]);
-          acc[i + ii][j + 1] = mx_mfma<1, ii>(r.b[j + 1], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 1]);
-          acc[i + ii][j + 2] = mx_mfma<2, ii>(r.b[j + 2], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 2]);
-          acc[i + ii][j + 3] = mx_mfma<3, ii>(r.b[j + 3], r.sb[j / 4], r.a[i + ii], r.sa[i / 4], acc[i + ii][j + 3]);
-        };
-        row(std::integral_constant<int, 0>{});
-        row(std::integral_constant<int, 1>{});
-        row(std::integral_constant<int, 2>{});
-        row(std::integral_constant<int, 3>{});
-      }
+      for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   };
+
+  // Results of item `it`: a lane's four consecutive columns of a row (the
+  // MFMAs form C^T) through LDS, 16 rows x kRowData bytes at a time, to
+  // 16-byte stores of whole row segments.
+  auto store = [&](int it) {
+    constexpr int kSize = kOut == kOutBf16 ? 2 : 4;
+    constexpr int kCols = kRowData / kSize, kLanes = kRowData / 16, kE = 16 / kSize;
+    using T = std::conditional_t<kOut == kOutBf16, uint16_t, float>;
+    char* stage = lds + kStages * kStage + w * kOutLds;
+    const int split = it / tiles;
+    int ti, tj;
+    mx_tile(it - split * tiles, g.tm, g.tn, ti, tj);
+    const int m0 = (ti * WR + wr) * FA * 16, n0 = (tj * WC + wc) * FB * 16;
+    const int sr = lane / kLanes, sc = lane % kLanes;
+    T* C = static_cast<T*>(g.C) + (g.n_split > 1 ? (int64_t)split * g.M * g.N : 0) +
+           (int64_t)(m0 + sr) * g.ldc + n0 + sc * kE;
+    auto put = [&](auto WHOLE) {
+      constexpr bool whole = decltype(WHOLE)::value;  // every lane's 16 bytes in or out
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) issue(s, s);
+      for (int h = 0; h < FB * 16 / kCols; ++h) {
+        f32x4 bias[kCols / 16];
+        if constexpr (kBias)
+#pragma unroll
+          for (int j = 0; j < kCols / 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              bias[j][e] = g.bias[min(n0 + h * kCols + 16 * j + 4 * (lane >> 4) + e, g.N - 1)];
+#pragma unroll
+        for (int i = 0; i < FA; ++i) {
+#pragma unroll
+          for (int j = 0; j < kCols / 16; ++j) {
+            f32x4 v = acc[i][h * (kCols / 16) + j];
+            if constexpr (kBias) v += bias[j];
+            char* to = stage + (lane & 15) * kRow + (16 * j + 4 * (lane >> 4)) * kSize;
+            if constexpr (kOut == kOutBf16)
+              *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                         bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+            else *reinterpret_cast<f32x4*>(to) = v;
+          }
+          asm volatile("" ::: "memory");
+#pragma unroll
+          for (int t = 0; t < kLanes / 4; ++t) {
+            const int r = t * (64 / kLanes);
+            const int m = m0 + 16 * i + r + sr, n = n0 + h * kCols + sc * kE;
+            const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
+            if (m >= g.M || n >= g.N) continue;
+            T* p = C + (int64_t)(16 * i + r) * g.ldc + h * kCols;
+            if constexpr (whole) {
+              if constexpr (kOut == kOutAcc) {
+                f32x4* p4 = reinterpret_cast<f32x4*>(p);
+                *p4 = *p4 + __builtin_bit_cast(f32x4, q);
+              } else {
+                *reinterpret_cast<uint4*>(p) = q;
+              }
+            } else {
+              T o[kE];
+              __builtin_memcpy(o, &q, 16);
+#pragma unroll
+              for (int e = 0; e < kE; ++e)
+                if (n + e < g.N) {
+                  if constexpr (kOut == kOutAcc) p[e] += o[e];
+                  else p[e] = o[e];
+                }
+            }
+          }
+          asm volatile("" ::: "memory");
+        }
+      }
+    };
+    if (g.vec) put(std::true_type{});
+    else put(std::false_type{});
+  };
+
+  seek(blockIdx.x);
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    static_for<kVm>(copy);
+    copied();
+  }
   __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 1) * kVm));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frags fr[2];
-  read(fr[0], 0);
-  int slot = 0;
-  auto step = [&](auto P, int i) {
+  static_for<kReads>([&](auto D) { read(D, fr[0], 0); });
+  int slot = 0, landed = 0;  // landed: coming steps whose copies are known to have landed
+  auto step = [&](auto P) {
     constexpr int p = decltype(P)::value;
-    const int next = slot + 1 == kStages ? 0 : slot + 1;
+    const int next = (slot + 1) % kStages;
     // step i's fragments are in registers, step i + 1's copies have landed
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 2) * kVm));
+    // (the branch over the wait in asm: see above)
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(63));
+    asm volatile("s_cmp_gt_i32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%1)\n1:"
+                 :: "s"(landed), "n"((kStages - 2) * kVm) : "scc", "memory");
+    --landed;
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(slot, i + kStages);
-    read(fr[1 - p], next);
-    mul(fr[p]);
+    const Frags& r = fr[p];
+    constexpr int kGroups = FA * FB / 4, kSide = kReads + kVm;
+    const int o = next * kStage;
+    // two reads, then a copy
+    static_for<kGroups>([&](auto G) {
+      constexpr int gr = decltype(G)::value;
+      constexpr int s0 = gr * kSide / kGroups, s1 = (gr + 1) * kSide / kGroups;
+      static_for<s1 - s0>([&](auto S) {
+        constexpr int k = s0 + decltype(S)::value;
+        constexpr int c = (k + 1) / 3 < kVm ? (k + 1) / 3 : kVm;  // copies before side op k
+        constexpr bool is_copy = k % 3 == 2 && k / 3 < kVm;
+        if constexpr (is_copy) copy(std::integral_constant<int, k / 3>{});
+        else read(std::integral_constant<int, k - c>{}, fr[1 - p], o);
+      });
+      constexpr int i = gr / (FB / 4), j = gr % (FB / 4) * 4;
+      auto one = [&](auto J) {
+        constexpr int jj = decltype(J)::value;
+        acc[i][j + jj] = mx_mfma<jj, i % 4>(r.f[j + jj], r.s[j / 4], r.f[FB + i], r.s[FB / 4 + i / 4], acc[i][j + jj]);
+      };
+      static_for<4>(one);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    copied();
     slot = next;
   };
-  for (int i = 0; i < steps; i += 2) {
-    step(std::integral_constant<int, 0>{}, i);
-    if (i + 1 < steps) step(std::integral_constant<int, 1>{}, i + 1);
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    clear();
+    const int s0 = it / tiles * g.per_split;
+    const int steps = max((min(g.steps, s0 + g.per_split) - s0 + 1) & ~1, kStages);
+    // the last kStages steps copy for the next item
+    for (int part = 0; part < 2; ++part) {
+      const int n = part ? kStages : steps - kStages;
+      for (int i = 0; i < n; i += 2) {
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+      }
+      if (part == 0) seek(it + gridDim.x);
+    }
+    // The copies in flight are those of the next kStages - 1 steps and have
+    // been under way since; once they are in, those steps need not wait
+    // behind the stores.
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+    landed = kStages - 1;
+    store(it);
   }
   // no copy may land in LDS that the next workgroup has been given
   __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
-  float* part = g.part + (int64_t)split * g.M * g.N;
-  const int m0 = (ti * WR + wr) * FA * 16 + (lane & 15), n0 = (tj * WC + wc) * FB * 16 + (lane >> 4) * 4;
-#pragma unroll
-  for (int i = 0; i < FA; ++i)
-#pragma unroll
-    for (int j = 0; j < FB; ++j) mx_store4(g, m0 + 16 * i, n0 + 16 * j, acc[i][j], part);
 }
 
 // C = the splits' partials, added in split order (+ bias, or to C).
@@ -465,7 +592,7 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
       for (int e = 0; e < 4; ++e)
         if (n + e < g.N) v[e] += p[e];
   }
-  mx_store4(g, m, n, v, nullptr);
+  mx_store4(g, m, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -597,7 +724,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
     f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][f][l * 4]);
 #pragma unroll
     for (int u = 1; u < kFewWaves; ++u) v += *reinterpret_cast<const f32x4*>(&sums[u][f][l * 4]);
-    mx_store4(g, f * 16 + (l & 15), (panel * 4 + frag) * 16 + (l >> 4) * 4, v, nullptr);
+    mx_store4(g, f * 16 + (l & 15), (panel * 4 + frag) * 16 + (l >> 4) * 4, v);
   }
 }
 
@@ -610,7 +737,7 @@ hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t co
   const int ct = (int)((cols + kQTile - 1) / kQTile);
   const int64_t tiles = (rows + kQTile - 1) / kQTile * ct;
   const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
-  const bool vec = ((uintptr_t)X & 15) == 0 && ld * es % 16 == 0;
+  const bool vec = ((uintptr_t)X & 15) == 0 && ld * es % 16 == 0 && cols * es % 16 == 0;
   auto go = [&](auto zero) {
     using T = decltype(zero);
     auto run = [&](auto kernel) {
@@ -651,7 +778,7 @@ MxPlan mx_plan(int64_t M, int64_t N, int64_t k) {
   }
   auto tiles = [&](int t) { return (M + t - 1) / t * ((N + t - 1) / t); };
   p.tile = tiles(256) >= 192 ? 256 : 128;
-  const int64_t slots = p.tile == 256 ? 256 : 512;
+  const int64_t slots = p.tile == 256 ? kMxSlots256 : kMxSlots128;
   int64_t want = slots / tiles(p.tile);
   if (want > steps / 8) want = steps / 8;
   if (want < 1) want = 1;
@@ -711,13 +838,29 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
   g.per_split = p.per_split;
   g.n_split = p.n_split;
   MxGemm h = g;
-  if (p.n_split > 1) {
-    h.part = g.part = static_cast<float*>(ws);
-    h.mode = kOutPart;
+  if (p.n_split > 1) {  // fp32 partials [split][M][N], summed by k_mx_reduce
+    g.part = static_cast<float*>(ws);
+    h.C = ws;
+    h.ldc = N;
+    h.mode = kOutF32;
+    h.bias = nullptr;
   }
-  const dim3 grid((uint32_t)((int64_t)g.tm * g.tn * p.n_split));
-  if (p.tile == 256) k_mx_gemm<2, 2, 8, 8, 4><<<grid, dim3(256), 0, s>>>(h);
-  else k_mx_gemm<2, 2, 4, 4, 4><<<grid, dim3(256), 0, s>>>(h);
+  const size_t es = h.mode == kOutBf16 ? 2 : 4;
+  h.vec = N * es % 16 == 0 && h.ldc * es % 16 == 0 && (uintptr_t)h.C % 16 == 0;
+  const int64_t items = (int64_t)g.tm * g.tn * p.n_split;
+  const int64_t most = p.tile == 256 ? kMxSlots256 : kMxSlots128;
+  const dim3 grid((uint32_t)(items < most ? items : most)), block(256);
+  auto run = [&](auto OUT, auto BIAS) {
+    constexpr int kOut = decltype(OUT)::value;
+    constexpr bool kBias = decltype(BIAS)::value;
+    if (p.tile == 256) k_mx_gemm<2, 2, 8, 8, kOut, kBias><<<grid, block, 0, s>>>(h);
+    else k_mx_gemm<2, 2, 4, 4, kOut, kBias><<<grid, block, 0, s>>>(h);
+  };
+  const std::integral_constant<int, kOutBf16> bf16;
+  const std::integral_constant<int, kOutF32> f32;
+  if (h.mode == kOutAcc) run(std::integral_constant<int, kOutAcc>{}, std::false_type{});
+  else if (h.bias) h.mode == kOutBf16 ? run(bf16, std::true_type{}) : run(f32, std::true_type{});
+  else h.mode == kOutBf16 ? run(bf16, std::false_type{}) : run(f32, std::false_type{});
   hipError_t e = done();
   if (e != hipSuccess || p.n_split == 1) return e;
   k_mx_reduce<<<dim3((uint32_t)((M * ((N + 3) / 4) + 255) / 256)), dim3(256), 0, s>>>(g);

@@ -54,6 +54,16 @@ __device__ __forceinline__ void stv(T* p, const float (&v)[kVec]) {
     for (int i = 0; i < kVec; ++i) p[i] = o.v[i];
 }
 
+template <class T, int kVec>
+__device__ __forceinline__ Vec<T, kVec> ldraw(const T* p) {
+  if constexpr (kVec * sizeof(T) == 16)
+    return __builtin_bit_cast(Vec<T, kVec>, *reinterpret_cast<const uint4*>(p));
+  Vec<T, kVec> o;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) o.v[i] = p[i];
+  return o;
+}
+
 // kVec floats of a d-vector that may be NULL (then `none`)
 template <int kVec>
 __device__ __forceinline__ void ldw(const float* p, int at, float none, float (&o)[kVec]) {
@@ -228,25 +238,40 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) gw[i][j] = gb[i][j] = 0.f;
   const int64_t begin = (int64_t)blockIdx.x * a.per, end = min(a.rows, begin + a.per);
+  // Rows are fetched one ahead, from addresses clamped into the run and the
+  // row; what lies outside counts as x = mean, dy = 0.
+  Vec<T, kVec> nx[kNV], ng[kNV];
+  float nr, nmu;
+  auto fetch = [&](int64_t row) {
+    row = min(row, end - 1);
+    const T* x = static_cast<const T*>(a.X) + row * a.d;
+    const T* dy = static_cast<const T*>(a.dY) + row * a.d;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int at = min((i * 64 * kW + l) * kVec, a.d - kVec);
+      nx[i] = ldraw<T, kVec>(x + at);
+      ng[i] = ldraw<T, kVec>(dy + at);
+    }
+    nr = a.rstd[row];
+    nmu = kLayer ? a.mean[row] : 0.f;
+  };
+  fetch(begin + grp);
   int phase = 0;
   for (int64_t base = begin; base < end; base += kGroups, phase ^= 1) {
     const int64_t row = base + grp;
     const bool live = row < end;
-    const T* x = static_cast<const T*>(a.X) + row * a.d;
-    const T* dy = static_cast<const T*>(a.dY) + row * a.d;
-    const float r = live ? a.rstd[row] : 0.f, mu = kLayer && live ? a.mean[row] : 0.f;
+    const float r = live ? nr : 0.f, mu = live ? nmu : 0.f;
     float h[kNV][kVec], g[kNV][kVec];
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int at = (i * 64 * kW + l) * kVec;
-      if (live && at < a.d) {
-        ldv<T, kVec>(x + at, h[i]);
-        ldv<T, kVec>(dy + at, g[i]);
-      } else {
+      const bool in = live && (i * 64 * kW + l) * kVec < a.d;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) h[i][j] = mu, g[i][j] = 0.f;
+      for (int j = 0; j < kVec; ++j) {
+        h[i][j] = in ? (float)nx[i].v[j] : mu;
+        g[i][j] = in ? (float)ng[i].v[j] : 0.f;
       }
     }
+    if (base + kGroups < end) fetch(row + kGroups);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -375,24 +400,26 @@ __global__ __launch_bounds__(256) void k_norm_cols(NormBwd a) {
   if (a.pb) a.pb[(int64_t)blockIdx.y * a.d + c] = gb;
 }
 
-// The partial rows summed: 32 columns x 8 threads a column per workgroup,
-// thread k of a column adds partials k, k + 8, ..., the eight in order.
+// The partial rows summed: 32 columns x 32 threads a column per workgroup,
+// thread k of a column adds partials k, k + 32, ..., then the 32 in order.
 // blockIdx.y: the weight's gradient, or the bias's.
-__global__ __launch_bounds__(256) void k_norm_sum(const float* pw, const float* pb, float* dw, float* db,
-                                                  int parts, int d, bool accumulate) {
-  __shared__ float s[8][32];
+__global__ __launch_bounds__(1024) void k_norm_sum(const float* pw, const float* pb, float* dw, float* db,
+                                                   int parts, int d, bool accumulate) {
+  __shared__ float s[32][33];
   const float* p = blockIdx.y ? pb : pw;
   float* o = blockIdx.y ? db : dw;
   if (!o) return;
   const int x = threadIdx.x & 31, k = threadIdx.x >> 5, c = (int)blockIdx.x * 32 + x;
   float v = 0.f;
-  if (c < d)
-    for (int i = k; i < parts; i += 8) v += p[(int64_t)i * d + c];
+  if (c < d) {
+#pragma unroll 8
+    for (int i = k; i < parts; i += 32) v += p[(int64_t)i * d + c];
+  }
   s[k][x] = v;
   __syncthreads();
   if (k || c >= d) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += s[i][x];
+  for (int i = 1; i < 32; ++i) v += s[i][x];
   o[c] = accumulate ? o[c] + v : v;
 }
 
@@ -509,7 +536,7 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
   else typed(0.f);
   hipError_t e = done();
   if (e != hipSuccess || !cols) return e;
-  k_norm_sum<<<dim3((uint32_t)((d + 31) / 32), dbias ? 2 : 1), dim3(256), 0, s>>>(a.pw, a.pb, dweight, dbias,
+  k_norm_sum<<<dim3((uint32_t)((d + 31) / 32), dbias ? 2 : 1), dim3(1024), 0, s>>>(a.pw, a.pb, dweight, dbias,
                                                                               a.parts, (int)d, accumulate);
   return done();
 }
