@@ -62,13 +62,14 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
   b = __uint_as_float(w & 0xffff0000u);
 }
 
-constexpr int kQTile = 128;     // the tile is kQTile x kQTile: one k step of either operand
+constexpr int kQRows = 128;     // rows of a quantize tile: one k step of the operand by columns
+constexpr int kQCols = 64;      // columns: a row panel of it, half a k step of the operand by rows
 constexpr int kQThreads = 256;
 
-// One tile of X through LDS.  By rows: a thread takes 32 consecutive columns
-// of a row, threads in fragment order, so a wave writes a whole 1 KB
-// fragment.  By columns: a thread takes two neighbouring columns of 32 rows.
-// The LDS row stride is 4 banks past a multiple of 64, so the 16 rows of a
+// One tile of X through LDS, a block of 32 per thread.  By rows: 32
+// consecutive columns of a row, threads in fragment order, so 32 lanes write
+// 512 contiguous bytes of a fragment.  By columns: 32 rows of a column.  The
+// LDS row stride is 4 banks past a multiple of 32, so the 16 rows of a
 // fragment fall in 16 distinct groups of 4 banks.
 template <class T, bool kByRow, bool kByCol>
 __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X, int64_t rows,
@@ -76,13 +77,13 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
                                                         uint8_t* C, int col_tiles, bool vec,
                                                         uint32_t* flags) {
   constexpr int kPer = 16 / sizeof(T);                  // elements of a 16-byte load
-  constexpr int kStride = kQTile * sizeof(T) + 16;      // bytes of an LDS row
-  constexpr int kChunks = kQTile / kPer;                // 16-byte chunks of a row
-  constexpr int kLoads = kQTile * kChunks / kQThreads;  // chunks per thread
-  __shared__ __attribute__((aligned(16))) char lds[kQTile * kStride];
+  constexpr int kStride = kQCols * sizeof(T) + 16;      // bytes of an LDS row
+  constexpr int kChunks = kQCols / kPer;                // 16-byte chunks of a row
+  constexpr int kLoads = kQRows * kChunks / kQThreads;  // chunks per thread
+  __shared__ __attribute__((aligned(16))) char lds[kQRows * kStride];
   const int t = threadIdx.x;
   const int tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
-  const int64_t r0 = (int64_t)tr * kQTile, c0 = (int64_t)tc * kQTile;
+  const int64_t r0 = (int64_t)tr * kQRows, c0 = (int64_t)tc * kQCols;
   // Loads go out together, from addresses clamped into X; what lies outside
   // becomes zero.
   if (vec) {  // every 16-byte chunk lies inside X or outside
@@ -101,16 +102,16 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
     }
   } else {
     constexpr int kAtOnce = 16;
-    for (int e0 = t; e0 < kQTile * kQTile; e0 += kAtOnce * kQThreads) {
+    for (int e0 = t; e0 < kQRows * kQCols; e0 += kAtOnce * kQThreads) {
       T v[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int e = e0 + i * kQThreads;
-        v[i] = X[min(r0 + e / kQTile, rows - 1) * ld + min(c0 + e % kQTile, cols - 1)];
+        v[i] = X[min(r0 + e / kQCols, rows - 1) * ld + min(c0 + e % kQCols, cols - 1)];
       }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const int e = e0 + i * kQThreads, r = e / kQTile, c = e % kQTile;
+        const int e = e0 + i * kQThreads, r = e / kQCols, c = e % kQCols;
         if (r0 + r >= rows || c0 + c >= cols) v[i] = (T)0.f;
         *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = v[i];
       }
@@ -119,15 +120,13 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
   __syncthreads();
   uint32_t fl = 0;
   if constexpr (kByRow) {
-    const int64_t panels = (rows + kMxRows - 1) / kMxRows;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = t + i * kQThreads;  // fragment-major: 8 fragments x 64 lanes
-      const int f = e >> 6, lane = e & 63, b = lane >> 4, r = f * 16 + (lane & 15);
-      const int64_t panel = (r0 >> 6) + (f >> 2);
-      if (panel >= panels) break;       // wave-uniform
+    // 8 fragments x 2 blocks x 16 rows; the panel's steps cover an even
+    // number of tiles, the last of which may lie past the columns (zeros)
+    const int f = t >> 5, bb = (t >> 4) & 1, r = f * 16 + (t & 15);
+    const int64_t panel = (r0 >> 6) + (f >> 2);
+    if (panel < (rows + kMxRows - 1) / kMxRows) {
       float v[32];
-      const char* src = lds + r * kStride + b * 32 * sizeof(T);
+      const char* src = lds + r * kStride + bb * 32 * sizeof(T);
 #pragma unroll
       for (int j = 0; j < 32 / kPer; ++j) {
         const uint4 q = *reinterpret_cast<const uint4*>(src + 16 * j);
@@ -145,44 +144,28 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
       }
       uint32_t code, bf = 0;
       const uint4 w = mx_block(v, code, bf);
-      if (r0 + r < rows && c0 + b * 32 < cols) fl |= bf;
-      uint8_t* out = R + (panel * col_tiles + tc) * (int64_t)kMxPanel;
+      if (r0 + r < rows && c0 + bb * 32 < cols) fl |= bf;
+      const int lane = ((tc & 1) * 2 + bb) * 16 + (t & 15);
+      uint8_t* out = R + (panel * (col_tiles / 2) + (tc >> 1)) * (int64_t)kMxPanel;
       *reinterpret_cast<uint4*>(out + (f & 3) * 1024 + lane * 16) = w;
       out[4096 + lane * 4 + (f & 3)] = (uint8_t)code;
     }
   }
   if constexpr (kByCol) {
-    const int64_t panels = (cols + kMxRows - 1) / kMxRows;
     const int64_t steps = (rows + kMxStep - 1) / kMxStep;
-    const int b = t >> 6, p = t & 63;  // rows 32 b .. +31, columns 2 p, 2 p + 1
-    const int c = 2 * p;
-    const int64_t panel = (c0 >> 6) + (c >> 6);
-    if (panel < panels) {
-      float lo[32], hi[32];
+    const int b = t >> 6, c = t & 63;  // rows 32 b .. +31 of column c
+    if (c0 < cols) {
+      float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const char* src = lds + (b * 32 + j) * kStride + c * sizeof(T);
-        if constexpr (sizeof(T) == 2) {
-          unpack2(*reinterpret_cast<const uint32_t*>(src), lo[j], hi[j]);
-        } else {
-          const float2 q = *reinterpret_cast<const float2*>(src);
-          lo[j] = q.x;
-          hi[j] = q.y;
-        }
-      }
-      uint32_t code0, code1, f0 = 0, f1 = 0;
-      const uint4 w0 = mx_block(lo, code0, f0);
-      const uint4 w1 = mx_block(hi, code1, f1);
-      if (r0 + b * 32 < rows) {
-        if (c0 + c < cols) fl |= f0;
-        if (c0 + c + 1 < cols) fl |= f1;
-      }
-      uint8_t* out = C + (panel * steps + tr) * (int64_t)kMxPanel;
-      const int f = (c >> 4) & 3, lane = b * 16 + (c & 15);
-      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16) = w0;
-      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16 + 16) = w1;
-      out[4096 + lane * 4 + f] = (uint8_t)code0;
-      out[4096 + lane * 4 + 4 + f] = (uint8_t)code1;
+      for (int j = 0; j < 32; ++j)
+        v[j] = ld1(reinterpret_cast<const T*>(lds + (b * 32 + j) * kStride + c * sizeof(T)));
+      uint32_t code, bf = 0;
+      const uint4 w = mx_block(v, code, bf);
+      if (r0 + b * 32 < rows && c0 + c < cols) fl |= bf;
+      uint8_t* out = C + (tc * steps + tr) * (int64_t)kMxPanel;
+      const int f = c >> 4, lane = b * 16 + (c & 15);
+      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16) = w;
+      out[4096 + lane * 4 + f] = (uint8_t)code;
     }
   }
   if (flags && fl) atomicOr(flags, fl);
@@ -219,7 +202,7 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
       for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
 #pragma unroll
       for (int j = 0; j < (int)sizeof(o) / 16; ++j)
-        reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(o)[j];
+        __builtin_nontemporal_store(reinterpret_cast<const nt_u4*>(o)[j], reinterpret_cast<nt_u4*>(dst) + j);
     } else {
       for (int j = 0; j < 8 && col + j < k; ++j) dst[j] = (T)v[j];
     }
@@ -734,8 +717,8 @@ hipError_t done() { return hipGetLastError(); }
 
 hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
                               uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s) {
-  const int ct = (int)((cols + kQTile - 1) / kQTile);
-  const int64_t tiles = (rows + kQTile - 1) / kQTile * ct;
+  const int ct = (int)((cols + kMxStep - 1) / kMxStep) * (kMxStep / kQCols);
+  const int64_t tiles = (rows + kQRows - 1) / kQRows * ct;
   const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
   const bool vec = ((uintptr_t)X & 15) == 0 && ld * es % 16 == 0 && cols * es % 16 == 0;
   auto go = [&](auto zero) {

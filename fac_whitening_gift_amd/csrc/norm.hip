@@ -43,13 +43,17 @@ __device__ __forceinline__ void ldv(const T* p, float (&o)[kVec]) {
   }
 }
 
-template <class T, int kVec>
+// kNt: around the caches.  The backward pass gains by it (16384 x 4096 bf16:
+// 89.8 -> 86.7 us), the forward pass loses (57.0 -> 59.7 us).
+template <class T, int kVec, bool kNt>
 __device__ __forceinline__ void stv(T* p, const float (&v)[kVec]) {
   Vec<T, kVec> o;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) o.v[i] = (T)v[i];
-  if constexpr (kVec * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, o);
-  else
+  if constexpr (kVec * sizeof(T) == 16) {
+    if constexpr (kNt) __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, o), reinterpret_cast<nt_u4*>(p));
+    else *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, o);
+  } else
 #pragma unroll
     for (int i = 0; i < kVec; ++i) p[i] = o.v[i];
 }
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_fwd(NormFwd a) {
     ldw<kVec>(a.bias, at, 0.f, b);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[i][j] = __builtin_fmaf(v[i][j] * r, w[j], b[j]);
-    stv<T, kVec>(y + at, v[i]);
+    stv<T, kVec, false>(y + at, v[i]);
   }
 }
 
@@ -238,7 +242,8 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) gw[i][j] = gb[i][j] = 0.f;
   const int64_t begin = (int64_t)blockIdx.x * a.per, end = min(a.rows, begin + a.per);
-  // Rows are fetched one ahead, from addresses clamped into the run and the
+  // Rows are fetched one ahead (not by 16 waves, whose registers that would
+  // overflow), from addresses clamped into the run and the
   // row; what lies outside counts as x = mean, dy = 0.
   Vec<T, kVec> nx[kNV], ng[kNV];
   float nr, nmu;
@@ -255,11 +260,13 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
     nr = a.rstd[row];
     nmu = kLayer ? a.mean[row] : 0.f;
   };
-  fetch(begin + grp);
+  constexpr bool kAhead = kW < 16;
+  if (kAhead) fetch(begin + grp);
   int phase = 0;
   for (int64_t base = begin; base < end; base += kGroups, phase ^= 1) {
     const int64_t row = base + grp;
     const bool live = row < end;
+    if (!kAhead) fetch(row);
     const float r = live ? nr : 0.f, mu = live ? nmu : 0.f;
     float h[kNV][kVec], g[kNV][kVec];
 #pragma unroll
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
         g[i][j] = in ? (float)ng[i].v[j] : 0.f;
       }
     }
-    if (base + kGroups < end) fetch(row + kGroups);
+    if (kAhead && base + kGroups < end) fetch(row + kGroups);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
@@ -320,7 +327,7 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
       if (!live || at >= a.d) continue;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) g[i][j] = r * (__builtin_fmaf(-h[i][j], s2, g[i][j]) - s1);
-      stv<T, kVec>(dx + at, g[i]);
+      stv<T, kVec, true>(dx + at, g[i]);
     }
   }
   if (!a.pw && !a.pb) return;
@@ -425,21 +432,28 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* pw, const float*
 
 hipError_t done() { return hipGetLastError(); }
 
-constexpr int kMaxCols = 64 * 16 * 16;  // widest row of the register form
+// Widest row of the register form (single elements take more registers, for
+// their addresses, than 16 waves have for 16 of them).
+constexpr int max_cols(int kVec) { return 64 * 16 * (kVec > 1 ? 16 : 8); }
 
-// Launch the instance for a width: kW waves a row, 8 or 16 elements a lane
-// (16 keep the backward pass, which holds four such arrays, at 4 waves per
-// SIMD).
+// Launch the instance for a width: kW waves a row and the elements of a lane.
+// Two waves with 32 elements each serve 4096 columns best (16384 rows of bf16,
+// forward / backward: 57.0 / 89.8 us; one wave with 64: 60.8; four with 16:
+// 59.6 / 90.6; eight with 8: 66.1 / 94.4).
 template <int kVec, class F>
 void by_width(int64_t d, F f) {
-  auto go = [&](auto W) {
-    constexpr int w = decltype(W)::value;
-    if (d <= 64 * w * 8) f(W, std::integral_constant<int, 8 / kVec>{});
-    else f(W, std::integral_constant<int, 16 / kVec>{});
-  };
-  if (d <= 1024) go(std::integral_constant<int, 1>{});
-  else if (d <= 4096) go(std::integral_constant<int, 4>{});
-  else go(std::integral_constant<int, 16>{});
+  auto go = [&](auto W, auto E) { f(W, std::integral_constant<int, decltype(E)::value / kVec>{}); };
+  const std::integral_constant<int, 1> w1;
+  const std::integral_constant<int, 2> w2;
+  const std::integral_constant<int, 8> w8, e8;
+  const std::integral_constant<int, 16> w16, e16;
+  const std::integral_constant<int, 32> e32;
+  if (d <= 512) go(w1, e8);
+  else if (d <= 1024) go(w1, e16);
+  else if (d <= 2048) go(w2, e16);
+  else if (d <= 4096) go(w2, e32);
+  else if (d <= 8192) go(w8, e16);
+  else go(w16, std::integral_constant<int, max_cols(kVec) / 1024>{});
 }
 
 constexpr int kNormParts = 1024;  // most partial rows of the weight's gradient
@@ -462,7 +476,7 @@ hipError_t launch_norm_forward(const void* X, int dtype, int64_t rows, int64_t d
     const bool vec = d % kFull == 0 && (((uintptr_t)X | (uintptr_t)Y | (uintptr_t)weight | (uintptr_t)bias) & 15) == 0;
     auto run = [&](auto VEC) {
       constexpr int kVec = decltype(VEC)::value;
-      if (d > kMaxCols) {
+      if (d > max_cols(kVec)) {
         if (kind == GIFT_NORM_LAYER) k_norm_fwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
         else k_norm_fwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
         return;
@@ -510,7 +524,7 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
     const bool vec = d % kFull == 0 && (((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX | (uintptr_t)weight) & 15) == 0;
     auto run = [&](auto VEC) {
       constexpr int kVec = decltype(VEC)::value;
-      if (d > kMaxCols) {
+      if (d > max_cols(kVec)) {
         if (dX) {
           if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
           else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
