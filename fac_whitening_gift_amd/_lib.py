@@ -7,7 +7,6 @@ is not built it raises instead of falling back to anything else.
 """
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -631,23 +630,18 @@ def _scratch(nbytes, device, ws):
     return ws, ws.data_ptr(), have
 
 
-def _on_stream(fn):
-    """Run a call given a stream as if that were the current one, so that what
-    it allocates (outputs, workspaces) belongs to that stream too."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kwargs)
-    return call
+def _on(stream, device, fn, *args):
+    """A call given a stream, run as if that were the current one: what it
+    allocates (outputs, workspaces) belongs to that stream too."""
+    if stream.device != device:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
-def _enqueue(device, stream, fn, *args):
+def _enqueue(device, fn, *args):
     """Call a library function with torch's current stream of the tensors'
     device appended."""
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, device))
     index = device.index
     if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -666,14 +660,15 @@ class MxOperand:
 
     __slots__ = ("rows", "k", "shape", "data", "device", "_struct", "_ref")
 
-    def __init__(self, rows, k, device="cuda", data=None):
-        self.rows, self.k = self.shape = (int(rows), int(k))
+    def __init__(self, rows, k, device="cuda", data=None, check=True):
+        self.rows, self.k = self.shape = (rows, k)
         nbytes = load().gift_mx_bytes(rows, k)
         if nbytes == 0:
-            raise ValueError("MXFP4 operand of %d x %d is out of range" % (self.rows, self.k))
+            raise ValueError("MXFP4 operand of %d x %d is out of range" % (rows, k))
         if data is None:
             data = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _dev(data, torch.uint8, (nbytes,), "data")
+        if check:
+            _dev(data, torch.uint8, (nbytes,), "data")
         self.data = data
         self.device = data.device
         self._struct = _Mx(rows, k, data.data_ptr())
@@ -692,7 +687,7 @@ def _quantize_target(want, rows, k, device, name):
     if want is None or want is False:
         return None
     if want is True:
-        return MxOperand(rows, k, device)
+        return MxOperand(rows, k, device, check=False)
     _operand(want, name, device)
     if want.shape != (rows, k):
         raise ValueError("%s has shape %s, expected %s" % (name, want.shape, (rows, k)))
@@ -703,28 +698,30 @@ def gift_mx_bytes(rows, k):
     return int(load().gift_mx_bytes(rows, k))
 
 
-@_on_stream
 def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
     """Quantize x (rows x cols, bf16 or fp32) to MXFP4 in one read: by_row /
     by_col True (allocate) or an MxOperand to fill, of x and of its transpose.
     -> (by_row operand or None, by_col operand or None)."""
+    if stream is not None:
+        return _on(stream, x.device, gift_mx_quantize, x, by_row, by_col, flags)
     ptr, dt, rows, cols, ld = _matrix(x, "x")
     row = _quantize_target(by_row, rows, cols, x.device, "by_row")
     col = _quantize_target(by_col, cols, rows, x.device, "by_col")
-    _enqueue(x.device, stream, load().gift_mx_quantize, ptr, dt, rows, cols, ld,
+    _enqueue(x.device, load().gift_mx_quantize, ptr, dt, rows, cols, ld,
              row._ref if row is not None else None, col._ref if col is not None else None,
              _flags_ptr(flags, x.device))
     return row, col
 
 
-@_on_stream
 def gift_mx_dequantize(a, dtype=torch.float32, out=None, stream=None):
     """-> rows x k tensor of the values the operand stands for."""
+    if stream is not None:
+        return _on(stream, a.device, gift_mx_dequantize, a, dtype, out)
     ref = _operand(a, "a")
     if out is None:
         out = torch.empty(a.shape, dtype=dtype, device=a.device)
     ptr, dt, _, _, ld = _matrix(out, "out", a.device, a.shape)
-    _enqueue(a.device, stream, load().gift_mx_dequantize, ref, ptr, dt, ld)
+    _enqueue(a.device, load().gift_mx_dequantize, ref, ptr, dt, ld)
     return out
 
 
@@ -732,11 +729,12 @@ def gift_mx_matmul_workspace_bytes(m, n, k):
     return int(load().gift_mx_matmul_workspace_bytes(m, n, k))
 
 
-@_on_stream
 def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=False, ws=None,
                    stream=None):
     """a (M x k), b (N x k) operands -> a b^T (+ bias), M x N of dtype (or out's);
     accumulate: out (fp32) += the product."""
+    if stream is not None:
+        return _on(stream, a.device, gift_mx_matmul, a, b, bias, out, dtype, accumulate, ws)
     ra, rb = _operand(a, "a"), _operand(b, "b", a.device)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
@@ -746,7 +744,7 @@ def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=F
     ptr, dt, _, _, ld = _matrix(out, "out", dev, shape)
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_matmul_workspace_bytes(a.rows, b.rows, a.k), dev, ws)
-    _enqueue(dev, stream, lib.gift_mx_matmul, ra, rb, _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
+    _enqueue(dev, lib.gift_mx_matmul, ra, rb, _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
              1 if accumulate else 0, wp, wb)
     return out
 
@@ -755,10 +753,11 @@ def gift_mx_linear_workspace_bytes(rows, n, k):
     return int(load().gift_mx_linear_workspace_bytes(rows, n, k))
 
 
-@_on_stream
 def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, stream=None):
     """x (rows x k, bf16 or fp32) quantized in the call, w an operand (n x k)
     -> x w^T (+ bias), rows x n of dtype (x's when not given)."""
+    if stream is not None:
+        return _on(stream, x.device, gift_mx_linear, x, w, bias, out, dtype, flags, ws)
     dev = x.device
     ptr, dt, rows, _, ld = _matrix(x, "x", w.device)
     rw = _operand(w, "w", dev)
@@ -770,7 +769,7 @@ def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, s
     yp, ydt, _, _, ldy = _matrix(out, "out", dev, shape)
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_linear_workspace_bytes(rows, w.rows, w.k), dev, ws)
-    _enqueue(dev, stream, lib.gift_mx_linear, ptr, dt, rows, ld, rw, _vector(bias, w.rows, "bias", dev),
+    _enqueue(dev, lib.gift_mx_linear, ptr, dt, rows, ld, rw, _vector(bias, w.rows, "bias", dev),
              yp, ydt, ldy, _flags_ptr(flags, dev), wp, wb)
     return out
 
@@ -786,11 +785,12 @@ def _f32(n, device):
     return torch.empty(n, dtype=torch.float32, device=device)
 
 
-@_on_stream
 def gift_norm_forward(x, weight=None, bias=None, eps=1e-5, kind=NORM_LAYER, out=None, mean=None,
                       rstd=None, stream=None):
     """Norm of every row of x (rows x d, bf16 or fp32); weight and bias: d fp32
     or None.  -> (y, mean (None for NORM_RMS), rstd)."""
+    if stream is not None:
+        return _on(stream, x.device, gift_norm_forward, x, weight, bias, eps, kind, out, mean, rstd)
     dev = x.device
     ptr, dt, rows, d = _dense(x, "x")
     if out is None:
@@ -798,16 +798,23 @@ def gift_norm_forward(x, weight=None, bias=None, eps=1e-5, kind=NORM_LAYER, out=
         yp = out.data_ptr()
     else:
         yp = _dense(out, "out", dev, (rows, d), x.dtype)[0]
+    mp = None
     if kind != NORM_LAYER:
         if mean is not None:
             raise ValueError("NORM_RMS has no mean")
     elif mean is None:
         mean = _f32(rows, dev)
+        mp = mean.data_ptr()
+    else:
+        mp = _vector(mean, rows, "mean", dev)
     if rstd is None:
         rstd = _f32(rows, dev)
-    _enqueue(dev, stream, load().gift_norm_forward, ptr, dt, rows, d, kind,
-             _vector(weight, d, "weight", dev), _vector(bias, d, "bias", dev), eps, yp,
-             _vector(mean, rows, "mean", dev), _vector(rstd, rows, "rstd", dev))
+        rp = rstd.data_ptr()
+    else:
+        rp = _vector(rstd, rows, "rstd", dev)
+    _enqueue(dev, load().gift_norm_forward, ptr, dt, rows, d, kind,
+             None if weight is None else _vector(weight, d, "weight", dev),
+             None if bias is None else _vector(bias, d, "bias", dev), eps, yp, mp, rp)
     return out, mean, rstd
 
 
@@ -815,13 +822,15 @@ def gift_norm_backward_workspace_bytes(rows, d):
     return int(load().gift_norm_backward_workspace_bytes(rows, d))
 
 
-@_on_stream
 def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dweight=None, dbias=None,
                        accumulate=False, ws=None, stream=None):
     """Gradients of gift_norm_forward for its statistics.  dx, dweight, dbias: a
     tensor to fill, False to leave out, None to allocate (dbias None: only for
     NORM_LAYER); accumulate adds to the given dweight and dbias.
     -> (dx, dweight, dbias), None for what was left out."""
+    if stream is not None:
+        return _on(stream, x.device, gift_norm_backward, dy, x, weight, mean, rstd, kind, dx, dweight,
+                   dbias, accumulate, ws)
     dev = x.device
     ptr, dt, rows, d = _dense(x, "x")
     gp = _dense(dy, "dy", dev, (rows, d), x.dtype)[0]
@@ -840,7 +849,7 @@ def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dwei
     need = lib.gift_norm_backward_workspace_bytes(rows, d) \
         if dweight is not None or dbias is not None else 0
     keep, wp, wb = _scratch(need, dev, ws)
-    _enqueue(dev, stream, lib.gift_norm_backward, gp, ptr, dt, rows, d, kind,
+    _enqueue(dev, lib.gift_norm_backward, gp, ptr, dt, rows, d, kind,
              _vector(weight, d, "weight", dev), _vector(mean, rows, "mean", dev),
              _vector(rstd, rows, "rstd", dev), xp, _vector(dweight, d, "dweight", dev),
              _vector(dbias, d, "dbias", dev), 1 if accumulate else 0, wp, wb)
