@@ -579,13 +579,13 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
 }
 
 // ---------------------------------------------------------------------------
-// few rows (M <= 64): a workgroup owns 16 columns of C (one fragment of B per
-// k step), its 8 waves take the k steps in turn, straight from memory into
-// the MFMA operands, and their sums are added in wave order through LDS.
-// kQuant: A is X itself (M <= 16 rows), quantized into LDS first.
+// Small products: a workgroup owns FM x 16 rows of a row panel (blockIdx.y)
+// and FN x 16 columns of a column panel of C.  Its 8 waves take the k steps
+// in turn, straight from memory into the MFMA operands, with no LDS and no
+// barrier in the loop, and their sums are added in wave order through LDS.
+// kQuant: A is X itself (at most 16 rows), quantized into LDS first.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
-constexpr int kFewUnroll = 4;
 
 struct MxFew {
   MxGemm g;
@@ -596,36 +596,37 @@ struct MxFew {
   bool xvec;
 };
 
-template <int FM, class T, bool kQuant>
+template <int FM, int FN, class T, bool kQuant>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
+  constexpr int kUnroll = FM + FN <= 5 ? 4 : 2;  // k steps in flight per wave
+  constexpr int kSub = 4 / FN;                   // workgroups of a column panel
   extern __shared__ __attribute__((aligned(16))) char dyn[];
-  __shared__ float sums[kFewWaves][FM][256];
+  __shared__ float sums[kFewWaves][FN][256];
   const MxGemm& g = q.g;
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  // the four fragments of a panel (one scale line) on one XCD
-  const int nf = (g.N + 15) / 16, panels = (nf + 3) / 4;
-  const int id = blockIdx.x;
+  // gridDim.x is a multiple of 8: a column panel stays on one XCD, with all
+  // its workgroups and row panels; XCDs below `rem` hold one panel more
+  const int panels = (g.N + kMxRows - 1) / kMxRows;
+  const int id = blockIdx.x, x = id % kXcd, u0 = id / kXcd;
   const int pq = panels / kXcd, rem = panels % kXcd;
-  int panel, frag;
-  {
-    const int x = id % kXcd, u = id / kXcd;
-    panel = x * pq + (x < rem ? x : rem) + u / 4;
-    frag = u % 4;
-    // XCDs below `rem` hold one panel more than the others
-    if (u / 4 >= pq + (x < rem ? 1 : 0)) return;
-  }
-  if (panel * 4 + frag >= nf) return;
-  const uint8_t* Bp = g.B + (int64_t)panel * g.steps * kMxPanel;
-  i32x4 b[kFewUnroll];
-  int sb[kFewUnroll];
+  if (u0 / kSub >= pq + (x < rem ? 1 : 0)) return;
+  const int panel = x * pq + (x < rem ? x : rem) + u0 / kSub, frag = u0 % kSub * FN;
+  if (panel * kMxRows + frag * 16 >= g.N) return;
+  const uint8_t* Bp = g.B + (int64_t)panel * g.steps * kMxPanel + frag * 1024;
+  i32x4 b[kUnroll][FN];
+  int sb[kUnroll];
   auto load_b = [&](int s) {
 #pragma unroll
-    for (int u = 0; u < kFewUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int st = min(s + u * kFewWaves, g.steps - 1);
       const uint8_t* p = Bp + (int64_t)st * kMxPanel;
-      b[u] = *reinterpret_cast<const i32x4*>(p + frag * 1024 + lane * 16);
-      sb[u] = p[4096 + lane * 4 + frag];
+#pragma unroll
+      for (int f = 0; f < FN; ++f) b[u][f] = *reinterpret_cast<const i32x4*>(p + f * 1024 + lane * 16);
+      const uint8_t* sc = p - frag * 1024 + 4096 + lane * 4;
+      if constexpr (FN == 1) sb[u] = sc[frag];
+      else if constexpr (FN == 2) sb[u] = *reinterpret_cast<const uint16_t*>(sc + frag);
+      else sb[u] = *reinterpret_cast<const int*>(sc);
     }
   };
   load_b(w);
@@ -669,45 +670,51 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
     if (q.flags && fl && id == 0) atomicOr(q.flags, fl);
     __syncthreads();
   }
-  f32x4 acc[FM];
+  f32x4 acc[FM][FN];
 #pragma unroll
-  for (int f = 0; f < FM; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int s = w; s < g.steps; s += kFewWaves * kFewUnroll) {
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s = w; s < g.steps; s += kFewWaves * kUnroll) {
     if (s != w) load_b(s);
-    i32x4 a[kFewUnroll][FM];
-    int sa[kFewUnroll];
+    i32x4 a[kUnroll][FM];
+    int sa[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kFewUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int st = min(s + u * kFewWaves, g.steps - 1);
       if constexpr (kQuant) {
         const int r = lane & 15, at = (st * 4 + (lane >> 4)) * g.M + (r < g.M ? r : 0);
         a[u][0] = *reinterpret_cast<const i32x4*>(dyn + at * 16);
         sa[u] = reinterpret_cast<const uint8_t*>(dyn)[(int64_t)g.steps * 4 * g.M * 16 + at];
       } else {
-        const uint8_t* p = g.A + (int64_t)st * kMxPanel;
+        const uint8_t* p = g.A + ((int64_t)blockIdx.y * g.steps + st) * kMxPanel;
 #pragma unroll
         for (int f = 0; f < FM; ++f) a[u][f] = *reinterpret_cast<const i32x4*>(p + f * 1024 + lane * 16);
         sa[u] = *reinterpret_cast<const int*>(p + 4096 + lane * 4);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kFewUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       if (s + u * kFewWaves >= g.steps) break;  // wave-uniform
-      acc[0] = mx_mfma<0, 0>(b[u], sb[u], a[u][0], sa[u], acc[0]);
-      if constexpr (FM > 1) acc[1] = mx_mfma<0, 1>(b[u], sb[u], a[u][1], sa[u], acc[1]);
-      if constexpr (FM > 2) acc[2] = mx_mfma<0, 2>(b[u], sb[u], a[u][2], sa[u], acc[2]);
-      if constexpr (FM > 3) acc[3] = mx_mfma<0, 3>(b[u], sb[u], a[u][3], sa[u], acc[3]);
+      static_for<FM * FN>([&](auto IJ) {
+        constexpr int i = decltype(IJ)::value / FN, j = decltype(IJ)::value % FN;
+        acc[i][j] = mx_mfma<j, i>(b[u][j], sb[u], a[u][i], sa[u], acc[i][j]);
+      });
     }
   }
 #pragma unroll
-  for (int f = 0; f < FM; ++f) *reinterpret_cast<f32x4*>(&sums[w][f][lane * 4]) = acc[f];
-  __syncthreads();
-  for (int e = t; e < FM * 64; e += 64 * kFewWaves) {
-    const int f = e >> 6, l = e & 63;
-    f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][f][l * 4]);
+  for (int i = 0; i < FM; ++i) {
+    if (i) __syncthreads();
 #pragma unroll
-    for (int u = 1; u < kFewWaves; ++u) v += *reinterpret_cast<const f32x4*>(&sums[u][f][l * 4]);
-    mx_store4(g, f * 16 + (l & 15), (panel * 4 + frag) * 16 + (l >> 4) * 4, v);
+    for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(&sums[w][j][lane * 4]) = acc[i][j];
+    __syncthreads();
+    if (t < FN * 64) {
+      const int j = t >> 6, l = t & 63;
+      f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][j][l * 4]);
+#pragma unroll
+      for (int k = 1; k < kFewWaves; ++k) v += *reinterpret_cast<const f32x4*>(&sums[k][j][l * 4]);
+      mx_store4(g, blockIdx.y * kMxRows + i * 16 + (l & 15), (panel * 4 + frag + j) * 16 + (l >> 4) * 4, v);
+    }
   }
 }
 
@@ -749,26 +756,60 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
   return done();
 }
 
-// How a product is cut: rows and columns per tile and the number of k splits.
+// How a product is cut.  The time of every candidate is estimated from its
+// sizes, in microseconds, with constants fitted to measurements on products
+// of 1 .. 16384 rows, 256 .. 11008 columns and k 256 .. 16384; the estimates
+// are within about 20% there, which is closer than the candidates lie
+// (measured, best against the next: 512 x 1024 x 1024 4.9 us in 32-column
+// workgroups, 6.7 in 128-tiles; 2000 x 4096 x 4096 23.0 us in 128-tiles, 32.0
+// in 256-tiles; 4096 x 4096 x 16384 113.6 us in 256-tiles, 134.1 in 128-tiles;
+// 256 x 1024 x 11008 14.3 us in 128-tiles split four ways, 24.5 unsplit).
 MxPlan mx_plan(int64_t M, int64_t N, int64_t k) {
   const int64_t steps = (k + kMxStep - 1) / kMxStep;
-  MxPlan p{};
-  if (M <= kMxFewRows) {
-    p.tile = 0;
-    p.n_split = 1;
-    p.per_split = (int)steps;
-    return p;
+  auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m; };
+  MxPlan best{};
+  double least = 1e300;
+  auto offer = [&](double us, int tile, int cols, int64_t per_split) {
+    if (us >= least) return;
+    least = us;
+    best.tile = tile;
+    best.cols = cols;
+    best.per_split = (int)per_split;
+    best.n_split = (int)up(steps, per_split);
+  };
+  // k_mx_few: a launch and a fixed latency, then the longer of a wave's chain
+  // of k steps and the operand bytes all workgroups load (at the rate the
+  // second-level caches give)
+  const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const int64_t panels = up(M, kMxRows);
+  if (panels <= 0xffff) {
+    const double rows = M <= 32 ? 0.65 : 1.0;
+    const double base[3] = {fm < 4 ? 3.6 : 4.3, fm < 4 ? 3.8 : 4.4, fm < 4 ? 3.9 : 4.7};
+    const double chain[3] = {1.65, 2.1, 2.8};
+    // an XCD reads all of A and an eighth of B; past its 4 MB cache the rate
+    // falls (512 x 700 x 16384: 22.5 us, in 128-tiles split four ways 17.1)
+    const double held = (double)((M + N / kXcd) * steps) * (kMxPanel / kMxRows);
+    const double slow = held > 4.5e6 ? 0.65 : 1.0;
+    const double rate[3] = {22e6 * slow, 17e6 * slow, 17e6 * slow};
+    for (int i = 0; i < 3; ++i) {
+      const int fn = 1 << i;
+      const double bytes = (double)panels * up(N, 16 * fn) * steps * ((fm + fn) * 1024 + 512);
+      const double lat = rows * chain[i] * steps / 32;
+      offer(base[i] + (lat > bytes / rate[i] ? lat : bytes / rate[i]), 0, 16 * fn, steps);
+    }
   }
-  auto tiles = [&](int t) { return (M + t - 1) / t * ((N + t - 1) / t); };
-  p.tile = tiles(256) >= 192 ? 256 : 128;
-  const int64_t slots = p.tile == 256 ? kMxSlots256 : kMxSlots128;
-  int64_t want = slots / tiles(p.tile);
-  if (want > steps / 8) want = steps / 8;
-  if (want < 1) want = 1;
-  if (want > 16) want = 16;
-  p.per_split = (int)((steps + want - 1) / want);
-  p.n_split = (int)((steps + p.per_split - 1) / p.per_split);
-  return p;
+  // tiles: rounds of the machine, each a chain of k steps; split sums write
+  // and read fp32 partials
+  const int64_t t256 = up(M, 256) * up(N, 256), t128 = up(M, 128) * up(N, 128);
+  const int64_t r256 = up(t256, kMxSlots256);
+  offer(10 + 0.78 * steps * r256 + 6 * (r256 - 1), 256, 0, steps);
+  for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= steps); want *= 2) {
+    const int64_t per = up(steps, want), items = t128 * up(steps, per), r = up(items, kMxSlots128);
+    double us = 5.5 + (items > 256 ? 0.5 : 0.21) * per * r + 1.5 * (r - 1);
+    if (want > 1) us += 4 + 2.0 * up(steps, per) * M * N * 4 / 4e6;
+    offer(us, 128, 0, per);
+  }
+  return best;
 }
 
 size_t mx_matmul_ws(int64_t M, int64_t N, int64_t k) {
@@ -794,10 +835,10 @@ MxGemm gemm_args(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64
   return g;
 }
 
-uint32_t few_blocks(const MxGemm& g) {
+uint32_t few_blocks(const MxGemm& g, int fn) {
   // every XCD gets the grid of the one with the most panels
   const int panels = (g.N + kMxRows - 1) / kMxRows;
-  return (uint32_t)((panels + kXcd - 1) / kXcd * kXcd * 4);
+  return (uint32_t)((panels + kXcd - 1) / kXcd * kXcd * (4 / fn));
 }
 }  // namespace
 
@@ -809,11 +850,22 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
   if (p.tile == 0) {
     MxFew q{};
     q.g = g;
-    const dim3 grid(few_blocks(g)), block(64 * kFewWaves);
-    if (M <= 16) k_mx_few<1, float, false><<<grid, block, 0, s>>>(q);
-    else if (M <= 32) k_mx_few<2, float, false><<<grid, block, 0, s>>>(q);
-    else if (M <= 48) k_mx_few<3, float, false><<<grid, block, 0, s>>>(q);
-    else k_mx_few<4, float, false><<<grid, block, 0, s>>>(q);
+    auto run = [&](auto FM, auto FN) {
+      constexpr int fm = decltype(FM)::value, fn = decltype(FN)::value;
+      const dim3 grid(few_blocks(g, fn), (uint32_t)((M + kMxRows - 1) / kMxRows)), block(64 * kFewWaves);
+      k_mx_few<fm, fn, float, false><<<grid, block, 0, s>>>(q);
+    };
+    const std::integral_constant<int, 1> i1;
+    const std::integral_constant<int, 2> i2;
+    const std::integral_constant<int, 4> i4;
+    auto rows = [&](auto FN) {
+      if (M <= 16) run(i1, FN);
+      else if (M <= 32) run(i2, FN);
+      else run(i4, FN);
+    };
+    if (p.cols == 16) rows(i1);
+    else if (p.cols == 32) rows(i2);
+    else rows(i4);
     return done();
   }
   g.tm = (int)((M + p.tile - 1) / p.tile);
@@ -868,10 +920,10 @@ hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t l
   q.flags = flags;
   const size_t es = x_dtype == GIFT_DTYPE_BF16 ? 2 : 4;
   q.xvec = ((uintptr_t)X & 15) == 0 && ldx * es % 16 == 0;
-  const dim3 grid(few_blocks(q.g)), block(64 * kFewWaves);
+  const dim3 grid(few_blocks(q.g, 1)), block(64 * kFewWaves);
   const size_t lds = few_lds(M, k);
-  if (x_dtype == GIFT_DTYPE_BF16) k_mx_few<1, __bf16, true><<<grid, block, lds, s>>>(q);
-  else k_mx_few<1, float, true><<<grid, block, lds, s>>>(q);
+  if (x_dtype == GIFT_DTYPE_BF16) k_mx_few<1, 1, __bf16, true><<<grid, block, lds, s>>>(q);
+  else k_mx_few<1, 1, float, true><<<grid, block, lds, s>>>(q);
   return done();
 }
 

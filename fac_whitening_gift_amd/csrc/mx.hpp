@@ -13,11 +13,11 @@ namespace gift {
 constexpr int kMxRows = 64;                      // rows of an operand panel
 constexpr int kMxStep = 128;                     // k elements of a step
 constexpr int kMxPanel = GIFT_MX_PANEL_BYTES;    // bytes of a panel's step
-constexpr int kMxFewRows = 64;                   // products of at most this many rows: k_mx_few
 constexpr size_t kMxFewLds = 96 << 10;           // LDS for the rows quantized in front of a product
 
 struct MxPlan {
   int tile;       // rows and columns of a tile, 0: k_mx_few
+  int cols;       // columns of a workgroup of k_mx_few
   int n_split;    // k splits
   int per_split;  // k steps of a split
 };

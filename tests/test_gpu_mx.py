@@ -152,7 +152,43 @@ def test_matmul(m, n, k):
     assert torch.equal(fg.gift_mx_matmul(ra, rb, dtype=torch.float32), f)   # the same bits again
 
 
-@pytest.mark.parametrize("m,n,k", [(20, 70, 200), (200, 150, 300), (600, 2000, 128)])
+# (cut into: 256-tiles, several and one a workgroup; 128-tiles, one, several and split
+# four ways; small products of 64 and 16 columns a workgroup)
+LARGE = [(8100, 8180, 4100), (4000, 4090, 4200), (1100, 3001, 1100), (4100, 4030, 2100), (1000, 1101, 16000),
+         (1030, 2050, 1100), (3000, 9, 300)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_matmul_large(m, n, k):
+    """Whole outputs against fp64 products, on the device, of the operands'
+    decoded values; accumulation over 3 micro-batches; the last panels and
+    k steps ragged."""
+    say("mx matmul large %dx%dx%d" % (m, n, k))
+    g = torch.Generator(device=DEV).manual_seed(m + n)
+    a, b = torch.randn(m, k, generator=g, device=DEV), torch.randn(n, k, generator=g, device=DEV)
+    a *= torch.exp2(torch.randint(-6, 7, (m, 1), generator=g, device=DEV).float())
+    ra, _ = fg.gift_mx_quantize(a, by_row=True)
+    rb, _ = fg.gift_mx_quantize(b, by_row=True)
+    va, vb = (fg.gift_mx_dequantize(r).double() for r in (ra, rb))
+    c, s = va @ vb.t(), va.abs() @ vb.abs().t()
+    tol = 2 * k * 2.0 ** -23 * s
+    f = fg.gift_mx_matmul(ra, rb, dtype=torch.float32)
+    assert bool(((f.double() - c).abs() <= tol).all())
+    bias = torch.randn(n, generator=g, device=DEV)
+    h = fg.gift_mx_matmul(ra, rb, bias=bias)
+    ref = c + bias.double()
+    # the fp32 sum, the bias' rounding, the rounding to bf16
+    t = tol + 2.0 ** -24 * (ref.abs() + tol)
+    assert bool(((h.double() - ref).abs() <= t + 2.0 ** -8 * (ref.abs() + t)).all())
+    assert torch.equal(fg.gift_mx_matmul(ra, rb), f.to(BF16))
+    acc = torch.zeros(m, n, device=DEV)
+    for _ in range(3):
+        fg.gift_mx_matmul(ra, rb, out=acc, accumulate=True)
+    assert bool(((acc.double() - 3 * c).abs() <= 3 * tol + 3 * 2.0 ** -24 * (3 * c.abs() + 3 * tol)).all())
+    assert torch.equal(fg.gift_mx_matmul(ra, rb, dtype=torch.float32), f)
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 70, 200), (200, 150, 300), (600, 2000, 128), (1100, 3001, 1100)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 def test_matmul_into_a_slice(m, n, k, dtype):
     """Rows of a wider C: what lies beside the product stays as it was."""

@@ -79,7 +79,7 @@ def test_matmul_refuses(want, case):
 
 def test_matmul_refuses_a_bad_workspace():
     lib = fg.load()
-    m, n, k = 256, 256, 16384   # few tiles, a long sum: split over k
+    m, n, k = 1024, 1024, 16384   # few tiles, a long sum: split over k
     need = fg.gift_mx_matmul_workspace_bytes(m, n, k)
     assert need >= 2 * m * n * 4
 
