@@ -656,18 +656,20 @@ class MxOperand:
     """An MXFP4 operand: a rows x k matrix quantized in blocks of 32 along k,
     in the layout of gift_mx (include/gift.h).  data: uint8 device tensor of
     gift_mx_bytes(rows, k), allocated when not given; gift_mx_quantize fills
-    it.  shape is (rows, k)."""
+    it.  like: a device tensor to allocate beside.  shape is (rows, k)."""
 
     __slots__ = ("rows", "k", "shape", "data", "device", "_struct", "_ref")
 
-    def __init__(self, rows, k, device="cuda", data=None, check=True):
+    def __init__(self, rows, k, device="cuda", data=None, like=None):
         self.rows, self.k = self.shape = (rows, k)
         nbytes = load().gift_mx_bytes(rows, k)
         if nbytes == 0:
             raise ValueError("MXFP4 operand of %d x %d is out of range" % (rows, k))
-        if data is None:
-            data = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if check:
+        if like is not None:
+            data = like.new_empty(nbytes, dtype=torch.uint8)
+        else:
+            if data is None:
+                data = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _dev(data, torch.uint8, (nbytes,), "data")
         self.data = data
         self.device = data.device
@@ -683,12 +685,12 @@ def _operand(op, name, device=None):
     return op._ref
 
 
-def _quantize_target(want, rows, k, device, name):
+def _quantize_target(want, rows, k, x, name):
     if want is None or want is False:
         return None
     if want is True:
-        return MxOperand(rows, k, device, check=False)
-    _operand(want, name, device)
+        return MxOperand(rows, k, like=x)
+    _operand(want, name, x.device)
     if want.shape != (rows, k):
         raise ValueError("%s has shape %s, expected %s" % (name, want.shape, (rows, k)))
     return want
@@ -705,11 +707,11 @@ def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
     if stream is not None:
         return _on(stream, x.device, gift_mx_quantize, x, by_row, by_col, flags)
     ptr, dt, rows, cols, ld = _matrix(x, "x")
-    row = _quantize_target(by_row, rows, cols, x.device, "by_row")
-    col = _quantize_target(by_col, cols, rows, x.device, "by_col")
+    row = _quantize_target(by_row, rows, cols, x, "by_row")
+    col = _quantize_target(by_col, cols, rows, x, "by_col")
     _enqueue(x.device, load().gift_mx_quantize, ptr, dt, rows, cols, ld,
              row._ref if row is not None else None, col._ref if col is not None else None,
-             _flags_ptr(flags, x.device))
+             None if flags is None else _flags_ptr(flags, x.device))
     return row, col
 
 
@@ -719,7 +721,7 @@ def gift_mx_dequantize(a, dtype=torch.float32, out=None, stream=None):
         return _on(stream, a.device, gift_mx_dequantize, a, dtype, out)
     ref = _operand(a, "a")
     if out is None:
-        out = torch.empty(a.shape, dtype=dtype, device=a.device)
+        out = a.data.new_empty(a.shape, dtype=dtype)
     ptr, dt, _, _, ld = _matrix(out, "out", a.device, a.shape)
     _enqueue(a.device, load().gift_mx_dequantize, ref, ptr, dt, ld)
     return out
@@ -738,10 +740,15 @@ def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=F
     ra, rb = _operand(a, "a"), _operand(b, "b", a.device)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    dev, shape = a.device, (a.rows, b.rows)
+    dev = a.device
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    ptr, dt, _, _, ld = _matrix(out, "out", dev, shape)
+        dt = _DTYPES.get(dtype)
+        if dt is None:
+            raise ValueError("dtype must be bf16 or fp32, got %s" % dtype)
+        out = a.data.new_empty((a.rows, b.rows), dtype=dtype)
+        ptr, ld = out.data_ptr(), b.rows
+    else:
+        ptr, dt, _, _, ld = _matrix(out, "out", dev, (a.rows, b.rows))
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_matmul_workspace_bytes(a.rows, b.rows, a.k), dev, ws)
     _enqueue(dev, lib.gift_mx_matmul, ra, rb, _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
@@ -763,10 +770,13 @@ def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, s
     rw = _operand(w, "w", dev)
     if x.shape[1] != w.k:
         raise ValueError("x has %d columns, w sums over %d" % (x.shape[1], w.k))
-    shape = (rows, w.rows)
     if out is None:
-        out = torch.empty(shape, dtype=dtype or x.dtype, device=dev)
-    yp, ydt, _, _, ldy = _matrix(out, "out", dev, shape)
+        out = x.new_empty((rows, w.rows), dtype=dtype)
+        if out.dtype not in _DTYPES:
+            raise ValueError("dtype must be bf16 or fp32, got %s" % dtype)
+        yp, ydt, ldy = out.data_ptr(), _DTYPES[out.dtype], w.rows
+    else:
+        yp, ydt, _, _, ldy = _matrix(out, "out", dev, (rows, w.rows))
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_linear_workspace_bytes(rows, w.rows, w.k), dev, ws)
     _enqueue(dev, lib.gift_mx_linear, ptr, dt, rows, ld, rw, _vector(bias, w.rows, "bias", dev),
@@ -838,19 +848,33 @@ def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dwei
         dbias = False
     if accumulate and (dweight is None or dbias is None):
         raise ValueError("accumulate adds to given gradients")
+    xp = wp = bp = None
     if dx is None:
         dx = torch.empty_like(x)
+        xp = dx.data_ptr()
     elif dx is False:
         dx = None
-    dweight = _f32(d, dev) if dweight is None else None if dweight is False else dweight
-    dbias = _f32(d, dev) if dbias is None else None if dbias is False else dbias
-    xp = None if dx is None else _dense(dx, "dx", dev, (rows, d), x.dtype)[0]
+    else:
+        xp = _dense(dx, "dx", dev, (rows, d), x.dtype)[0]
+    if dweight is None:
+        dweight = _f32(d, dev)
+        wp = dweight.data_ptr()
+    elif dweight is False:
+        dweight = None
+    else:
+        wp = _vector(dweight, d, "dweight", dev)
+    if dbias is None:
+        dbias = _f32(d, dev)
+        bp = dbias.data_ptr()
+    elif dbias is False:
+        dbias = None
+    else:
+        bp = _vector(dbias, d, "dbias", dev)
     lib = load()
-    need = lib.gift_norm_backward_workspace_bytes(rows, d) \
-        if dweight is not None or dbias is not None else 0
-    keep, wp, wb = _scratch(need, dev, ws)
+    need = lib.gift_norm_backward_workspace_bytes(rows, d) if wp or bp else 0
+    keep, sp, sb = _scratch(need, dev, ws)
     _enqueue(dev, lib.gift_norm_backward, gp, ptr, dt, rows, d, kind,
-             _vector(weight, d, "weight", dev), _vector(mean, rows, "mean", dev),
-             _vector(rstd, rows, "rstd", dev), xp, _vector(dweight, d, "dweight", dev),
-             _vector(dbias, d, "dbias", dev), 1 if accumulate else 0, wp, wb)
+             None if weight is None else _vector(weight, d, "weight", dev),
+             None if mean is None else _vector(mean, rows, "mean", dev),
+             _vector(rstd, rows, "rstd", dev), xp, wp, bp, 1 if accumulate else 0, sp, sb)
     return dx, dweight, dbias

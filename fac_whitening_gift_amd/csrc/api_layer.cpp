@@ -66,7 +66,7 @@ gift_status launched(hipError_t e) { return e == hipSuccess ? GIFT_OK : hip_fail
 
 // Workspace of gift_mx_linear: X's operand, then the product's.
 size_t linear_ws(int64_t rows, int64_t n, int64_t k) {
-  if (mx_linear_one_launch(rows, k)) return 0;
+  if (mx_linear_cols(rows, n, k)) return 0;
   return align_up(gift_mx_bytes(rows, k)) + mx_matmul_ws(rows, n, k);
 }
 
@@ -151,7 +151,7 @@ gift_status gift_mx_linear(const void* X, int x_dtype, int64_t rows, int64_t ldx
   GIFT_TRY(check_ws(ws, ws_bytes, linear_ws(rows, W->rows, W->k)));
   hipStream_t st = (hipStream_t)stream;
   const uint8_t* w = static_cast<const uint8_t*>(W->data);
-  if (mx_linear_one_launch(rows, W->k))
+  if (mx_linear_cols(rows, W->rows, W->k))
     return launched(launch_mx_linear_few(X, x_dtype, rows, ldx, w, W->rows, W->k, bias, Y, y_dtype, ldy,
                                          dev_flags, st));
   uint8_t* q = static_cast<uint8_t*>(ws);

@@ -468,7 +468,9 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(
                 f32x4* p4 = reinterpret_cast<f32x4*>(p);
                 *p4 = *p4 + __builtin_bit_cast(f32x4, q);
               } else {
-                *reinterpret_cast<uint4*>(p) = q;
+                // around the caches: 4096^3 43.2 -> 41.5 us, 16384 x 1536 x 4096
+                // 58.4 -> 56.6 us
+                __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, q), reinterpret_cast<nt_u4*>(p));
               }
             } else {
               T o[kE];
@@ -764,52 +766,55 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
 // workgroups, 6.7 in 128-tiles; 2000 x 4096 x 4096 23.0 us in 128-tiles, 32.0
 // in 256-tiles; 4096 x 4096 x 16384 113.6 us in 256-tiles, 134.1 in 128-tiles;
 // 256 x 1024 x 11008 14.3 us in 128-tiles split four ways, 24.5 unsplit).
-MxPlan mx_plan(int64_t M, int64_t N, int64_t k) {
-  const int64_t steps = (k + kMxStep - 1) / kMxStep;
-  auto up = [](int64_t x, int64_t m) { return (x + m - 1) / m; };
+static int64_t up_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
+
+// k_mx_few with 16 fn columns a workgroup: a launch and a fixed latency, then
+// the longer of a wave's chain of k steps and the operand bytes that all
+// workgroups load, at the rate the second-level caches give.
+static double few_us(int64_t M, int64_t N, int64_t steps, int fn) {
+  const int i = fn == 1 ? 0 : fn == 2 ? 1 : 2;
+  const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const double base[2][3] = {{3.6, 3.8, 3.9}, {4.3, 4.4, 4.7}}, chain[3] = {1.65, 2.1, 2.8};
+  const double lat = (M <= 32 ? 0.65 : 1.0) * chain[i] * steps / 32;
+  // an XCD reads all of A and an eighth of B; past its 4 MB cache the rate
+  // falls (512 x 700 x 16384: 22.5 us, in 128-tiles split four ways 17.1)
+  const double held = (double)((M + N / kXcd) * steps) * (kMxPanel / kMxRows);
+  const double rate = (i ? 17e6 : 22e6) * (held > 4.5e6 ? 0.65 : 1.0);
+  const double bytes = (double)up_div(M, kMxRows) * up_div(N, 16 * fn) * steps * ((fm + fn) * 1024 + 512);
+  return base[fm > 2][i] + (lat > bytes / rate ? lat : bytes / rate);
+}
+
+static MxPlan plan_us(int64_t M, int64_t N, int64_t k, double& least) {
+  const int64_t steps = up_div(k, kMxStep);
   MxPlan best{};
-  double least = 1e300;
+  least = 1e300;
   auto offer = [&](double us, int tile, int cols, int64_t per_split) {
     if (us >= least) return;
     least = us;
     best.tile = tile;
     best.cols = cols;
     best.per_split = (int)per_split;
-    best.n_split = (int)up(steps, per_split);
+    best.n_split = (int)up_div(steps, per_split);
   };
-  // k_mx_few: a launch and a fixed latency, then the longer of a wave's chain
-  // of k steps and the operand bytes all workgroups load (at the rate the
-  // second-level caches give)
-  const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const int64_t panels = up(M, kMxRows);
-  if (panels <= 0xffff) {
-    const double rows = M <= 32 ? 0.65 : 1.0;
-    const double base[3] = {fm < 4 ? 3.6 : 4.3, fm < 4 ? 3.8 : 4.4, fm < 4 ? 3.9 : 4.7};
-    const double chain[3] = {1.65, 2.1, 2.8};
-    // an XCD reads all of A and an eighth of B; past its 4 MB cache the rate
-    // falls (512 x 700 x 16384: 22.5 us, in 128-tiles split four ways 17.1)
-    const double held = (double)((M + N / kXcd) * steps) * (kMxPanel / kMxRows);
-    const double slow = held > 4.5e6 ? 0.65 : 1.0;
-    const double rate[3] = {22e6 * slow, 17e6 * slow, 17e6 * slow};
-    for (int i = 0; i < 3; ++i) {
-      const int fn = 1 << i;
-      const double bytes = (double)panels * up(N, 16 * fn) * steps * ((fm + fn) * 1024 + 512);
-      const double lat = rows * chain[i] * steps / 32;
-      offer(base[i] + (lat > bytes / rate[i] ? lat : bytes / rate[i]), 0, 16 * fn, steps);
-    }
-  }
+  if (up_div(M, kMxRows) <= 0xffff)  // grid.y
+    for (int fn = 1; fn <= 4; fn *= 2) offer(few_us(M, N, steps, fn), 0, 16 * fn, steps);
   // tiles: rounds of the machine, each a chain of k steps; split sums write
   // and read fp32 partials
-  const int64_t t256 = up(M, 256) * up(N, 256), t128 = up(M, 128) * up(N, 128);
-  const int64_t r256 = up(t256, kMxSlots256);
+  const int64_t t256 = up_div(M, 256) * up_div(N, 256), t128 = up_div(M, 128) * up_div(N, 128);
+  const int64_t r256 = up_div(t256, kMxSlots256);
   offer(10 + 0.78 * steps * r256 + 6 * (r256 - 1), 256, 0, steps);
   for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= steps); want *= 2) {
-    const int64_t per = up(steps, want), items = t128 * up(steps, per), r = up(items, kMxSlots128);
+    const int64_t per = up_div(steps, want), items = t128 * up_div(steps, per), r = up_div(items, kMxSlots128);
     double us = 5.5 + (items > 256 ? 0.5 : 0.21) * per * r + 1.5 * (r - 1);
-    if (want > 1) us += 4 + 2.0 * up(steps, per) * M * N * 4 / 4e6;
+    if (want > 1) us += 4 + 2.0 * up_div(steps, per) * M * N * 4 / 4e6;
     offer(us, 128, 0, per);
   }
   return best;
+}
+
+MxPlan mx_plan(int64_t M, int64_t N, int64_t k) {
+  double us;
+  return plan_us(M, N, k, us);
 }
 
 size_t mx_matmul_ws(int64_t M, int64_t N, int64_t k) {
@@ -907,7 +912,28 @@ static size_t few_lds(int64_t M, int64_t k) {
   return (size_t)((k + kMxStep - 1) / kMxStep * 4 * M * 17);
 }
 
-bool mx_linear_one_launch(int64_t M, int64_t k) { return M <= 16 && few_lds(M, k) <= kMxFewLds; }
+// Columns of a workgroup of the one-launch form, 0: quantize, then multiply.
+// In one launch every workgroup quantizes all of X, 0.75 us for each 512
+// blocks; a launch of its own takes 2.8 us (16 x 4096 -> 11008: 12.2, 10.0,
+// 7.4 us with 16, 32, 64 columns; 16 x 11008 -> 4096: 13.5 us in one launch,
+// 10.0 in two; 1 x 4096 -> 4096: 3.6 and 6.3).
+int mx_linear_cols(int64_t M, int64_t N, int64_t k) {
+  if (M > 16 || few_lds(M, k) > kMxFewLds) return 0;
+  const int64_t steps = up_div(k, kMxStep);
+  double least;
+  plan_us(M, N, k, least);
+  least += 2.8;
+  int cols = 0;
+  for (int fn = 1; fn <= 4; fn *= 2) {
+    const double load = up_div(N, 16 * fn) / 256.0;
+    const double us = few_us(M, N, steps, fn) + 0.75 * (M * steps * 4 / 512.0) * (load > 1 ? load : 1);
+    if (us < least) {
+      least = us;
+      cols = 16 * fn;
+    }
+  }
+  return cols;
+}
 
 hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t ldx, const uint8_t* W,
                                 int64_t N, int64_t k, const float* bias, void* Y, int dtype, int64_t ldy,
@@ -920,10 +946,17 @@ hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t l
   q.flags = flags;
   const size_t es = x_dtype == GIFT_DTYPE_BF16 ? 2 : 4;
   q.xvec = ((uintptr_t)X & 15) == 0 && ldx * es % 16 == 0;
-  const dim3 grid(few_blocks(q.g, 1)), block(64 * kFewWaves);
   const size_t lds = few_lds(M, k);
-  if (x_dtype == GIFT_DTYPE_BF16) k_mx_few<1, 1, __bf16, true><<<grid, block, lds, s>>>(q);
-  else k_mx_few<1, 1, float, true><<<grid, block, lds, s>>>(q);
+  auto run = [&](auto FN) {
+    constexpr int fn = decltype(FN)::value;
+    const dim3 grid(few_blocks(q.g, fn)), block(64 * kFewWaves);
+    if (x_dtype == GIFT_DTYPE_BF16) k_mx_few<1, fn, __bf16, true><<<grid, block, lds, s>>>(q);
+    else k_mx_few<1, fn, float, true><<<grid, block, lds, s>>>(q);
+  };
+  const int cols = mx_linear_cols(M, N, k);
+  if (cols == 16) run(std::integral_constant<int, 1>{});
+  else if (cols == 32) run(std::integral_constant<int, 2>{});
+  else run(std::integral_constant<int, 4>{});
   return done();
 }
 

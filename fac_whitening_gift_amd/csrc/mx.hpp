@@ -23,7 +23,7 @@ struct MxPlan {
 };
 MxPlan mx_plan(int64_t M, int64_t N, int64_t k);
 size_t mx_matmul_ws(int64_t M, int64_t N, int64_t k);
-bool mx_linear_one_launch(int64_t M, int64_t k);
+int mx_linear_cols(int64_t M, int64_t N, int64_t k);  // 0: two launches
 
 hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
                               uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s);

@@ -208,7 +208,7 @@ def test_matmul_into_a_slice(m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 @pytest.mark.parametrize("m,n,k", [(1, 40, 64), (1, 1000, 4096), (5, 129, 1000), (16, 64, 2048), (16, 32, 8192),
-                                   (24, 100, 600), (70, 90, 260)])
+                                   (24, 100, 600), (70, 90, 260), (2, 9000, 300), (16, 5000, 513)])
 def test_linear(m, n, k, dtype):
     say("mx linear %dx%dx%d %s" % (m, n, k, dtype))
     x, w = _draw(m, k, m + n, dtype, 3), _draw(n, k, k, torch.float32, 3)
