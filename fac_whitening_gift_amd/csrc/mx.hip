@@ -256,17 +256,15 @@ struct MxGemm {
   bool vec;        // C takes 4-element stores
 };
 enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
-// workgroups of a launch: one (256 x 256 tiles) or two per CU
-constexpr int kMxSlots256 = 256, kMxSlots128 = 512;
 
 // Tile of a workgroup: workgroups go to the XCDs in turn, so XCD x takes the
-// x-th contiguous run of the tiles in an order that walks bands of 4 tile
-// rows column by column: the tiles running together on one XCD share operand
-// panels in its L2.
+// x-th contiguous run of the tiles in an order that walks bands of 8 tile
+// rows column by column: the tiles running together on one XCD (64 of 128 x
+// 256: 8 x 8) share operand panels in its L2.
 __device__ __forceinline__ void mx_tile(int id, int tm, int tn, int& ti, int& tj) {
   const int n = tm * tn, q = n / kXcd, rem = n % kXcd, x = id % kXcd;
   const int u = x * q + (x < rem ? x : rem) + id / kXcd;
-  constexpr int kBand = 4;
+  constexpr int kBand = 8;
   const int band = u / (kBand * tn), first = band * kBand;
   const int h = tm - first < kBand ? tm - first : kBand;
   const int v = u - first * tn;
@@ -316,80 +314,95 @@ __device__ __forceinline__ void static_for(F f) {
 }
 
 // The product on tiles of (WR FA 16) x (WC FB 16): WR x WC waves, each with
-// FA x FB accumulator tiles.  A workgroup takes the work items (a tile and a
-// range of k steps) blockIdx.x, blockIdx.x + gridDim.x, ... as one stream of
-// k steps.  The operands' blocks of a step are copied as they lie into one
-// of kStages LDS stages by the buffer unit; the fragments come out of LDS
-// with one conflict-free 16-byte read per lane.  Per step i: wait until step
+// FA x FB accumulator tiles; a workgroup takes one tile and one range of k
+// steps.  The operands' blocks of a step are copied as they lie into one of
+// kStages LDS stages by the buffer unit; the fragments come out of LDS with
+// one conflict-free 16-byte read per lane.  Per step i: wait until step
 // i + 1's copies have landed, barrier, then run step i's MFMAs with, spread
 // between them, the copies of step i + kStages into the stage that step i has
 // left and the reads of step i + 1's fragments into the other register set.
-// The copies run ahead across items, so a tile's results leave (through a
-// wave's own corner of LDS, as whole row segments) while the next tile's
-// operands arrive.  Copies past an item's end write zeros (raw buffer
-// bounds): items are rounded up to an even number of steps, at least
-// kStages.  The loops hold no branch around a step: the compiler would sink
-// the MFMAs below it, away from the copies and reads they are spread among.
-template <int WR, int WC, int FA, int FB, int kOut, bool kBias>
-__global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(MxGemm g) {
-  constexpr int kWaves = WR * WC, kStages = 4;
+// Two workgroups of 128 x 256 or three of 128 x 128 share a CU, so one's
+// results leave under the other's MFMAs.
+// The loop holds no branch: the compiler would sink the MFMAs below it, away
+// from the copies and reads they are spread among.
+template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias>
+__global__ __launch_bounds__(64 * WR * WC, FB > 4 ? 2 : 3) void k_mx_gemm(MxGemm g) {
+  constexpr int kWaves = WR * WC;
   constexpr int kPA = WR * FA / 4, kPB = WC * FB / 4;  // panels of the tile
-  constexpr int kPer = (kPA + kPB) / kWaves;           // panels copied by a wave
-  static_assert(kPer * kWaves == kPA + kPB && FA % 4 == 0 && FB % 4 == 0, "whole panels");
+  static_assert(FA % 4 == 0 && FB % 4 == 0 && kPA * 4 % kWaves == 0 && kPB * 4 % kWaves == 0, "whole panels");
   constexpr int kStage = (kPA + kPB) * kMxPanel;
-  constexpr int kVm = 5 * kPer;                        // copies of a wave and step
+  // A wave's copies of a step: fragments of A and of B, then scales of a
+  // panel or more of each (where waves outnumber panels, some copy the same)
+  constexpr int kFA = kPA * 4 / kWaves, kFB = kPB * 4 / kWaves;
+  constexpr int kSA = (kPA + kWaves - 1) / kWaves, kSB = (kPB + kWaves - 1) / kWaves;
+  constexpr int kVm = kFA + kFB + kSA + kSB;
   constexpr int kRowData = FB * 32 > 256 ? 256 : FB * 32;  // bytes of a staged row of C
   constexpr int kRow = kRowData + 16;  // 4 banks past a power of two: 16 rows of one column, no conflict
-  constexpr int kOutLds = 16 * kRow;
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage + kWaves * kOutLds];
+  static_assert(kWaves * 16 * kRow <= kStages * kStage, "the results' staging fits in the stages");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = w / WC, wc = w % WC;
-  const int tiles = g.tm * g.tn, items = tiles * g.n_split;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  uint32_t vo[5];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) vo[f] = f * 1024 + lane * 16;
-  vo[4] = 4096 + lane * 4;
+  const int tiles = g.tm * g.tn, split = (int)blockIdx.x / tiles;
+  int ti, tj;
+  mx_tile((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
+  const int s0 = split * g.per_split, n_steps = min(g.steps, s0 + g.per_split) - s0;
+  const int steps = (n_steps + 1) & ~1;
 
-  // The copies' position in the stream.  Panels past an operand's last
-  // repeat it (their rows and columns of C are not written).
+  // The tile's first panel of A and of B as raw buffers, and for every copy
+  // of the wave its offset from there.  Panels past an operand's last repeat
+  // it (their rows and columns of C are not written); steps past the last
+  // lie outside both buffers and so become zeros.
   int c_step = 0, c_slot = 0;
-  __amdgpu_buffer_rsrc_t rs[kPer];
-  auto seek = [&](int it) {
-    const bool any = it < items;
-    if (!any) it = 0;
-    const int split = it / tiles;
-    int ti, tj;
-    mx_tile(it - split * tiles, g.tm, g.tn, ti, tj);
-    const int s0 = split * g.per_split;
-    const int n = any ? min(g.steps, s0 + g.per_split) - s0 : 0;
-    c_step = 0;
+  __amdgpu_buffer_rsrc_t rs[2];
+  uint32_t vo[kVm];
+  {
+    const int fa = ti * kPA, fb = tj * kPB;  // first panels, and how many lie in the operand
+    const int na = min(kPA, (g.M + kMxRows - 1) / kMxRows - fa), nb = min(kPB, (g.N + kMxRows - 1) / kMxRows - fb);
+    const int64_t len = (int64_t)g.steps * kMxPanel;
+    auto buffer = [&](const uint8_t* base, int first, int n) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          reinterpret_cast<void*>(uniform64(reinterpret_cast<uint64_t>(base) + first * len + (int64_t)s0 * kMxPanel)),
+          (short)0, __builtin_amdgcn_readfirstlane((int)(uint32_t)(n * len - (int64_t)s0 * kMxPanel)),
+          (int)kRawBufferWord3);
+    };
+    rs[0] = buffer(g.A, fa, na);
+    rs[1] = buffer(g.B, fb, nb);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int p = w * kPer + i;
-      const bool isb = p >= kPA;
-      const int last = ((isb ? g.N : g.M) + kMxRows - 1) / kMxRows - 1;
-      const int panel = min(isb ? tj * kPB + p - kPA : ti * kPA + p, last);
-      const uint64_t base = reinterpret_cast<uint64_t>(isb ? g.B : g.A) +
-                            ((uint64_t)panel * g.steps + s0) * kMxPanel;
-      rs[i] = __builtin_amdgcn_make_buffer_rsrc(
-          reinterpret_cast<void*>(uniform64(base)), (short)0,
-          __builtin_amdgcn_readfirstlane(n * kMxPanel), (int)kRawBufferWord3);
-    }
-  };
+    for (int d = 0; d < kFA; ++d)
+      vo[d] = (uint32_t)(min((w * kFA + d) / 4, na - 1) * len) + (w * kFA + d) % 4 * 1024 + lane * 16;
+#pragma unroll
+    for (int d = 0; d < kFB; ++d)
+      vo[kFA + d] = (uint32_t)(min((w * kFB + d) / 4, nb - 1) * len) + (w * kFB + d) % 4 * 1024 + lane * 16;
+#pragma unroll
+    for (int d = 0; d < kSA; ++d)
+      vo[kFA + kFB + d] = (uint32_t)(min((w + d * kWaves) % kPA, na - 1) * len) + 4096 + lane * 4;
+#pragma unroll
+    for (int d = 0; d < kSB; ++d)
+      vo[kFA + kFB + kSA + d] = (uint32_t)(min((w + d * kWaves) % kPB, nb - 1) * len) + 4096 + lane * 4;
+  }
   // copy `d` of the wave's kVm of a step
   auto copy = [&](auto D) {
-    constexpr int d = decltype(D)::value, i = d / 5, f = d % 5;
-    const uint32_t to = lds0 + (uint32_t)c_slot * kStage + (uint32_t)(w * kPer + i) * kMxPanel;
-    // the step goes into the vector offset, which the bounds check covers
-    const uint32_t off = (uint32_t)c_step * kMxPanel;
-    if constexpr (f < 4) dma16(rs[i], to + f * 1024, vo[f] + off);
-    else dma4(rs[i], to + 4096, vo[4] + off);
+    constexpr int d = decltype(D)::value;
+    // The step goes into the vector offset, which the bounds check covers;
+    // kOutside lies past four of the longest panels and does not carry.
+    constexpr uint32_t kOutside = 0x89000000u, kLen = ((1u << 24) / kMxStep) * kMxPanel;
+    static_assert(kOutside >= 4 * kLen && 3ull * kLen + kMxPanel + kOutside <= ~0u, "outside every buffer");
+    const uint32_t to = lds0 + (uint32_t)c_slot * kStage;
+    const uint32_t from = vo[d] + (c_step < n_steps ? (uint32_t)c_step * kMxPanel : kOutside);
+    if constexpr (d < kFA)
+      dma16(rs[0], to + (w * kFA + d) / 4 * kMxPanel + (w * kFA + d) % 4 * 1024, from);
+    else if constexpr (d < kFA + kFB)
+      dma16(rs[1], to + (kPA + (w * kFB + d - kFA) / 4) * kMxPanel + (w * kFB + d - kFA) % 4 * 1024, from);
+    else if constexpr (d < kFA + kFB + kSA)
+      dma4(rs[0], to + (w + (d - kFA - kFB) * kWaves) % kPA * kMxPanel + 4096, from);
+    else
+      dma4(rs[1], to + (kPA + (w + (d - kFA - kFB - kSA) * kWaves) % kPB) * kMxPanel + 4096, from);
   };
   auto copied = [&] {
-    c_slot = (c_slot + 1) % kStages;
+    c_slot = c_slot + 1 == kStages ? 0 : c_slot + 1;
     ++c_step;
   };
 
@@ -410,88 +423,11 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(
   };
 
   f32x4 acc[FA][FB];
-  auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < FA; ++i)
+  for (int i = 0; i < FA; ++i)
 #pragma unroll
-      for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
+    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Results of item `it`: a lane's four consecutive columns of a row (the
-  // MFMAs form C^T) through LDS, 16 rows x kRowData bytes at a time, to
-  // 16-byte stores of whole row segments.
-  auto store = [&](int it) {
-    constexpr int kSize = kOut == kOutBf16 ? 2 : 4;
-    constexpr int kCols = kRowData / kSize, kLanes = kRowData / 16, kE = 16 / kSize;
-    using T = std::conditional_t<kOut == kOutBf16, uint16_t, float>;
-    char* stage = lds + kStages * kStage + w * kOutLds;
-    const int split = it / tiles;
-    int ti, tj;
-    mx_tile(it - split * tiles, g.tm, g.tn, ti, tj);
-    const int m0 = (ti * WR + wr) * FA * 16, n0 = (tj * WC + wc) * FB * 16;
-    const int sr = lane / kLanes, sc = lane % kLanes;
-    T* C = static_cast<T*>(g.C) + (g.n_split > 1 ? (int64_t)split * g.M * g.N : 0) +
-           (int64_t)(m0 + sr) * g.ldc + n0 + sc * kE;
-    auto put = [&](auto WHOLE) {
-      constexpr bool whole = decltype(WHOLE)::value;  // every lane's 16 bytes in or out
-#pragma unroll
-      for (int h = 0; h < FB * 16 / kCols; ++h) {
-        f32x4 bias[kCols / 16];
-        if constexpr (kBias)
-#pragma unroll
-          for (int j = 0; j < kCols / 16; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              bias[j][e] = g.bias[min(n0 + h * kCols + 16 * j + 4 * (lane >> 4) + e, g.N - 1)];
-#pragma unroll
-        for (int i = 0; i < FA; ++i) {
-#pragma unroll
-          for (int j = 0; j < kCols / 16; ++j) {
-            f32x4 v = acc[i][h * (kCols / 16) + j];
-            if constexpr (kBias) v += bias[j];
-            char* to = stage + (lane & 15) * kRow + (16 * j + 4 * (lane >> 4)) * kSize;
-            if constexpr (kOut == kOutBf16)
-              *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
-                                                         bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
-            else *reinterpret_cast<f32x4*>(to) = v;
-          }
-          asm volatile("" ::: "memory");
-#pragma unroll
-          for (int t = 0; t < kLanes / 4; ++t) {
-            const int r = t * (64 / kLanes);
-            const int m = m0 + 16 * i + r + sr, n = n0 + h * kCols + sc * kE;
-            const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
-            if (m >= g.M || n >= g.N) continue;
-            T* p = C + (int64_t)(16 * i + r) * g.ldc + h * kCols;
-            if constexpr (whole) {
-              if constexpr (kOut == kOutAcc) {
-                f32x4* p4 = reinterpret_cast<f32x4*>(p);
-                *p4 = *p4 + __builtin_bit_cast(f32x4, q);
-              } else {
-                // around the caches: 4096^3 43.2 -> 41.5 us, 16384 x 1536 x 4096
-                // 58.4 -> 56.6 us
-                __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, q), reinterpret_cast<nt_u4*>(p));
-              }
-            } else {
-              T o[kE];
-              __builtin_memcpy(o, &q, 16);
-#pragma unroll
-              for (int e = 0; e < kE; ++e)
-                if (n + e < g.N) {
-                  if constexpr (kOut == kOutAcc) p[e] += o[e];
-                  else p[e] = o[e];
-                }
-            }
-          }
-          asm volatile("" ::: "memory");
-        }
-      }
-    };
-    if (g.vec) put(std::true_type{});
-    else put(std::false_type{});
-  };
-
-  seek(blockIdx.x);
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
     static_for<kVm>(copy);
@@ -502,30 +438,25 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(
   asm volatile("" ::: "memory");
   Frags fr[2];
   static_for<kReads>([&](auto D) { read(D, fr[0], 0); });
-  int slot = 0, landed = 0;  // landed: coming steps whose copies are known to have landed
+  int slot = 0;
   auto step = [&](auto P) {
     constexpr int p = decltype(P)::value;
-    const int next = (slot + 1) % kStages;
+    const int next = slot + 1 == kStages ? 0 : slot + 1;
     // step i's fragments are in registers, step i + 1's copies have landed
-    // (the branch over the wait in asm: see above)
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(63));
-    asm volatile("s_cmp_gt_i32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%1)\n1:"
-                 :: "s"(landed), "n"((kStages - 2) * kVm) : "scc", "memory");
-    --landed;
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 2) * kVm));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     const Frags& r = fr[p];
     constexpr int kGroups = FA * FB / 4, kSide = kReads + kVm;
     const int o = next * kStage;
-    // two reads, then a copy
+    // reads and copies in their proportion
     static_for<kGroups>([&](auto G) {
       constexpr int gr = decltype(G)::value;
       constexpr int s0 = gr * kSide / kGroups, s1 = (gr + 1) * kSide / kGroups;
       static_for<s1 - s0>([&](auto S) {
         constexpr int k = s0 + decltype(S)::value;
-        constexpr int c = (k + 1) / 3 < kVm ? (k + 1) / 3 : kVm;  // copies before side op k
-        constexpr bool is_copy = k % 3 == 2 && k / 3 < kVm;
-        if constexpr (is_copy) copy(std::integral_constant<int, k / 3>{});
+        constexpr int c = k * kVm / kSide;  // copies before side op k
+        if constexpr ((k + 1) * kVm / kSide > c) copy(std::integral_constant<int, c>{});
         else read(std::integral_constant<int, k - c>{}, fr[1 - p], o);
       });
       constexpr int i = gr / (FB / 4), j = gr % (FB / 4) * 4;
@@ -539,28 +470,83 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 32 ? 1 : 2) void k_mx_gemm(
     copied();
     slot = next;
   };
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    clear();
-    const int s0 = it / tiles * g.per_split;
-    const int steps = max((min(g.steps, s0 + g.per_split) - s0 + 1) & ~1, kStages);
-    // the last kStages steps copy for the next item
-    for (int part = 0; part < 2; ++part) {
-      const int n = part ? kStages : steps - kStages;
-      for (int i = 0; i < n; i += 2) {
-        step(std::integral_constant<int, 0>{});
-        step(std::integral_constant<int, 1>{});
-      }
-      if (part == 0) seek(it + gridDim.x);
-    }
-    // The copies in flight are those of the next kStages - 1 steps and have
-    // been under way since; once they are in, those steps need not wait
-    // behind the stores.
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
-    landed = kStages - 1;
-    store(it);
+  for (int i = 0; i < steps; i += 2) {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
   }
-  // no copy may land in LDS that the next workgroup has been given
+  // every copy has landed and every wave has read its last fragments: the
+  // stages are free for the results
   __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  // A lane holds four consecutive columns of a row (the MFMAs form C^T):
+  // through a wave's own corner of LDS, 16 rows x kRowData bytes at a time, to
+  // 16-byte stores of whole row segments.
+  constexpr int kSize = kOut == kOutBf16 ? 2 : 4;
+  constexpr int kCols = kRowData / kSize, kLanes = kRowData / 16, kE = 16 / kSize;
+  using T = std::conditional_t<kOut == kOutBf16, uint16_t, float>;
+  char* stage = lds + w * 16 * kRow;
+  const int m0 = (ti * WR + wr) * FA * 16, n0 = (tj * WC + wc) * FB * 16;
+  const int sr = lane / kLanes, sc = lane % kLanes;
+  T* C = static_cast<T*>(g.C) + (g.n_split > 1 ? (int64_t)split * g.M * g.N : 0) +
+         (int64_t)(m0 + sr) * g.ldc + n0 + sc * kE;
+  auto put = [&](auto WHOLE) {
+    constexpr bool whole = decltype(WHOLE)::value;  // every lane's 16 bytes in or out
+#pragma unroll
+    for (int h = 0; h < FB * 16 / kCols; ++h) {
+      f32x4 bias[kCols / 16];
+      if constexpr (kBias)
+#pragma unroll
+        for (int j = 0; j < kCols / 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            bias[j][e] = g.bias[min(n0 + h * kCols + 16 * j + 4 * (lane >> 4) + e, g.N - 1)];
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+#pragma unroll
+        for (int j = 0; j < kCols / 16; ++j) {
+          f32x4 v = acc[i][h * (kCols / 16) + j];
+          if constexpr (kBias) v += bias[j];
+          char* to = stage + (lane & 15) * kRow + (16 * j + 4 * (lane >> 4)) * kSize;
+          if constexpr (kOut == kOutBf16)
+            *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                       bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+          else *reinterpret_cast<f32x4*>(to) = v;
+        }
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < kLanes / 4; ++t) {
+          const int r = t * (64 / kLanes);
+          const int m = m0 + 16 * i + r + sr, n = n0 + h * kCols + sc * kE;
+          const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
+          if (m >= g.M || n >= g.N) continue;
+          T* p = C + (int64_t)(16 * i + r) * g.ldc + h * kCols;
+          if constexpr (whole) {
+            if constexpr (kOut == kOutAcc) {
+              f32x4* p4 = reinterpret_cast<f32x4*>(p);
+              *p4 = *p4 + __builtin_bit_cast(f32x4, q);
+            } else {
+              // around the caches: 4096^3 43.2 -> 41.5 us, 16384 x 1536 x 4096
+              // 58.4 -> 56.6 us
+              __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, q), reinterpret_cast<nt_u4*>(p));
+            }
+          } else {
+            T o[kE];
+            __builtin_memcpy(o, &q, 16);
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+              if (n + e < g.N) {
+                if constexpr (kOut == kOutAcc) p[e] += o[e];
+                else p[e] = o[e];
+              }
+          }
+        }
+        asm volatile("" ::: "memory");
+      }
+    }
+  };
+  if (g.vec) put(std::true_type{});
+  else put(std::false_type{});
 }
 
 // C = the splits' partials, added in split order (+ bias, or to C).
@@ -761,11 +747,11 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
 // How a product is cut.  The time of every candidate is estimated from its
 // sizes, in microseconds, with constants fitted to measurements on products
 // of 1 .. 16384 rows, 256 .. 11008 columns and k 256 .. 16384; the estimates
-// are within about 20% there, which is closer than the candidates lie
-// (measured, best against the next: 512 x 1024 x 1024 4.9 us in 32-column
-// workgroups, 6.7 in 128-tiles; 2000 x 4096 x 4096 23.0 us in 128-tiles, 32.0
-// in 256-tiles; 4096 x 4096 x 16384 113.6 us in 256-tiles, 134.1 in 128-tiles;
-// 256 x 1024 x 11008 14.3 us in 128-tiles split four ways, 24.5 unsplit).
+// are within about 20% there.  Measured, the best and the next: 512 x 1024 x
+// 1024 4.9 us in 32-column workgroups, 6.7 in 128 x 128 tiles; 1000 x 11008 x
+// 4096 26.8 us in 128 x 128, 28.9 in 128 x 256; 16384 x 11008 x 4096 346.8 us
+// in 128 x 256, 365.9 in 128 x 128; 256 x 1024 x 11008 13.9 us in 128 x 128
+// split four ways, 22.8 unsplit.
 static int64_t up_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // k_mx_few with 16 fn columns a workgroup: a launch and a fixed latency, then
@@ -788,27 +774,26 @@ static MxPlan plan_us(int64_t M, int64_t N, int64_t k, double& least) {
   const int64_t steps = up_div(k, kMxStep);
   MxPlan best{};
   least = 1e300;
-  auto offer = [&](double us, int tile, int cols, int64_t per_split) {
+  auto offer = [&](double us, int rows, int cols, int64_t per_split) {
     if (us >= least) return;
     least = us;
-    best.tile = tile;
+    best.rows = rows;
     best.cols = cols;
     best.per_split = (int)per_split;
     best.n_split = (int)up_div(steps, per_split);
   };
   if (up_div(M, kMxRows) <= 0xffff)  // grid.y
-    for (int fn = 1; fn <= 4; fn *= 2) offer(few_us(M, N, steps, fn), 0, 16 * fn, steps);
-  // tiles: rounds of the machine, each a chain of k steps; split sums write
-  // and read fp32 partials
-  const int64_t t256 = up_div(M, 256) * up_div(N, 256), t128 = up_div(M, 128) * up_div(N, 128);
-  const int64_t r256 = up_div(t256, kMxSlots256);
-  offer(10 + 0.78 * steps * r256 + 6 * (r256 - 1), 256, 0, steps);
+    for (int fn = 1; fn <= 4; fn *= 2) offer(few_us(M, N, steps, fn), 64, 16 * fn, steps);
+  // k_mx_gemm: a k step's time by the workgroups per CU; split sums write and
+  // read fp32 partials
+  const int64_t tiles = up_div(M, 128) * up_div(N, 128);
   for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= steps); want *= 2) {
-    const int64_t per = up_div(steps, want), items = t128 * up_div(steps, per), r = up_div(items, kMxSlots128);
-    double us = 5.5 + (items > 256 ? 0.5 : 0.21) * per * r + 1.5 * (r - 1);
-    if (want > 1) us += 4 + 2.0 * up_div(steps, per) * M * N * 4 / 4e6;
-    offer(us, 128, 0, per);
+    const int64_t per = up_div(steps, want), split = up_div(steps, per);
+    const double x = tiles * split / 256.0, step = 0.25 * x > 0.21 ? 0.25 * x : 0.21;
+    offer(5 + step * per + (split > 1 ? 3 + 1.6 * split * M * N * 4 / 4e6 : 0), 128, 128, per);
   }
+  const double x = up_div(M, 128) * up_div(N, 256) / 256.0;
+  offer(6.5 + (x <= 1 ? 0.42 : x <= 2 ? 0.25 + 0.33 * x : 0.47 * x) * steps, 128, 256, steps);
   return best;
 }
 
@@ -852,7 +837,7 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
                             void* ws, hipStream_t s) {
   const MxPlan p = mx_plan(M, N, k);
   MxGemm g = gemm_args(A, B, M, N, k, bias, C, dtype, ldc, accumulate);
-  if (p.tile == 0) {
+  if (p.rows == 64) {
     MxFew q{};
     q.g = g;
     auto run = [&](auto FM, auto FN) {
@@ -873,8 +858,8 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
     else rows(i4);
     return done();
   }
-  g.tm = (int)((M + p.tile - 1) / p.tile);
-  g.tn = (int)((N + p.tile - 1) / p.tile);
+  g.tm = (int)up_div(M, p.rows);
+  g.tn = (int)up_div(N, p.cols);
   g.per_split = p.per_split;
   g.n_split = p.n_split;
   MxGemm h = g;
@@ -887,14 +872,12 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
   }
   const size_t es = h.mode == kOutBf16 ? 2 : 4;
   h.vec = N * es % 16 == 0 && h.ldc * es % 16 == 0 && (uintptr_t)h.C % 16 == 0;
-  const int64_t items = (int64_t)g.tm * g.tn * p.n_split;
-  const int64_t most = p.tile == 256 ? kMxSlots256 : kMxSlots128;
-  const dim3 grid((uint32_t)(items < most ? items : most)), block(256);
+  const dim3 grid((uint32_t)((int64_t)g.tm * g.tn * p.n_split)), block(256);
   auto run = [&](auto OUT, auto BIAS) {
     constexpr int kOut = decltype(OUT)::value;
     constexpr bool kBias = decltype(BIAS)::value;
-    if (p.tile == 256) k_mx_gemm<2, 2, 8, 8, kOut, kBias><<<grid, block, 0, s>>>(h);
-    else k_mx_gemm<2, 2, 4, 4, kOut, kBias><<<grid, block, 0, s>>>(h);
+    if (p.cols == 256) k_mx_gemm<2, 2, 4, 8, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
+    else k_mx_gemm<2, 2, 4, 4, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
   };
   const std::integral_constant<int, kOutBf16> bf16;
   const std::integral_constant<int, kOutF32> f32;

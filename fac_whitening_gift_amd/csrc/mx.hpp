@@ -16,8 +16,8 @@ constexpr int kMxPanel = GIFT_MX_PANEL_BYTES;    // bytes of a panel's step
 constexpr size_t kMxFewLds = 96 << 10;           // LDS for the rows quantized in front of a product
 
 struct MxPlan {
-  int tile;       // rows and columns of a tile, 0: k_mx_few
-  int cols;       // columns of a workgroup of k_mx_few
+  int rows;       // of a workgroup: 64 (k_mx_few) or 128 (k_mx_gemm)
+  int cols;       // 16, 32, 64 or 128, 256
   int n_split;    // k splits
   int per_split;  // k steps of a split
 };
