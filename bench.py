@@ -30,6 +30,7 @@ JSON line on stdout.
     python bench.py --study reduce [--ranks 8]   # simulated data-parallel reduction
     python bench.py --study matrixfree    # refresh power steps with A Q = X^T (X Q) / N
     python bench.py --study stream        # HBM rates of the round trip's access patterns
+    python bench.py --study layer [--ref-shape 1024,2816,8192]   # a layer's MXFP4 step into the round trip
 """
 
 import argparse
@@ -68,9 +69,9 @@ def parse():
                         "(no device QR or eigendecomposition), no quality report")
     p.add_argument("--study", default=None,
                    choices=["staleness", "interval", "rank", "reference", "copy", "reduce",
-                            "matrixfree", "stream"])
+                            "matrixfree", "stream", "layer"])
     p.add_argument("--ref-shape", default="1024,2816,8192",
-                   help="hidden,mlp,tokens of the block of the reference study")
+                   help="hidden,mlp,tokens of the block of the reference and layer studies")
     p.add_argument("--rank-list", default="8,16,32,64,b32,b64",
                    help="factor ranks, and bN for block-diagonal N x N blocks (rank study)")
     p.add_argument("--intervals", default="10,25,50,100", help="refresh intervals (interval study)")
@@ -211,7 +212,7 @@ def main():
         sys.exit(2)
     studies = {"staleness": staleness_study, "interval": interval_study, "rank": rank_study,
                "reference": reference_study, "reduce": reduce_study,
-               "matrixfree": matrixfree_study, "stream": stream_study}
+               "matrixfree": matrixfree_study, "stream": stream_study, "layer": layer_study}
     if args.study == "copy":
         print(json.dumps(copy_calibration()), flush=True)
         return
@@ -1166,6 +1167,83 @@ def reduce_study(args, device="cuda:0"):
                 res[method]["unwhiten_ms"] = round(t1.elapsed_time(t2), 4)
         res["m2_reduction"] = round(1 - res["gift"]["m2"] / res["euclid"]["m2"], 4)
         out[fmt] = res
+    return out
+
+
+# ---------------------------------------------------------------------------
+# layer study
+# ---------------------------------------------------------------------------
+
+def layer_study(args, device="cuda:0"):
+    """A gate layer's training step with its products in MXFP4, from the
+    residual stream to the round trip of its gradient: RMS norm, refresh of
+    the factor on the norm's output X, Y = X W^T, dX = dY W and G = dY^T X on
+    operands quantized along the summed axis, the norm's backward pass, and
+    the round trip of G (GIFT and Euclidean; per-tensor E4M3 and MXFP4).
+    Errors against fp64 products of the unquantized tensors (torch, as
+    measurement harness): M1 of Y, dX and G, and M1 and M2 of the
+    reconstructed G, so that the payload's error can be read beside the
+    product's own."""
+    import torch
+
+    import synth
+    import fac_whitening_gift_amd as fg
+
+    dev = torch.device(device)
+    hidden, mlp, tokens = (int(v) for v in args.ref_shape.split(","))
+    g = torch.Generator(device=dev).manual_seed(7)
+    spec = synth.InputSpec("residual", hidden, tokens, 1.5)
+    H = synth.draw_input(spec, seed=1000, device=dev, as_bf16=True)["X"]
+    weight = torch.ones(hidden, device=dev)
+    W = torch.randn(mlp, hidden, generator=g, device=dev) * hidden ** -0.5
+    dY = (torch.randn(tokens, mlp, generator=g, device=dev)
+          * torch.randn(tokens, 1, generator=g, device=dev).exp() * 1e-3).bfloat16()
+    factor = fg.Factor(hidden, device=dev)
+    ev = lambda: torch.cuda.Event(enable_timing=True)  # noqa: E731
+    ms, marks = {}, []
+
+    def timed(name, fn):
+        fn()  # warm-up
+        a, b = ev(), ev()
+        a.record()
+        res = fn()
+        b.record()
+        marks.append((name, a, b))
+        return res
+
+    X, _, rstd = timed("norm_forward", lambda: fg.gift_norm_forward(H, weight, kind=fg.NORM_RMS))
+    fg.gift_refresh_factor(X, factor, seed=3)
+    xr, xc = timed("quantize_x", lambda: fg.gift_mx_quantize(X, by_row=True, by_col=True))
+    wr, wc = timed("quantize_w", lambda: fg.gift_mx_quantize(W, by_row=True, by_col=True))
+    Y = timed("y", lambda: fg.gift_mx_matmul(xr, wr))
+    gr, gc = timed("quantize_dy", lambda: fg.gift_mx_quantize(dY, by_row=True, by_col=True))
+    dX = timed("dx", lambda: fg.gift_mx_matmul(gr, wc))
+    G = timed("g", lambda: fg.gift_mx_matmul(gc, xc, dtype=torch.float32))
+    timed("norm_backward", lambda: fg.gift_norm_backward(dX, H, weight, None, rstd, kind=fg.NORM_RMS))
+    torch.cuda.synchronize()
+    for name, a, b in marks:
+        ms[name] = round(a.elapsed_time(b), 4)
+
+    def m1(got, want):
+        return round(float((got.double() - want).norm() / want.norm()), 5)
+
+    X64, W64, dY64 = X.double(), W.double(), dY.double()
+    G64 = dY64.T @ X64
+    out = {"study": "layer", "hidden": hidden, "mlp": mlp, "tokens": tokens, "ms": ms,
+           "m1": {"y": m1(Y, X64 @ W64.T), "dx": m1(dX, dY64 @ W64), "g": m1(G, G64)}}
+    S = kfac_metric(X)
+    num, den = m2_parts(G64, G, S)
+    out["g_m2"] = round(math.sqrt(num / den), 5)
+    for fmt, sc in (("e4m3_tensor", fg.SCALE_TENSOR), ("mxfp4", fg.SCALE_MXFP4)):
+        out[fmt] = {}
+        for method in ("gift", "euclid"):
+            L = fg.Layer(G, factor=factor if method == "gift" else None, mxfp4=sc == fg.SCALE_MXFP4)
+            fg.gift_whiten_quantize([L], scaling=sc)
+            fg.gift_dequant_unwhiten([L], scaling=sc)
+            total, own = m2_parts(G64, L.G_hat, S)[0], m2_parts(G, L.G_hat, S)
+            out[fmt][method] = {"m1_total": m1(L.G_hat, G64), "m1_payload": m1(L.G_hat, G.double()),
+                                "m2_total": round(math.sqrt(total / den), 5),
+                                "m2_payload": round(math.sqrt(own[0] / own[1]), 5)}
     return out
 
 

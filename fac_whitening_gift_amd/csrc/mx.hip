@@ -761,13 +761,12 @@ static double few_us(int64_t M, int64_t N, int64_t steps, int fn) {
   const int i = fn == 1 ? 0 : fn == 2 ? 1 : 2;
   const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const double base[2][3] = {{3.6, 3.8, 3.9}, {4.3, 4.4, 4.7}}, chain[3] = {1.65, 2.1, 2.8};
-  const double lat = (M <= 32 ? 0.65 : 1.0) * chain[i] * steps / 32;
-  // an XCD reads all of A and an eighth of B; past its 4 MB cache the rate
-  // falls (512 x 700 x 16384: 22.5 us, in 128-tiles split four ways 17.1)
-  const double held = (double)((M + N / kXcd) * steps) * (kMxPanel / kMxRows);
-  const double rate = (i ? 17e6 : 22e6) * (held > 4.5e6 ? 0.65 : 1.0);
+  const double lat = (M <= 32 ? 0.65 : 1.0) * chain[i] * steps / 32, rate = i ? 17e6 : 22e6;
   const double bytes = (double)up_div(M, kMxRows) * up_div(N, 16 * fn) * steps * ((fm + fn) * 1024 + 512);
-  return base[fm > 2][i] + (lat > bytes / rate ? lat : bytes / rate);
+  // an XCD reads all of A and an eighth of B; past its 4 MB cache loads take
+  // longer (x 700 x 16384: 256 rows 12.1 us, 512 rows 22.5)
+  const double held = (double)((M + N / kXcd) * steps) * (kMxPanel / kMxRows);
+  return base[fm > 2][i] + (lat > bytes / rate ? lat : bytes / rate) / (held > 4.5e6 ? 0.45 : 1.0);
 }
 
 static MxPlan plan_us(int64_t M, int64_t N, int64_t k, double& least) {
@@ -790,7 +789,7 @@ static MxPlan plan_us(int64_t M, int64_t N, int64_t k, double& least) {
   for (int64_t want = 1; want <= 16 && (want == 1 || want * 4 <= steps); want *= 2) {
     const int64_t per = up_div(steps, want), split = up_div(steps, per);
     const double x = tiles * split / 256.0, step = 0.25 * x > 0.21 ? 0.25 * x : 0.21;
-    offer(5 + step * per + (split > 1 ? 3 + 1.6 * split * M * N * 4 / 4e6 : 0), 128, 128, per);
+    offer(5 + step * per + (split > 1 ? 2.5 + 0.35 * split + 1.6 * split * M * N * 4 / 4e6 : 0), 128, 128, per);
   }
   const double x = up_div(M, 128) * up_div(N, 256) / 256.0;
   offer(6.5 + (x <= 1 ? 0.42 : x <= 2 ? 0.25 + 0.33 * x : 0.47 * x) * steps, 128, 256, steps);
