@@ -96,6 +96,8 @@ gift_status gift_mx_quantize(const void* X, int x_dtype, int64_t rows, int64_t c
       return fail(GIFT_ERR_INVALID_ARG, "by_col is %lld x %lld, the transposed X %lld x %lld",
                   (long long)by_col->rows, (long long)by_col->k, (long long)cols, (long long)rows);
   }
+  if (by_row && by_col && by_row->data == by_col->data)
+    return fail(GIFT_ERR_INVALID_ARG, "by_row and by_col are the same buffer");
   GIFT_TRY(check_flags(dev_flags));
   return launched(launch_mx_quantize(X, x_dtype, rows, cols, ld,
                                      by_row ? static_cast<uint8_t*>(by_row->data) : nullptr,

@@ -525,14 +525,14 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
     auto run = [&](auto VEC) {
       constexpr int kVec = decltype(VEC)::value;
       if (d > max_cols(kVec)) {
-        if (dX) {
-          if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-          else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-        }
-        if (cols) {
+        if (cols) {  // first: dX may overwrite dY
           const dim3 grid((uint32_t)((d + 255) / 256), (uint32_t)a.parts);
           if (kind == GIFT_NORM_LAYER) k_norm_cols<T, true><<<grid, dim3(256), 0, s>>>(a);
           else k_norm_cols<T, false><<<grid, dim3(256), 0, s>>>(a);
+        }
+        if (dX) {
+          if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+          else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
         }
         return;
       }

@@ -117,7 +117,7 @@ def test_forward_and_backward(rows, d, dtype, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("d", [96, 100, 4096])
+@pytest.mark.parametrize("d", [96, 100, 4096, 9001, 17000])
 def test_unaligned_and_in_place(d, kind):
     """Rows that start anywhere; Y over X, dX over dY; nothing written beside."""
     say("norm unaligned d=%d kind %d" % (d, kind))
@@ -139,7 +139,8 @@ def test_unaligned_and_in_place(d, kind):
         assert float(flat[0]) == 5.0 and float(flat[-2]) == 5.0
         _check_backward(dy, x, w, want[1], want[2], kind, (got[0], got[1], got[2]))
         D = dy.to(DEV)
-        assert torch.equal(fg.gift_norm_backward(D, X, W, want[1], want[2], kind=kind, dx=D)[0], ref[0])
+        got = fg.gift_norm_backward(D, X, W, want[1], want[2], kind=kind, dx=D)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
 def test_rows_of_one_value_and_far_means():

@@ -46,6 +46,7 @@ def test_sizes():
     (INVALID, dict(row=mx(63))), (INVALID, dict(row=mx(64, 129))), (INVALID, dict(col=mx(64, 128))),
     (INVALID, dict(row=mx(data=None))), (INVALID, dict(row=mx(data=0x40008))),
     (INVALID, dict(flags=0x50002)),
+    (INVALID, dict(rows=128, row=mx(128, 128), col=mx(128, 128))),
 ])
 def test_quantize_refuses(want, case):
     a = dict(x=X, dt=BF, rows=64, cols=128, ld=128, row=mx(), col=mx(128, 64, 0x50000), flags=None)
