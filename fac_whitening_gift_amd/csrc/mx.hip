@@ -66,7 +66,11 @@ constexpr int kQRows = 128;     // rows of a quantize tile: one k step of the op
 constexpr int kQCols = 64;      // columns: a row panel of it, half a k step of the operand by rows
 constexpr int kQThreads = 256;
 
-// One tile of X through LDS, a block of 32 per thread.  By rows: 32
+// One tile of X through LDS, a block of 32 per thread; X is read once for
+// both operands.  Bound by memory: 16384 x 4096 bf16 into both 40 us, 205 MB
+// at 5.1 TB/s (a copy: 4.9); with a row segment of 128 columns a tile 45 us
+// there and half the workgroups on small matrices (1000 x 1024: 5.8 us
+// against 4.4).  By rows: 32
 // consecutive columns of a row, threads in fragment order, so 32 lanes write
 // 512 contiguous bytes of a fragment.  By columns: 32 rows of a column.  The
 // LDS row stride is 4 banks past a multiple of 32, so the 16 rows of a
@@ -171,8 +175,9 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
   if (flags && fl) atomicOr(flags, fl);
 }
 
-// One 64 x 128 block of the operand per iteration: through LDS, then a
-// thread decodes 8 consecutive elements of a row.
+// A 64 x 128 block of the operand per workgroup: through LDS, then a thread
+// decodes 8 consecutive elements of a row.  Bound by its stores, which go
+// around the caches: 16384 x 4096 to bf16 38 -> 26 us, 170 MB at 6.5 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ A, int64_t rows,
                                                     int64_t k, int steps, T* out, int64_t ld,
@@ -253,7 +258,7 @@ struct MxGemm {
   int tm, tn;      // tiles
   int n_split;
   int mode;        // kOut*
-  bool vec;        // C takes 4-element stores
+  bool vec;        // C takes 16-byte stores (k_mx_few, k_mx_reduce: of 4 elements)
 };
 enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
 
@@ -322,11 +327,23 @@ __device__ __forceinline__ void static_for(F f) {
 // between them, the copies of step i + kStages into the stage that step i has
 // left and the reads of step i + 1's fragments into the other register set.
 // Two workgroups of 128 x 256 or three of 128 x 128 share a CU, so one's
-// results leave under the other's MFMAs.
-// The loop holds no branch: the compiler would sink the MFMAs below it, away
-// from the copies and reads they are spread among.
+// results leave under the other's MFMAs.  The loop holds no branch: the
+// compiler would sink the MFMAs below it, away from the copies and reads they
+// are spread among.
+//
+// Bound by power, then by LDS: on large products the matrix units are busy
+// 65% of the cycles (SQ counters) at the 1.6 GHz that the clock falls to, 4.3
+// to 4.9 PFLOP/s; a loop of these MFMAs alone on the same random codes, with
+// no loads, reaches 5.6 to 7.3 (9.7 on zeros).  LDS traffic decides among
+// tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
+// eight for 16.  Measured against it, 16384 x 1536 x 4096 / 16384 x 4096 x
+// 11008: 128 x 256 tiles 52.7 / 338 us (waves of 64 x 128: 53.7 / 338), two
+// waves of 128 x 128 a tile 65.7 / 348, 256 x 256 tiles, one to a CU,
+// running on from tile to tile 64 / 332, 128 x 128 tiles 55.9 / -.  Without
+// its copies or without its LDS reads that 256 x 256 loop took 85% of its
+// time, without both 75%.
 template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias>
-__global__ __launch_bounds__(64 * WR * WC, FB > 4 ? 2 : 3) void k_mx_gemm(MxGemm g) {
+__global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(MxGemm g) {
   constexpr int kWaves = WR * WC;
   constexpr int kPA = WR * FA / 4, kPB = WC * FB / 4;  // panels of the tile
   static_assert(FA % 4 == 0 && FB % 4 == 0 && kPA * 4 % kWaves == 0 && kPB * 4 % kWaves == 0, "whole panels");
@@ -526,8 +543,8 @@ __global__ __launch_bounds__(64 * WR * WC, FB > 4 ? 2 : 3) void k_mx_gemm(MxGemm
               f32x4* p4 = reinterpret_cast<f32x4*>(p);
               *p4 = *p4 + __builtin_bit_cast(f32x4, q);
             } else {
-              // around the caches: 4096^3 43.2 -> 41.5 us, 16384 x 1536 x 4096
-              // 58.4 -> 56.6 us
+              // around the caches: 4096^3 36.1 -> 34.5 us, 16384 x 11008 x
+              // 4096 448 -> 424 us
               __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, q), reinterpret_cast<nt_u4*>(p));
             }
           } else {
@@ -572,6 +589,10 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
 // in turn, straight from memory into the MFMA operands, with no LDS and no
 // barrier in the loop, and their sums are added in wave order through LDS.
 // kQuant: A is X itself (at most 16 rows), quantized into LDS first.
+// Bound by a launch and one chain of loads (1 x 4096 -> 4096 3.6 us, an empty
+// launch 2.3), by the weights' bytes (1 x 4096 -> 11008 4.4 us for 24 MB) and,
+// with many rows, by the operand bytes that every workgroup loads from the
+// second-level caches (512 x 4096 x 4096 in 16 columns 20.6 us, 347 MB).
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
@@ -875,7 +896,7 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
   auto run = [&](auto OUT, auto BIAS) {
     constexpr int kOut = decltype(OUT)::value;
     constexpr bool kBias = decltype(BIAS)::value;
-    if (p.cols == 256) k_mx_gemm<2, 2, 4, 8, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
+    if (p.cols == 256) k_mx_gemm<1, 4, 8, 4, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
     else k_mx_gemm<2, 2, 4, 4, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
   };
   const std::integral_constant<int, kOutBf16> bf16;

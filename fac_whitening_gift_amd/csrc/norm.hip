@@ -6,6 +6,11 @@
 // come from one read.  Rows too wide for that are walked again from memory
 // (k_norm_fwd_wide, k_norm_bwd_wide).  All sums are fp32, added in a fixed
 // order.
+//
+// Bound by memory: 16384 x 4096 bf16 forward 57 to 59 us (268 MB, 4.6 TB/s),
+// backward 82 us and 5 us for the sum of its 1024 partial rows (437 MB, 5.0
+// TB/s); a copy of 4 GB runs at 4.9 TB/s.  Eight-element lanes with 8 waves a
+// row, and one row at a time without fetching the next, were slower or equal.
 #include <type_traits>
 
 #include "device.hpp"
