@@ -580,21 +580,21 @@ def _matrix(t, name, device=None, shape=None, dtype=None):
     code = _DTYPES.get(t.dtype)
     if code is None or (dtype is not None and t.dtype != dtype):
         raise ValueError("%s must be %s, got %s" % (name, dtype or "bf16 or fp32", t.dtype))
-    if not t.is_cuda:
+    if device is not None:
+        if t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    elif not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     have = t.shape
     if len(have) != 2 or (shape is not None and have != shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(have),
                                                            shape or "rows x columns"))
     rows, cols = have
     if t.is_contiguous():
-        ld = cols
-    else:
-        ld, step = t.stride()
-        if (cols > 1 and step != 1) or ld < cols:
-            raise ValueError("%s must have contiguous rows" % name)
+        return t.data_ptr(), code, rows, cols, cols
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or ld < cols:
+        raise ValueError("%s must have contiguous rows" % name)
     return t.data_ptr(), code, rows, cols, ld
 
 
@@ -661,7 +661,6 @@ class MxOperand:
     __slots__ = ("rows", "k", "shape", "data", "device", "_struct", "_ref")
 
     def __init__(self, rows, k, device="cuda", data=None, like=None):
-        self.rows, self.k = self.shape = (rows, k)
         nbytes = load().gift_mx_bytes(rows, k)
         if nbytes == 0:
             raise ValueError("MXFP4 operand of %d x %d is out of range" % (rows, k))
@@ -671,6 +670,9 @@ class MxOperand:
             if data is None:
                 data = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _dev(data, torch.uint8, (nbytes,), "data")
+        self.rows = rows
+        self.k = k
+        self.shape = (rows, k)
         self.data = data
         self.device = data.device
         self._struct = _Mx(rows, k, data.data_ptr())
@@ -686,8 +688,6 @@ def _operand(op, name, device=None):
 
 
 def _quantize_target(want, rows, k, x, name):
-    if want is None or want is False:
-        return None
     if want is True:
         return MxOperand(rows, k, like=x)
     _operand(want, name, x.device)
@@ -707,10 +707,14 @@ def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
     if stream is not None:
         return _on(stream, x.device, gift_mx_quantize, x, by_row, by_col, flags)
     ptr, dt, rows, cols, ld = _matrix(x, "x")
-    row = _quantize_target(by_row, rows, cols, x, "by_row")
-    col = _quantize_target(by_col, cols, rows, x, "by_col")
-    _enqueue(x.device, load().gift_mx_quantize, ptr, dt, rows, cols, ld,
-             row._ref if row is not None else None, col._ref if col is not None else None,
+    row = col = row_ref = col_ref = None
+    if by_row:
+        row = _quantize_target(by_row, rows, cols, x, "by_row")
+        row_ref = row._ref
+    if by_col:
+        col = _quantize_target(by_col, cols, rows, x, "by_col")
+        col_ref = col._ref
+    _enqueue(x.device, load().gift_mx_quantize, ptr, dt, rows, cols, ld, row_ref, col_ref,
              None if flags is None else _flags_ptr(flags, x.device))
     return row, col
 
@@ -751,7 +755,8 @@ def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=F
         ptr, dt, _, _, ld = _matrix(out, "out", dev, (a.rows, b.rows))
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_matmul_workspace_bytes(a.rows, b.rows, a.k), dev, ws)
-    _enqueue(dev, lib.gift_mx_matmul, ra, rb, _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
+    _enqueue(dev, lib.gift_mx_matmul, ra, rb,
+             None if bias is None else _vector(bias, b.rows, "bias", dev), ptr, dt, ld,
              1 if accumulate else 0, wp, wb)
     return out
 
@@ -779,8 +784,9 @@ def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, s
         yp, ydt, _, _, ldy = _matrix(out, "out", dev, (rows, w.rows))
     lib = load()
     keep, wp, wb = _scratch(lib.gift_mx_linear_workspace_bytes(rows, w.rows, w.k), dev, ws)
-    _enqueue(dev, lib.gift_mx_linear, ptr, dt, rows, ld, rw, _vector(bias, w.rows, "bias", dev),
-             yp, ydt, ldy, _flags_ptr(flags, dev), wp, wb)
+    _enqueue(dev, lib.gift_mx_linear, ptr, dt, rows, ld, rw,
+             None if bias is None else _vector(bias, w.rows, "bias", dev), yp, ydt, ldy,
+             None if flags is None else _flags_ptr(flags, dev), wp, wb)
     return out
 
 
