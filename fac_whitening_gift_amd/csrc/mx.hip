@@ -78,7 +78,7 @@ constexpr int kQThreads = 256;
 template <class T, bool kByRow, bool kByCol>
 __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X, int64_t rows,
                                                         int64_t cols, int64_t ld, uint8_t* R,
-                                                        uint8_t* C, int col_tiles, bool vec,
+                                                        uint8_t* C, int col_tiles,
                                                         uint32_t* flags) {
   constexpr int kPer = 16 / sizeof(T);                  // elements of a 16-byte load
   constexpr int kStride = kQCols * sizeof(T) + 16;      // bytes of an LDS row
@@ -90,35 +90,38 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
   const int64_t r0 = (int64_t)tr * kQRows, c0 = (int64_t)tc * kQCols;
   // Loads go out together, from addresses clamped into X; what lies outside
   // becomes zero.
-  if (vec) {  // every 16-byte chunk lies inside X or outside
+  if (cols >= kPer) {
     uint4 v[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int e = t + i * kQThreads;
       const int64_t r = min(r0 + e / kChunks, rows - 1), c = min(c0 + e % kChunks * kPer, cols - kPer);
-      v[i] = *reinterpret_cast<const uint4*>(X + r * ld + c);
+      v[i] = ld16(X + r * ld + c);
     }
+    // the chunk that the columns end in was loaded `over` elements early
+    const int over = (int)(kPer - cols % kPer) % kPer;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int e = t + i * kQThreads, r = e / kChunks, c = e % kChunks;
-      if (r0 + r >= rows || c0 + c * kPer >= cols) v[i] = make_uint4(0, 0, 0, 0);
+      const int64_t left = cols - (c0 + c * kPer);
+      if (r0 + r >= rows || left <= 0) {
+        v[i] = make_uint4(0, 0, 0, 0);
+      } else if (left < kPer) {
+        T* to = reinterpret_cast<T*>(lds + r * kStride + c * 16);
+        T x[kPer];
+        __builtin_memcpy(x, &v[i], 16);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) to[(j - over + kPer) % kPer] = j < over ? (T)0.f : x[j];
+        continue;
+      }
       *reinterpret_cast<uint4*>(lds + r * kStride + c * 16) = v[i];
     }
   } else {
-    constexpr int kAtOnce = 16;
-    for (int e0 = t; e0 < kQRows * kQCols; e0 += kAtOnce * kQThreads) {
-      T v[kAtOnce];
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int e = e0 + i * kQThreads;
-        v[i] = X[min(r0 + e / kQCols, rows - 1) * ld + min(c0 + e % kQCols, cols - 1)];
-      }
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int e = e0 + i * kQThreads, r = e / kQCols, c = e % kQCols;
-        if (r0 + r >= rows || c0 + c >= cols) v[i] = (T)0.f;
-        *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = v[i];
-      }
+    for (int e = t; e < kQRows * kQCols; e += kQThreads) {
+      const int r = e / kQCols, c = e % kQCols;
+      T x = (T)0.f;
+      if (r0 + r < rows && c0 + c < cols) x = X[(r0 + r) * ld + c0 + c];
+      *reinterpret_cast<T*>(lds + r * kStride + c * sizeof(T)) = x;
     }
   }
   __syncthreads();
@@ -176,12 +179,14 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
 }
 
 // A 64 x 128 block of the operand per workgroup: through LDS, then a thread
-// decodes 8 consecutive elements of a row.  Bound by its stores, which go
-// around the caches: 16384 x 4096 to bf16 38 -> 26 us, 170 MB at 6.5 TB/s.
+// decodes 16 bytes of a row.  Bound by its stores, which go around the caches
+// where rows start aligned: 16384 x 4096 to bf16 38 -> 26 us, 170 MB at 6.5
+// TB/s (and through them where not: 4095 columns DQNT -> DQPLAIN us).
 template <class T>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ A, int64_t rows,
                                                     int64_t k, int steps, T* out, int64_t ld,
-                                                    bool vec) {
+                                                    bool nt) {
+  constexpr int kPer = 16 / sizeof(T), kPieces = kMxStep / kPer;  // a row of the block
   __shared__ __attribute__((aligned(16))) uint8_t lds[kMxPanel];
   const int t = threadIdx.x;
   const int64_t panel = blockIdx.x / steps;
@@ -191,25 +196,32 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
     *reinterpret_cast<uint4*>(lds + 16 * i) = *reinterpret_cast<const uint4*>(src + 16 * i);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = t + 256 * i, r = e >> 4, piece = e & 15, b = piece >> 2;
-    const int64_t row = panel * kMxRows + r, col = (int64_t)s * kMxStep + piece * 8;
+  for (int i = 0; i < kMxRows * kPieces / 256; ++i) {
+    const int e = t + 256 * i, r = e / kPieces, piece = e % kPieces, b = piece * kPer / 32;
+    const int64_t row = panel * kMxRows + r, col = (int64_t)s * kMxStep + piece * kPer;
     if (row >= rows || col >= k) continue;
     const int lane = b * 16 + (r & 15), f = r >> 4;
-    const uint32_t codes = *reinterpret_cast<const uint32_t*>(lds + f * 1024 + lane * 16 + (piece & 3) * 4);
+    const uint8_t* codes = lds + f * 1024 + lane * 16 + piece * kPer % 32 / 2;
     const uint32_t sc = lds[4096 + lane * 4 + f];
-    const float4 a = mx_decode4(codes & 0xffffu, sc), c = mx_decode4(codes >> 16, sc);
-    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    T o[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer / 4; ++j) {
+      const float4 v = mx_decode4(reinterpret_cast<const uint16_t*>(codes)[j], sc);
+      o[4 * j] = (T)v.x;
+      o[4 * j + 1] = (T)v.y;
+      o[4 * j + 2] = (T)v.z;
+      o[4 * j + 3] = (T)v.w;
+    }
     T* dst = out + row * ld + col;
-    if (vec && col + 8 <= k) {
-      T o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = (T)v[j];
-#pragma unroll
-      for (int j = 0; j < (int)sizeof(o) / 16; ++j)
-        __builtin_nontemporal_store(reinterpret_cast<const nt_u4*>(o)[j], reinterpret_cast<nt_u4*>(dst) + j);
+    uint4 w;
+    __builtin_memcpy(&w, o, 16);
+    if (col + kPer <= k) {
+      if (nt) st16_nt(dst, w);
+      else st16(dst, w);
     } else {
-      for (int j = 0; j < 8 && col + j < k; ++j) dst[j] = (T)v[j];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (col + j < k) dst[j] = o[j];
     }
   }
 }
@@ -258,7 +270,7 @@ struct MxGemm {
   int tm, tn;      // tiles
   int n_split;
   int mode;        // kOut*
-  bool vec;        // C takes 16-byte stores (k_mx_few, k_mx_reduce: of 4 elements)
+  bool nt;         // rows of C start aligned
 };
 enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
 
@@ -292,17 +304,18 @@ __device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v
   const int64_t at = (int64_t)m * g.ldc + n;
   if (g.mode == kOutBf16) {
     uint16_t* p = static_cast<uint16_t*>(g.C) + at;
-    if (whole && g.vec)
-      *reinterpret_cast<uint2*>(p) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
-                                                bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+    using any8 = unsigned __attribute__((ext_vector_type(2), aligned(2)));
+    if (whole)
+      *reinterpret_cast<any8*>(p) = any8{bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                         bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
     else
       for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = (uint16_t)bf16_bits(v[e]);
     return;
   }
   float* p = static_cast<float*>(g.C) + at;
-  if (whole && g.vec) {
-    f32x4* q = reinterpret_cast<f32x4*>(p);
-    *q = g.mode == kOutAcc ? *q + v : v;
+  if (whole) {
+    if (g.mode == kOutAcc) v += __builtin_bit_cast(f32x4, ld16(p));
+    st16(p, __builtin_bit_cast(uint4, v));
   } else {
     for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = g.mode == kOutAcc ? p[e] + v[e] : v[e];
   }
@@ -507,63 +520,56 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(
   const int sr = lane / kLanes, sc = lane % kLanes;
   T* C = static_cast<T*>(g.C) + (g.n_split > 1 ? (int64_t)split * g.M * g.N : 0) +
          (int64_t)(m0 + sr) * g.ldc + n0 + sc * kE;
-  auto put = [&](auto WHOLE) {
-    constexpr bool whole = decltype(WHOLE)::value;  // every lane's 16 bytes in or out
 #pragma unroll
-    for (int h = 0; h < FB * 16 / kCols; ++h) {
-      f32x4 bias[kCols / 16];
-      if constexpr (kBias)
+  for (int h = 0; h < FB * 16 / kCols; ++h) {
+    f32x4 bias[kCols / 16];
+    if constexpr (kBias)
 #pragma unroll
-        for (int j = 0; j < kCols / 16; ++j)
+      for (int j = 0; j < kCols / 16; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            bias[j][e] = g.bias[min(n0 + h * kCols + 16 * j + 4 * (lane >> 4) + e, g.N - 1)];
+        for (int e = 0; e < 4; ++e)
+          bias[j][e] = g.bias[min(n0 + h * kCols + 16 * j + 4 * (lane >> 4) + e, g.N - 1)];
 #pragma unroll
-      for (int i = 0; i < FA; ++i) {
+    for (int i = 0; i < FA; ++i) {
 #pragma unroll
-        for (int j = 0; j < kCols / 16; ++j) {
-          f32x4 v = acc[i][h * (kCols / 16) + j];
-          if constexpr (kBias) v += bias[j];
-          char* to = stage + (lane & 15) * kRow + (16 * j + 4 * (lane >> 4)) * kSize;
-          if constexpr (kOut == kOutBf16)
-            *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
-                                                       bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
-          else *reinterpret_cast<f32x4*>(to) = v;
-        }
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int t = 0; t < kLanes / 4; ++t) {
-          const int r = t * (64 / kLanes);
-          const int m = m0 + 16 * i + r + sr, n = n0 + h * kCols + sc * kE;
-          const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
-          if (m >= g.M || n >= g.N) continue;
-          T* p = C + (int64_t)(16 * i + r) * g.ldc + h * kCols;
-          if constexpr (whole) {
-            if constexpr (kOut == kOutAcc) {
-              f32x4* p4 = reinterpret_cast<f32x4*>(p);
-              *p4 = *p4 + __builtin_bit_cast(f32x4, q);
-            } else {
-              // around the caches: 4096^3 36.1 -> 34.5 us, 16384 x 11008 x
-              // 4096 448 -> 424 us
-              __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, q), reinterpret_cast<nt_u4*>(p));
-            }
-          } else {
-            T o[kE];
-            __builtin_memcpy(o, &q, 16);
-#pragma unroll
-            for (int e = 0; e < kE; ++e)
-              if (n + e < g.N) {
-                if constexpr (kOut == kOutAcc) p[e] += o[e];
-                else p[e] = o[e];
-              }
-          }
-        }
-        asm volatile("" ::: "memory");
+      for (int j = 0; j < kCols / 16; ++j) {
+        f32x4 v = acc[i][h * (kCols / 16) + j];
+        if constexpr (kBias) v += bias[j];
+        char* to = stage + (lane & 15) * kRow + (16 * j + 4 * (lane >> 4)) * kSize;
+        if constexpr (kOut == kOutBf16)
+          *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                     bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+        else *reinterpret_cast<f32x4*>(to) = v;
       }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < kLanes / 4; ++t) {
+        const int r = t * (64 / kLanes);
+        const int m = m0 + 16 * i + r + sr, n = n0 + h * kCols + sc * kE;
+        const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
+        if (m >= g.M || n >= g.N) continue;
+        T* p = C + (int64_t)(16 * i + r) * g.ldc + h * kCols;
+        if (n + kE <= g.N) {
+          // results around the caches where rows start aligned: 4096^3 36.1 ->
+          // 34.5 us, 16384 x 11008 x 4096 448 -> 424 us
+          if constexpr (kOut == kOutAcc)
+            st16(p, __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, ld16(p)) + __builtin_bit_cast(f32x4, q)));
+          else if (g.nt) st16_nt(p, q);
+          else st16(p, q);
+        } else {
+          T o[kE];
+          __builtin_memcpy(o, &q, 16);
+#pragma unroll
+          for (int e = 0; e < kE; ++e)
+            if (n + e < g.N) {
+              if constexpr (kOut == kOutAcc) p[e] += o[e];
+              else p[e] = o[e];
+            }
+        }
+      }
+      asm volatile("" ::: "memory");
     }
-  };
-  if (g.vec) put(std::true_type{});
-  else put(std::false_type{});
+  }
 }
 
 // C = the splits' partials, added in split order (+ bias, or to C).
@@ -574,7 +580,7 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < g.n_split; ++s) {
     const float* p = g.part + ((int64_t)s * g.M + m) * g.N + n;
-    if ((g.N & 3) == 0) v += *reinterpret_cast<const f32x4*>(p);
+    if (n + 4 <= g.N) v += __builtin_bit_cast(f32x4, ld16(p));
     else
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -602,7 +608,6 @@ struct MxFew {
   int64_t ldx;
   int64_t k;
   uint32_t* flags;
-  bool xvec;
 };
 
 template <int FM, int FN, class T, bool kQuant>
@@ -649,11 +654,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
       const int64_t k0 = (int64_t)kb * 32;
       const T* src = X + m * q.ldx + k0;
       float v[32];
-      if (q.xvec && k0 + 32 <= q.k) {
+      if (k0 + 32 <= q.k) {
         constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
         for (int j = 0; j < 32 / kPer; ++j) {
-          const uint4 c = reinterpret_cast<const uint4*>(src)[j];
+          const uint4 c = ld16(src + j * kPer);
           if constexpr (sizeof(T) == 2) {
             unpack2(c.x, v[8 * j], v[8 * j + 1]);
             unpack2(c.y, v[8 * j + 2], v[8 * j + 3]);
@@ -729,19 +734,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
 
 hipError_t done() { return hipGetLastError(); }
 
+// every row starts 16-byte aligned
+bool rows_aligned(const void* p, int64_t ld, int dtype) {
+  return (uintptr_t)p % 16 == 0 && ld * (dtype == GIFT_DTYPE_BF16 ? 2 : 4) % 16 == 0;
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
                               uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s) {
   const int ct = (int)((cols + kMxStep - 1) / kMxStep) * (kMxStep / kQCols);
   const int64_t tiles = (rows + kQRows - 1) / kQRows * ct;
-  const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
-  const bool vec = ((uintptr_t)X & 15) == 0 && ld * es % 16 == 0 && cols * es % 16 == 0;
   auto go = [&](auto zero) {
     using T = decltype(zero);
     auto run = [&](auto kernel) {
       kernel<<<dim3((uint32_t)tiles), dim3(kQThreads), 0, s>>>(static_cast<const T*>(X), rows, cols, ld,
-                                                               by_row, by_col, ct, vec, flags);
+                                                               by_row, by_col, ct, flags);
     };
     if (by_row && by_col) run(k_mx_quant<T, true, true>);
     else if (by_row) run(k_mx_quant<T, true, false>);
@@ -756,12 +764,11 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
                                 int64_t ld, hipStream_t s) {
   const int steps = (int)((k + kMxStep - 1) / kMxStep);
   const int64_t blocks = (rows + kMxRows - 1) / kMxRows * steps;
-  const size_t es = dtype == GIFT_DTYPE_BF16 ? 2 : 4;
-  const bool vec = ((uintptr_t)out & 15) == 0 && ld * es % 16 == 0;
+  const bool nt = rows_aligned(out, ld, dtype);
   if (dtype == GIFT_DTYPE_BF16)
-    k_mx_dequant<__bf16><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<__bf16*>(out), ld, vec);
+    k_mx_dequant<__bf16><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<__bf16*>(out), ld, nt);
   else
-    k_mx_dequant<float><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<float*>(out), ld, vec);
+    k_mx_dequant<float><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<float*>(out), ld, nt);
   return done();
 }
 
@@ -840,8 +847,6 @@ MxGemm gemm_args(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64
   g.N = (int)N;
   g.steps = (int)((k + kMxStep - 1) / kMxStep);
   g.mode = dtype == GIFT_DTYPE_BF16 ? kOutBf16 : accumulate ? kOutAcc : kOutF32;
-  const size_t bytes = dtype == GIFT_DTYPE_BF16 ? 8 : 16;
-  g.vec = ldc % 4 == 0 && (uintptr_t)C % bytes == 0;
   return g;
 }
 
@@ -890,8 +895,7 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
     h.mode = kOutF32;
     h.bias = nullptr;
   }
-  const size_t es = h.mode == kOutBf16 ? 2 : 4;
-  h.vec = N * es % 16 == 0 && h.ldc * es % 16 == 0 && (uintptr_t)h.C % 16 == 0;
+  h.nt = rows_aligned(h.C, h.ldc, h.mode == kOutBf16 ? GIFT_DTYPE_BF16 : GIFT_DTYPE_F32);
   const dim3 grid((uint32_t)((int64_t)g.tm * g.tn * p.n_split)), block(256);
   auto run = [&](auto OUT, auto BIAS) {
     constexpr int kOut = decltype(OUT)::value;
@@ -947,8 +951,6 @@ hipError_t launch_mx_linear_few(const void* X, int x_dtype, int64_t M, int64_t l
   q.ldx = ldx;
   q.k = k;
   q.flags = flags;
-  const size_t es = x_dtype == GIFT_DTYPE_BF16 ? 2 : 4;
-  q.xvec = ((uintptr_t)X & 15) == 0 && ldx * es % 16 == 0;
   const size_t lds = few_lds(M, k);
   auto run = [&](auto FN) {
     constexpr int fn = decltype(FN)::value;

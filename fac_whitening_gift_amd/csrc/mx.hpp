@@ -1,5 +1,5 @@
-// Launchers of mx.hip (MXFP4 operands and products) and norm.hip (layer and
-// RMS norm) for the entry points in api_layer.cpp.
+// What mx.hip (MXFP4 operands and products), norm.hip (layer and RMS norm)
+// and the entry points in api_layer.cpp share.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,6 +9,26 @@
 #include "../../include/gift.h"
 
 namespace gift {
+
+// 16-byte accesses at any element of a T array.  Rows of odd length start
+// anywhere; global memory takes wide accesses there, and the element-aligned
+// type makes the compiler emit them.
+template <class T>
+using any16 = unsigned __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+
+template <class T>
+__device__ __forceinline__ uint4 ld16(const T* p) {
+  return __builtin_bit_cast(uint4, *reinterpret_cast<const any16<T>*>(p));
+}
+template <class T>
+__device__ __forceinline__ void st16(T* p, const uint4& v) {
+  *reinterpret_cast<any16<T>*>(p) = __builtin_bit_cast(any16<T>, v);
+}
+// around the caches
+template <class T>
+__device__ __forceinline__ void st16_nt(T* p, const uint4& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(any16<T>, v), reinterpret_cast<any16<T>*>(p));
+}
 
 constexpr int kMxRows = 64;                      // rows of an operand panel
 constexpr int kMxStep = 128;                     // k elements of a step

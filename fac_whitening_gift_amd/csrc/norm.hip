@@ -1,8 +1,7 @@
 // Layer norm and RMS norm, forward and backward (gift_norm_* of
 // include/gift.h), one pass over the rows.
 //
-// A row belongs to a group of kW waves, which keep it in registers (kNV
-// vectors a lane): the mean, the variance around it and the result
+// A row belongs to kL lanes, which keep it in registers (kNV vectors each): the mean, the variance around it and the result
 // come from one read.  Rows too wide for that are walked again from memory
 // (k_norm_fwd_wide, k_norm_bwd_wide).  All sums are fp32, added in a fixed
 // order.
@@ -20,92 +19,107 @@ namespace gift {
 
 namespace {
 
-template <class T, int kVec>
-struct Vec {
-  T v[kVec];
-};
+template <class T>
+constexpr int kVecOf = 16 / sizeof(T);  // elements of a 16-byte vector
 
-template <class T, int kVec>
-__device__ __forceinline__ void ldv(const T* p, float (&o)[kVec]) {
-  if constexpr (kVec * sizeof(T) == 16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
+// 16 bytes of T as floats
+template <class T>
+__device__ __forceinline__ void unpack(const uint4& q, float (&o)[kVecOf<T>]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(T) == 2) {
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[2 * i] = __uint_as_float(w[i] << 16);
-        o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      o[2 * i] = __uint_as_float(w[i] << 16);
+      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     } else {
-      o[0] = __uint_as_float(q.x);
-      o[1] = __uint_as_float(q.y);
-      o[2] = __uint_as_float(q.z);
-      o[3] = __uint_as_float(q.w);
+      o[i] = __uint_as_float(w[i]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) o[i] = (float)p[i];
   }
 }
 
-// kNt: around the caches.  The backward pass gains by it (16384 x 4096 bf16:
-// 89.8 -> 86.7 us), the forward pass loses (57.0 -> 59.7 us).
-template <class T, int kVec, bool kNt>
-__device__ __forceinline__ void stv(T* p, const float (&v)[kVec]) {
-  Vec<T, kVec> o;
+template <class T>
+__device__ __forceinline__ uint4 pack(const float (&v)[kVecOf<T>]) {
+  struct { T v[kVecOf<T>]; } o;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) o.v[i] = (T)v[i];
-  if constexpr (kVec * sizeof(T) == 16) {
-    if constexpr (kNt) __builtin_nontemporal_store(__builtin_bit_cast(nt_u4, o), reinterpret_cast<nt_u4*>(p));
-    else *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, o);
-  } else
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) p[i] = o.v[i];
+  for (int i = 0; i < kVecOf<T>; ++i) o.v[i] = (T)v[i];
+  return __builtin_bit_cast(uint4, o);
 }
 
-template <class T, int kVec>
-__device__ __forceinline__ Vec<T, kVec> ldraw(const T* p) {
-  if constexpr (kVec * sizeof(T) == 16)
-    return __builtin_bit_cast(Vec<T, kVec>, *reinterpret_cast<const uint4*>(p));
-  Vec<T, kVec> o;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) o.v[i] = p[i];
-  return o;
-}
-
-// kVec floats of a d-vector that may be NULL (then `none`)
+// v moved down by `by` elements, `fill` behind: a row's last vector, loaded
+// so as to end with the row
 template <int kVec>
-__device__ __forceinline__ void ldw(const float* p, int at, float none, float (&o)[kVec]) {
+__device__ __forceinline__ void shift(float (&v)[kVec], int by, float fill) {
+#pragma unroll
+  for (int b = 1; b < kVec; b *= 2)
+    if (by & b) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = j + b < kVec ? v[j + b < kVec ? j + b : 0] : fill;
+    }
+}
+
+// kVec floats at `at` of a d-vector that may be NULL (then `none`)
+template <int kVec, bool kTail>
+__device__ __forceinline__ void ldw(const float* p, int at, int d, float none, float (&o)[kVec]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) o[i] = none;
     return;
   }
-  if constexpr (kVec % 4 == 0) {
+  const int from = kTail ? min(at, d - kVec) : at;
 #pragma unroll
-    for (int i = 0; i < kVec / 4; ++i) {
-      const float4 q = *reinterpret_cast<const float4*>(p + at + 4 * i);
-      o[4 * i] = q.x;
-      o[4 * i + 1] = q.y;
-      o[4 * i + 2] = q.z;
-      o[4 * i + 3] = q.w;
-    }
+  for (int i = 0; i < kVec / 4; ++i) {
+    const uint4 q = ld16(p + from + 4 * i);
+    o[4 * i] = __uint_as_float(q.x);
+    o[4 * i + 1] = __uint_as_float(q.y);
+    o[4 * i + 2] = __uint_as_float(q.z);
+    o[4 * i + 3] = __uint_as_float(q.w);
+  }
+  if (kTail && at != from) shift(o, at - from, 0.f);
+}
+
+// A lane's vector at column `at` < d of a row of Y.  kNt: around the caches.
+// The backward pass gains by it where rows start aligned (16384 x 4096 bf16:
+// 89.8 -> 86.7 us; 4095 columns: NT108 against NTPLAIN), the forward pass
+// loses (57.0 -> 59.7 us).
+template <class T, bool kNt, bool kTail>
+__device__ __forceinline__ void stv(T* row, int at, int d, const float (&v)[kVecOf<T>]) {
+  if (kTail && at + kVecOf<T> > d) {
+#pragma unroll
+    for (int i = 0; i < kVecOf<T>; ++i)
+      if (at + i < d) row[at + i] = (T)v[i];
+  } else if constexpr (kNt) {
+    st16_nt(row + at, pack<T>(v));
   } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) o[i] = p[at + i];
+    st16(row + at, pack<T>(v));
   }
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// n <= kVec elements (the wide kernels)
+template <class T>
+__device__ __forceinline__ void ldn(const T* p, int n, float (&o)[kVecOf<T>]) {
+  if (n >= kVecOf<T>) {
+    unpack<T>(ld16(p), o);
+  } else {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    for (int i = 0; i < kVecOf<T>; ++i) o[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+
+// Sum over the kL <= 64 lanes of a row (or over a wave).
+template <int kL>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = (kL < 64 ? kL : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
 
-// Sum of v over the kW waves of a row's group; buf: kW floats of the group.
-template <int kW>
+constexpr int waves_of(int kL) { return kL > 64 ? kL / 64 : 1; }
+
+// Sum of v over the kL lanes of a row; buf: one float per wave of them.
+template <int kL>
 __device__ __forceinline__ float group_sum(float v, float* buf) {
-  v = wave_sum(v);
+  constexpr int kW = waves_of(kL);
+  v = lane_sum<kL>(v);
   if constexpr (kW > 1) {
     const int w = (threadIdx.x >> 6) % kW;
     if ((threadIdx.x & 63) == 0) buf[w] = v;
@@ -129,24 +143,31 @@ struct NormFwd {
   float eps;
 };
 
-constexpr int group_threads(int kW) { return kW < 4 ? 256 : 64 * kW; }
+constexpr int group_threads(int kL) { return kL < 256 ? 256 : kL; }
 
-template <class T, int kVec, int kNV, int kW, bool kLayer>
-__global__ __launch_bounds__(group_threads(kW)) void k_norm_fwd(NormFwd a) {
-  constexpr int kGroups = group_threads(kW) / (64 * kW);
-  __shared__ float buf[2][kGroups][kW];
-  const int grp = threadIdx.x / (64 * kW), l = threadIdx.x % (64 * kW);
+// kTail: d is no multiple of the vector; the row's last vector is loaded to
+// end with the row and moved into place.
+template <class T, int kNV, int kL, bool kLayer, bool kTail>
+__global__ __launch_bounds__(group_threads(kL)) void k_norm_fwd(NormFwd a) {
+  constexpr int kVec = kVecOf<T>;
+  constexpr int kGroups = group_threads(kL) / kL;
+  __shared__ float buf[2][kGroups][waves_of(kL)];
+  const int grp = threadIdx.x / kL, l = threadIdx.x % kL;
   const int64_t row = (int64_t)blockIdx.x * kGroups + grp;
   const bool live = row < a.rows;  // a dead group still meets the barriers
   const T* x = static_cast<const T*>(a.X) + row * a.d;
   float v[kNV][kVec];
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int at = (i * 64 * kW + l) * kVec;
-    if (live && at < a.d) ldv<T, kVec>(x + at, v[i]);
-    else
+    const int at = (i * kL + l) * kVec;
+    if (live && at < a.d) {
+      const int from = kTail ? min(at, a.d - kVec) : at;
+      unpack<T>(ld16(x + from), v[i]);
+      if (kTail && at != from) shift(v[i], at - from, 0.f);
+    } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) v[i][j] = 0.f;
+    }
   }
   float mu = 0.f;
   if constexpr (kLayer) {
@@ -155,12 +176,13 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_fwd(NormFwd a) {
     for (int i = 0; i < kNV; ++i)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) s += v[i][j];
-    mu = group_sum<kW>(s, buf[0][grp]) / (float)a.d;
+    mu = group_sum<kL>(s, buf[0][grp]) / (float)a.d;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      if ((i * 64 * kW + l) * kVec < a.d)
+      const int at = (i * kL + l) * kVec;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[i][j] -= mu;
+      for (int j = 0; j < kVec; ++j)
+        if (at + (kTail ? j : 0) < a.d) v[i][j] -= mu;
     }
   }
   float q = 0.f;
@@ -168,7 +190,7 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_fwd(NormFwd a) {
   for (int i = 0; i < kNV; ++i)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
-  const float r = 1.0f / sqrtf(group_sum<kW>(q, buf[1][grp]) / (float)a.d + a.eps);
+  const float r = 1.0f / sqrtf(group_sum<kL>(q, buf[1][grp]) / (float)a.d + a.eps);
   if (!live) return;
   if (l == 0) {
     if (kLayer && a.mean) a.mean[row] = mu;
@@ -177,14 +199,14 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_fwd(NormFwd a) {
   T* y = static_cast<T*>(a.Y) + row * a.d;
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int at = (i * 64 * kW + l) * kVec;
+    const int at = (i * kL + l) * kVec;
     if (at >= a.d) continue;
     float w[kVec], b[kVec];
-    ldw<kVec>(a.weight, at, 1.f, w);
-    ldw<kVec>(a.bias, at, 0.f, b);
+    ldw<kVec, kTail>(a.weight, at, a.d, 1.f, w);
+    ldw<kVec, kTail>(a.bias, at, a.d, 0.f, b);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) v[i][j] = __builtin_fmaf(v[i][j] * r, w[j], b[j]);
-    stv<T, kVec, false>(y + at, v[i]);
+    stv<T, false, kTail>(y, at, a.d, v[i]);
   }
 }
 
@@ -192,29 +214,48 @@ constexpr int kWide = 1024;  // threads of the wide kernels, one row per workgro
 
 template <class T, bool kLayer>
 __global__ __launch_bounds__(kWide) void k_norm_fwd_wide(NormFwd a) {
+  constexpr int kVec = kVecOf<T>;
   __shared__ float buf[2][kWide / 64];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.X) + row * a.d;
   T* y = static_cast<T*>(a.Y) + row * a.d;
+  auto each = [&](auto f) {
+    for (int at = threadIdx.x * kVec; at < a.d; at += kWide * kVec) {
+      const int n = min(kVec, a.d - at);
+      float v[kVec];
+      ldn<T>(x + at, n, v);
+      f(at, n, v);
+    }
+  };
   float mu = 0.f;
   if constexpr (kLayer) {
     float s = 0.f;
-    for (int i = threadIdx.x; i < a.d; i += kWide) s += (float)x[i];
-    mu = group_sum<kWide / 64>(s, buf[0]) / (float)a.d;
+    each([&](int, int, const float (&v)[kVec]) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) s += v[j];
+    });
+    mu = group_sum<kWide>(s, buf[0]) / (float)a.d;
   }
   float q = 0.f;
-  for (int i = threadIdx.x; i < a.d; i += kWide) {
-    const float c = (float)x[i] - mu;
-    q = __builtin_fmaf(c, c, q);
-  }
-  const float r = 1.0f / sqrtf(group_sum<kWide / 64>(q, buf[1]) / (float)a.d + a.eps);
+  each([&](int, int n, const float (&v)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const float c = j < n ? v[j] - mu : 0.f;
+      q = __builtin_fmaf(c, c, q);
+    }
+  });
+  const float r = 1.0f / sqrtf(group_sum<kWide>(q, buf[1]) / (float)a.d + a.eps);
   if (threadIdx.x == 0) {
     if (kLayer && a.mean) a.mean[row] = mu;
     if (a.rstd) a.rstd[row] = r;
   }
-  for (int i = threadIdx.x; i < a.d; i += kWide)
-    y[i] = (T)__builtin_fmaf(((float)x[i] - mu) * r, a.weight ? a.weight[i] : 1.f,
-                             a.bias ? a.bias[i] : 0.f);
+  each([&](int at, int n, float (&v)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+      if (j < n)
+        v[j] = __builtin_fmaf((v[j] - mu) * r, a.weight ? a.weight[at + j] : 1.f, a.bias ? a.bias[at + j] : 0.f);
+    stv<T, false, true>(y, at, a.d, v);
+  });
 }
 
 struct NormBwd {
@@ -235,22 +276,23 @@ struct NormBwd {
 // A workgroup walks its run of rows; a group's lanes own the same columns in
 // every row, so the weight's and the bias's gradients grow in registers and
 // leave as one partial row per workgroup.
-template <class T, int kVec, int kNV, int kW, bool kLayer>
-__global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
-  constexpr int kGroups = group_threads(kW) / (64 * kW);
-  constexpr int kCols = 64 * kW * kVec * kNV;
+template <class T, int kNV, int kL, bool kLayer, bool kTail>
+__global__ __launch_bounds__(group_threads(kL)) void k_norm_bwd(NormBwd a) {
+  constexpr int kVec = kVecOf<T>;
+  constexpr int kGroups = group_threads(kL) / kL;
+  constexpr int kCols = kL * kVec * kNV;
+  constexpr int kW = waves_of(kL);
   __shared__ float buf[2][2][kGroups][kW];
-  const int grp = threadIdx.x / (64 * kW), l = threadIdx.x % (64 * kW);
+  const int grp = threadIdx.x / kL, l = threadIdx.x % kL;
   float gw[kNV][kVec], gb[kNV][kVec];
 #pragma unroll
   for (int i = 0; i < kNV; ++i)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) gw[i][j] = gb[i][j] = 0.f;
   const int64_t begin = (int64_t)blockIdx.x * a.per, end = min(a.rows, begin + a.per);
-  // Rows are fetched one ahead (not by 16 waves, whose registers that would
-  // overflow), from addresses clamped into the run and the
+  // Rows are fetched one ahead, from addresses clamped into the run and the
   // row; what lies outside counts as x = mean, dy = 0.
-  Vec<T, kVec> nx[kNV], ng[kNV];
+  uint4 nx[kNV], ng[kNV];
   float nr, nmu;
   auto fetch = [&](int64_t row) {
     row = min(row, end - 1);
@@ -258,38 +300,43 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
     const T* dy = static_cast<const T*>(a.dY) + row * a.d;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int at = min((i * 64 * kW + l) * kVec, a.d - kVec);
-      nx[i] = ldraw<T, kVec>(x + at);
-      ng[i] = ldraw<T, kVec>(dy + at);
+      const int at = min((i * kL + l) * kVec, a.d - kVec);
+      nx[i] = ld16(x + at);
+      ng[i] = ld16(dy + at);
     }
     nr = a.rstd[row];
     nmu = kLayer ? a.mean[row] : 0.f;
   };
-  constexpr bool kAhead = kW < 16;
-  if (kAhead) fetch(begin + grp);
+  fetch(begin + grp);
   int phase = 0;
   for (int64_t base = begin; base < end; base += kGroups, phase ^= 1) {
     const int64_t row = base + grp;
     const bool live = row < end;
-    if (!kAhead) fetch(row);
     const float r = live ? nr : 0.f, mu = live ? nmu : 0.f;
     float h[kNV][kVec], g[kNV][kVec];
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const bool in = live && (i * 64 * kW + l) * kVec < a.d;
+      const int at = (i * kL + l) * kVec;
+      const bool in = live && at < a.d;
+      unpack<T>(nx[i], h[i]);
+      unpack<T>(ng[i], g[i]);
+      if (kTail && in && at > a.d - kVec) {
+        shift(h[i], at - (a.d - kVec), mu);
+        shift(g[i], at - (a.d - kVec), 0.f);
+      }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        h[i][j] = in ? (float)nx[i].v[j] : mu;
-        g[i][j] = in ? (float)ng[i].v[j] : 0.f;
+        h[i][j] = in ? h[i][j] : mu;
+        g[i][j] = in ? g[i][j] : 0.f;
       }
     }
-    if (kAhead && base + kGroups < end) fetch(row + kGroups);
+    if (base + kGroups < end) fetch(row + kGroups);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int at = (i * 64 * kW + l) * kVec;
+      const int at = (i * kL + l) * kVec;
       float w[kVec];
-      if (at < a.d) ldw<kVec>(a.weight, at, 1.f, w);
+      if (at < a.d) ldw<kVec, kTail>(a.weight, at, a.d, 1.f, w);
       else
 #pragma unroll
         for (int j = 0; j < kVec; ++j) w[j] = 0.f;
@@ -306,8 +353,8 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
     if (!a.dX) continue;
     // both sums in one exchange; the two phases' buffers let the next row
     // start without another barrier
-    s2 = wave_sum(s2);
-    if constexpr (kLayer) s1 = wave_sum(s1);
+    s2 = lane_sum<kL>(s2);
+    if constexpr (kLayer) s1 = lane_sum<kL>(s1);
     if constexpr (kW > 1) {
       const int w = (threadIdx.x >> 6) % kW;
       if ((threadIdx.x & 63) == 0) {
@@ -328,11 +375,11 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
     T* dx = static_cast<T*>(a.dX) + row * a.d;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int at = (i * 64 * kW + l) * kVec;
+      const int at = (i * kL + l) * kVec;
       if (!live || at >= a.d) continue;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) g[i][j] = r * (__builtin_fmaf(-h[i][j], s2, g[i][j]) - s1);
-      stv<T, kVec, true>(dx + at, g[i]);
+      stv<T, !kTail, kTail>(dx, at, a.d, g[i]);
     }
   }
   if (!a.pw && !a.pb) return;
@@ -347,9 +394,9 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
       for (int i = 0; i < kNV; ++i)
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-          sums[grp][(i * 64 * kW + l) * kVec + j] = which ? gb[i][j] : gw[i][j];
+          sums[grp][(i * kL + l) * kVec + j] = which ? gb[i][j] : gw[i][j];
       __syncthreads();
-      for (int c = threadIdx.x; c < a.d; c += group_threads(kW)) {
+      for (int c = threadIdx.x; c < a.d; c += group_threads(kL)) {
         float v = sums[0][c];
 #pragma unroll
         for (int k = 1; k < kGroups; ++k) v += sums[k][c];
@@ -359,14 +406,14 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
   } else {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int at = (i * 64 * kW + l) * kVec;
+      const int at = (i * kL + l) * kVec;
       if (at >= a.d) continue;
-      if (a.pw)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) a.pw[(int64_t)blockIdx.x * a.d + at + j] = gw[i][j];
-      if (a.pb)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) a.pb[(int64_t)blockIdx.x * a.d + at + j] = gb[i][j];
+      for (int j = 0; j < kVec; ++j) {
+        if (kTail && at + j >= a.d) continue;
+        if (a.pw) a.pw[(int64_t)blockIdx.x * a.d + at + j] = gw[i][j];
+        if (a.pb) a.pb[(int64_t)blockIdx.x * a.d + at + j] = gb[i][j];
+      }
     }
   }
 }
@@ -375,24 +422,43 @@ __global__ __launch_bounds__(group_threads(kW)) void k_norm_bwd(NormBwd a) {
 // weight's and bias's gradients come from k_norm_cols.
 template <class T, bool kLayer>
 __global__ __launch_bounds__(kWide) void k_norm_bwd_wide(NormBwd a) {
+  constexpr int kVec = kVecOf<T>;
   __shared__ float buf[2][kWide / 64];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.X) + row * a.d;
   const T* dy = static_cast<const T*>(a.dY) + row * a.d;
   T* dx = static_cast<T*>(a.dX) + row * a.d;
   const float r = a.rstd[row], mu = kLayer ? a.mean[row] : 0.f;
+  // g and h of a vector, zeros past the row
+  auto each = [&](auto f) {
+    for (int at = threadIdx.x * kVec; at < a.d; at += kWide * kVec) {
+      const int n = min(kVec, a.d - at);
+      float h[kVec], g[kVec];
+      ldn<T>(x + at, n, h);
+      ldn<T>(dy + at, n, g);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        h[j] = j < n ? (h[j] - mu) * r : 0.f;
+        if (j < n && a.weight) g[j] *= a.weight[at + j];
+      }
+      f(at, g, h);
+    }
+  };
   float s1 = 0.f, s2 = 0.f;
-  for (int i = threadIdx.x; i < a.d; i += kWide) {
-    const float g = (float)dy[i] * (a.weight ? a.weight[i] : 1.f);
-    s2 = __builtin_fmaf(g, ((float)x[i] - mu) * r, s2);
-    if constexpr (kLayer) s1 += g;
-  }
-  s2 = group_sum<kWide / 64>(s2, buf[1]) / (float)a.d;
-  if constexpr (kLayer) s1 = group_sum<kWide / 64>(s1, buf[0]) / (float)a.d;
-  for (int i = threadIdx.x; i < a.d; i += kWide) {
-    const float g = (float)dy[i] * (a.weight ? a.weight[i] : 1.f);
-    dx[i] = (T)(r * (__builtin_fmaf(-((float)x[i] - mu) * r, s2, g) - s1));
-  }
+  each([&](int, const float (&g)[kVec], const float (&h)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      s2 = __builtin_fmaf(g[j], h[j], s2);
+      if constexpr (kLayer) s1 += g[j];
+    }
+  });
+  s2 = group_sum<kWide>(s2, buf[1]) / (float)a.d;
+  if constexpr (kLayer) s1 = group_sum<kWide>(s1, buf[0]) / (float)a.d;
+  each([&](int at, float (&g)[kVec], const float (&h)[kVec]) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) g[j] = r * (__builtin_fmaf(-h[j], s2, g[j]) - s1);
+    stv<T, false, true>(dx, at, a.d, g);
+  });
 }
 
 // Partial gradients of a run of rows, a column per thread.
@@ -437,28 +503,37 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* pw, const float*
 
 hipError_t done() { return hipGetLastError(); }
 
-// Widest row of the register form (single elements take more registers, for
-// their addresses, than 16 waves have for 16 of them).
-constexpr int max_cols(int kVec) { return 64 * 16 * (kVec > 1 ? 16 : 8); }
+constexpr int kMaxCols = 512 * 32;  // widest row of the register form
 
-// Launch the instance for a width: kW waves a row and the elements of a lane.
-// Two waves with 32 elements each serve 4096 columns best (16384 rows of bf16,
-// forward / backward: 57.0 / 89.8 us; one wave with 64: 60.8; four with 16:
-// 59.6 / 90.6; eight with 8: 66.1 / 94.4).
+// Launch the instance for a width: kL lanes a row and the elements of a lane.
+// 128 lanes with 32 elements each serve 4096 columns best (16384 rows of bf16,
+// forward / backward: 57.0 / 89.8 us; 64 with 64: 60.8; 256 with 16: 59.6 /
+// 90.6; 512 with 8: 66.1 / 94.4).
 template <int kVec, class F>
 void by_width(int64_t d, F f) {
-  auto go = [&](auto W, auto E) { f(W, std::integral_constant<int, decltype(E)::value / kVec>{}); };
-  const std::integral_constant<int, 1> w1;
-  const std::integral_constant<int, 2> w2;
-  const std::integral_constant<int, 8> w8, e8;
-  const std::integral_constant<int, 16> w16, e16;
-  const std::integral_constant<int, 32> e32;
-  if (d <= 512) go(w1, e8);
-  else if (d <= 1024) go(w1, e16);
-  else if (d <= 2048) go(w2, e16);
-  else if (d <= 4096) go(w2, e32);
-  else if (d <= 8192) go(w8, e16);
-  else go(w16, std::integral_constant<int, max_cols(kVec) / 1024>{});
+  auto go = [&](auto L, auto E) {
+    const std::integral_constant<int, decltype(E)::value / kVec> nv;
+    if (d % kVec) f(L, nv, std::true_type{});
+    else f(L, nv, std::false_type{});
+  };
+  const std::integral_constant<int, 16> l16, e16;
+  const std::integral_constant<int, 32> l32, e32;
+  const std::integral_constant<int, 64> l64;
+  const std::integral_constant<int, 128> l128;
+  const std::integral_constant<int, 256> l256;
+  const std::integral_constant<int, 512> l512;
+  const std::integral_constant<int, 8> e8;
+  const std::integral_constant<int, 24> e24;
+  if (d <= 16 * 8) go(l16, e8);
+  else if (d <= 32 * 8) go(l32, e8);
+  else if (d <= 64 * 8) go(l64, e8);
+  else if (d <= 64 * 16) go(l64, e16);
+  else if (d <= 128 * 16) go(l128, e16);
+  else if (d <= 128 * 32) go(l128, e32);
+  else if (d <= 256 * 24) go(l256, e24);
+  else if (d <= 256 * 32) go(l256, e32);
+  else if (d <= 512 * 24) go(l512, e24);
+  else go(l512, e32);
 }
 
 constexpr int kNormParts = 1024;  // most partial rows of the weight's gradient
@@ -477,25 +552,19 @@ hipError_t launch_norm_forward(const void* X, int dtype, int64_t rows, int64_t d
   NormFwd a{X, Y, weight, bias, mean, rstd, rows, (int)d, eps};
   auto typed = [&](auto zero) {
     using T = decltype(zero);
-    constexpr int kFull = 16 / sizeof(T);
-    const bool vec = d % kFull == 0 && (((uintptr_t)X | (uintptr_t)Y | (uintptr_t)weight | (uintptr_t)bias) & 15) == 0;
-    auto run = [&](auto VEC) {
-      constexpr int kVec = decltype(VEC)::value;
-      if (d > max_cols(kVec)) {
-        if (kind == GIFT_NORM_LAYER) k_norm_fwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-        else k_norm_fwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-        return;
-      }
-      by_width<kVec>(d, [&](auto W, auto NV) {
-        constexpr int kW = decltype(W)::value, kNV = decltype(NV)::value;
-        constexpr int kGroups = group_threads(kW) / (64 * kW);
-        const dim3 grid((uint32_t)((rows + kGroups - 1) / kGroups)), block(group_threads(kW));
-        if (kind == GIFT_NORM_LAYER) k_norm_fwd<T, kVec, kNV, kW, true><<<grid, block, 0, s>>>(a);
-        else k_norm_fwd<T, kVec, kNV, kW, false><<<grid, block, 0, s>>>(a);
-      });
-    };
-    if (vec) run(std::integral_constant<int, kFull>{});
-    else run(std::integral_constant<int, 1>{});
+    if (d > kMaxCols || d < kVecOf<T>) {
+      if (kind == GIFT_NORM_LAYER) k_norm_fwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+      else k_norm_fwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+      return;
+    }
+    by_width<kVecOf<T>>(d, [&](auto L, auto NV, auto TAIL) {
+      constexpr int kL = decltype(L)::value, kNV = decltype(NV)::value;
+      constexpr bool kTail = decltype(TAIL)::value;
+      constexpr int kGroups = group_threads(kL) / kL;
+      const dim3 grid((uint32_t)((rows + kGroups - 1) / kGroups)), block(group_threads(kL));
+      if (kind == GIFT_NORM_LAYER) k_norm_fwd<T, kNV, kL, true, kTail><<<grid, block, 0, s>>>(a);
+      else k_norm_fwd<T, kNV, kL, false, kTail><<<grid, block, 0, s>>>(a);
+    });
   };
   if (dtype == GIFT_DTYPE_BF16) typed((__bf16)0.f);
   else typed(0.f);
@@ -525,31 +594,25 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
   if (dbias) a.pb = static_cast<float*>(ws) + (size_t)most * d;
   auto typed = [&](auto zero) {
     using T = decltype(zero);
-    constexpr int kFull = 16 / sizeof(T);
-    const bool vec = d % kFull == 0 && (((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX | (uintptr_t)weight) & 15) == 0;
-    auto run = [&](auto VEC) {
-      constexpr int kVec = decltype(VEC)::value;
-      if (d > max_cols(kVec)) {
-        if (cols) {  // first: dX may overwrite dY
-          const dim3 grid((uint32_t)((d + 255) / 256), (uint32_t)a.parts);
-          if (kind == GIFT_NORM_LAYER) k_norm_cols<T, true><<<grid, dim3(256), 0, s>>>(a);
-          else k_norm_cols<T, false><<<grid, dim3(256), 0, s>>>(a);
-        }
-        if (dX) {
-          if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-          else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-        }
-        return;
+    if (d > kMaxCols || d < kVecOf<T>) {
+      if (cols) {  // first: dX may overwrite dY
+        const dim3 grid((uint32_t)((d + 255) / 256), (uint32_t)a.parts);
+        if (kind == GIFT_NORM_LAYER) k_norm_cols<T, true><<<grid, dim3(256), 0, s>>>(a);
+        else k_norm_cols<T, false><<<grid, dim3(256), 0, s>>>(a);
       }
-      by_width<kVec>(d, [&](auto W, auto NV) {
-        constexpr int kW = decltype(W)::value, kNV = decltype(NV)::value;
-        const dim3 grid((uint32_t)a.parts), block(group_threads(kW));
-        if (kind == GIFT_NORM_LAYER) k_norm_bwd<T, kVec, kNV, kW, true><<<grid, block, 0, s>>>(a);
-        else k_norm_bwd<T, kVec, kNV, kW, false><<<grid, block, 0, s>>>(a);
-      });
-    };
-    if (vec) run(std::integral_constant<int, kFull>{});
-    else run(std::integral_constant<int, 1>{});
+      if (dX) {
+        if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+        else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+      }
+      return;
+    }
+    by_width<kVecOf<T>>(d, [&](auto L, auto NV, auto TAIL) {
+      constexpr int kL = decltype(L)::value, kNV = decltype(NV)::value;
+      constexpr bool kTail = decltype(TAIL)::value;
+      const dim3 grid((uint32_t)a.parts), block(group_threads(kL));
+      if (kind == GIFT_NORM_LAYER) k_norm_bwd<T, kNV, kL, true, kTail><<<grid, block, 0, s>>>(a);
+      else k_norm_bwd<T, kNV, kL, false, kTail><<<grid, block, 0, s>>>(a);
+    });
   };
   if (dtype == GIFT_DTYPE_BF16) typed((__bf16)0.f);
   else typed(0.f);
