@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
 // A 64 x 128 block of the operand per workgroup: through LDS, then a thread
 // decodes 16 bytes of a row.  Bound by its stores, which go around the caches
 // where rows start aligned: 16384 x 4096 to bf16 38 -> 26 us, 170 MB at 6.5
-// TB/s (and through them where not: 4095 columns DQNT -> DQPLAIN us).
+// TB/s (and through them where not: 4095 columns 63 -> 36 us).
 template <class T>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ A, int64_t rows,
                                                     int64_t k, int steps, T* out, int64_t ld,

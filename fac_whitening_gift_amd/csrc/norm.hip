@@ -7,9 +7,8 @@
 // order.
 //
 // Bound by memory: 16384 x 4096 bf16 forward 57 to 59 us (268 MB, 4.6 TB/s),
-// backward 82 us and 5 us for the sum of its 1024 partial rows (437 MB, 5.0
-// TB/s); a copy of 4 GB runs at 4.9 TB/s.  Eight-element lanes with 8 waves a
-// row, and one row at a time without fetching the next, were slower or equal.
+// backward 82 us with the sum of its 512 partial rows (436 MB with them, 5.3
+// TB/s); a copy of 4 GB runs at 4.9 TB/s.
 #include <type_traits>
 
 #include "device.hpp"
@@ -79,7 +78,7 @@ __device__ __forceinline__ void ldw(const float* p, int at, int d, float none, f
 
 // A lane's vector at column `at` < d of a row of Y.  kNt: around the caches.
 // The backward pass gains by it where rows start aligned (16384 x 4096 bf16:
-// 89.8 -> 86.7 us; 4095 columns: NT108 against NTPLAIN), the forward pass
+// 89.8 -> 86.7 us), the forward pass
 // loses (57.0 -> 59.7 us).
 template <class T, bool kNt, bool kTail>
 __device__ __forceinline__ void stv(T* row, int at, int d, const float (&v)[kVecOf<T>]) {
@@ -536,12 +535,13 @@ void by_width(int64_t d, F f) {
   else go(l512, e32);
 }
 
-constexpr int kNormParts = 1024;  // most partial rows of the weight's gradient
-
-int norm_parts(int64_t rows) {
-  // at least 4 rows a workgroup
-  const int64_t p = (rows + 3) / 4;
-  return (int)(p < kNormParts ? p : kNormParts);
+// Workgroups of the backward pass, each leaving one partial row of the
+// weight's gradient: at least 4 rows each, and about as many as are resident
+// (16384 rows of bf16, 256 / 512 / 1024 of them: 300 columns 28.0 / 19.9 /
+// 18.0 us, 4096 columns 104.8 / 82.3 / 91.7, 9000 columns 236 / 251 / 282).
+int norm_parts(int64_t rows, int64_t d) {
+  const int64_t p = (rows + 3) / 4, most = d <= 512 ? 1024 : d <= 8192 ? 512 : 256;
+  return (int)(p < most ? p : most);
 }
 
 }  // namespace
@@ -571,7 +571,7 @@ hipError_t launch_norm_forward(const void* X, int dtype, int64_t rows, int64_t d
   return done();
 }
 
-size_t norm_backward_ws(int64_t rows, int64_t d) { return (size_t)norm_parts(rows) * d * 2 * sizeof(float); }
+size_t norm_backward_ws(int64_t rows, int64_t d) { return (size_t)norm_parts(rows, d) * d * 2 * sizeof(float); }
 
 hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_t rows, int64_t d,
                                 int kind, const float* weight, const float* mean, const float* rstd,
@@ -586,7 +586,7 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
   a.rstd = rstd;
   a.rows = rows;
   a.d = (int)d;
-  const int most = norm_parts(rows);
+  const int most = norm_parts(rows, d);
   a.per = (rows + most - 1) / most;
   a.parts = (int)((rows + a.per - 1) / a.per);
   const bool cols = dweight || dbias;
