@@ -182,10 +182,9 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
 // decodes 16 bytes of a row.  Bound by its stores, which go around the caches
 // where rows start aligned: 16384 x 4096 to bf16 38 -> 26 us, 170 MB at 6.5
 // TB/s (and through them where not: 4095 columns 63 -> 36 us).
-template <class T>
+template <class T, bool kNt>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ A, int64_t rows,
-                                                    int64_t k, int steps, T* out, int64_t ld,
-                                                    bool nt) {
+                                                    int64_t k, int steps, T* out, int64_t ld) {
   constexpr int kPer = 16 / sizeof(T), kPieces = kMxStep / kPer;  // a row of the block
   __shared__ __attribute__((aligned(16))) uint8_t lds[kMxPanel];
   const int t = threadIdx.x;
@@ -216,7 +215,7 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
     uint4 w;
     __builtin_memcpy(&w, o, 16);
     if (col + kPer <= k) {
-      if (nt) st16_nt(dst, w);
+      if constexpr (kNt) st16_nt(dst, w);
       else st16(dst, w);
     } else {
 #pragma unroll
@@ -270,7 +269,6 @@ struct MxGemm {
   int tm, tn;      // tiles
   int n_split;
   int mode;        // kOut*
-  bool nt;         // rows of C start aligned
 };
 enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
 
@@ -355,7 +353,7 @@ __device__ __forceinline__ void static_for(F f) {
 // running on from tile to tile 64 / 332, 128 x 128 tiles 55.9 / -.  Without
 // its copies or without its LDS reads that 256 x 256 loop took 85% of its
 // time, without both 75%.
-template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias>
+template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias, bool kNt>
 __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(MxGemm g) {
   constexpr int kWaves = WR * WC;
   constexpr int kPA = WR * FA / 4, kPB = WC * FB / 4;  // panels of the tile
@@ -554,7 +552,7 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(
           // 34.5 us, 16384 x 11008 x 4096 448 -> 424 us
           if constexpr (kOut == kOutAcc)
             st16(p, __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, ld16(p)) + __builtin_bit_cast(f32x4, q)));
-          else if (g.nt) st16_nt(p, q);
+              else if constexpr (kNt) st16_nt(p, q);
           else st16(p, q);
         } else {
           T o[kE];
@@ -734,9 +732,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
 
 hipError_t done() { return hipGetLastError(); }
 
-// every row starts 16-byte aligned
+// every row starts with a 128-byte line: whole lines can go around the caches
+// (9000 columns of bf16, 16-byte aligned: dequantize 124 us around, 88 through)
 bool rows_aligned(const void* p, int64_t ld, int dtype) {
-  return (uintptr_t)p % 16 == 0 && ld * (dtype == GIFT_DTYPE_BF16 ? 2 : 4) % 16 == 0;
+  return (uintptr_t)p % 128 == 0 && ld * (dtype == GIFT_DTYPE_BF16 ? 2 : 4) % 128 == 0;
 }
 
 }  // namespace
@@ -764,11 +763,17 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
                                 int64_t ld, hipStream_t s) {
   const int steps = (int)((k + kMxStep - 1) / kMxStep);
   const int64_t blocks = (rows + kMxRows - 1) / kMxRows * steps;
-  const bool nt = rows_aligned(out, ld, dtype);
-  if (dtype == GIFT_DTYPE_BF16)
-    k_mx_dequant<__bf16><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<__bf16*>(out), ld, nt);
-  else
-    k_mx_dequant<float><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(A, rows, k, steps, static_cast<float*>(out), ld, nt);
+  auto run = [&](auto zero, auto NT) {
+    using T = decltype(zero);
+    k_mx_dequant<T, decltype(NT)::value><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
+        A, rows, k, steps, static_cast<T*>(out), ld);
+  };
+  auto typed = [&](auto zero) {
+    if (rows_aligned(out, ld, dtype)) run(zero, std::true_type{});
+    else run(zero, std::false_type{});
+  };
+  if (dtype == GIFT_DTYPE_BF16) typed((__bf16)0.f);
+  else typed(0.f);
   return done();
 }
 
@@ -895,19 +900,24 @@ hipError_t launch_mx_matmul(const uint8_t* A, const uint8_t* B, int64_t M, int64
     h.mode = kOutF32;
     h.bias = nullptr;
   }
-  h.nt = rows_aligned(h.C, h.ldc, h.mode == kOutBf16 ? GIFT_DTYPE_BF16 : GIFT_DTYPE_F32);
   const dim3 grid((uint32_t)((int64_t)g.tm * g.tn * p.n_split)), block(256);
-  auto run = [&](auto OUT, auto BIAS) {
+  auto run = [&](auto OUT, auto BIAS, auto NT) {
     constexpr int kOut = decltype(OUT)::value;
-    constexpr bool kBias = decltype(BIAS)::value;
-    if (p.cols == 256) k_mx_gemm<1, 4, 8, 4, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
-    else k_mx_gemm<2, 2, 4, 4, 3, kOut, kBias><<<grid, block, 0, s>>>(h);
+    constexpr bool kBias = decltype(BIAS)::value, kNt = decltype(NT)::value;
+    if (p.cols == 256) k_mx_gemm<1, 4, 8, 4, 3, kOut, kBias, kNt><<<grid, block, 0, s>>>(h);
+    else k_mx_gemm<2, 2, 4, 4, 3, kOut, kBias, kNt><<<grid, block, 0, s>>>(h);
   };
-  const std::integral_constant<int, kOutBf16> bf16;
-  const std::integral_constant<int, kOutF32> f32;
-  if (h.mode == kOutAcc) run(std::integral_constant<int, kOutAcc>{}, std::false_type{});
-  else if (h.bias) h.mode == kOutBf16 ? run(bf16, std::true_type{}) : run(f32, std::true_type{});
-  else h.mode == kOutBf16 ? run(bf16, std::false_type{}) : run(f32, std::false_type{});
+  auto biased = [&](auto OUT, auto NT) {
+    if (h.bias) run(OUT, std::true_type{}, NT);
+    else run(OUT, std::false_type{}, NT);
+  };
+  auto typed = [&](auto OUT) {
+    if (rows_aligned(h.C, h.ldc, h.mode == kOutBf16 ? GIFT_DTYPE_BF16 : GIFT_DTYPE_F32)) biased(OUT, std::true_type{});
+    else biased(OUT, std::false_type{});
+  };
+  if (h.mode == kOutAcc) run(std::integral_constant<int, kOutAcc>{}, std::false_type{}, std::false_type{});
+  else if (h.mode == kOutBf16) typed(std::integral_constant<int, kOutBf16>{});
+  else typed(std::integral_constant<int, kOutF32>{});
   hipError_t e = done();
   if (e != hipSuccess || p.n_split == 1) return e;
   k_mx_reduce<<<dim3((uint32_t)((M * ((N + 3) / 4) + 255) / 256)), dim3(256), 0, s>>>(g);
