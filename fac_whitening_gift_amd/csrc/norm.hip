@@ -1,8 +1,9 @@
 // Layer norm and RMS norm, forward and backward (gift_norm_* of
 // include/gift.h), one pass over the rows.
 //
-// A row belongs to kL lanes, which keep it in registers (kNV vectors each): the mean, the variance around it and the result
-// come from one read.  Rows too wide for that are walked again from memory
+// A row belongs to kL lanes, which keep it in registers (kNV vectors each):
+// the mean, the variance around it and the result come from one read.  Rows
+// too wide for that (or shorter than a vector) are walked again from memory
 // (k_norm_fwd_wide, k_norm_bwd_wide).  All sums are fp32, added in a fixed
 // order.
 //
@@ -77,9 +78,8 @@ __device__ __forceinline__ void ldw(const float* p, int at, int d, float none, f
 }
 
 // A lane's vector at column `at` < d of a row of Y.  kNt: around the caches.
-// The backward pass gains by it where rows start aligned (16384 x 4096 bf16:
-// 89.8 -> 86.7 us), the forward pass
-// loses (57.0 -> 59.7 us).
+// The backward pass gains by it in whole vectors (16384 x 4096 bf16: 89.5 ->
+// 81.5 us), the forward pass loses (57.0 -> 59.7 us).
 template <class T, bool kNt, bool kTail>
 __device__ __forceinline__ void stv(T* row, int at, int d, const float (&v)[kVecOf<T>]) {
   if (kTail && at + kVecOf<T> > d) {

@@ -391,7 +391,10 @@ size_t gift_group_workspace_bytes(int op, const gift_layer *layers,
  * Y = X W^T, dX = dY W and the weight gradient G = dY^T X (what
  * gift_whiten_quantize takes), each operand quantized to MXFP4 along the
  * axis its product sums over, with the scale and rounding rules of
- * GIFT_SCALE_MXFP4 above.
+ * GIFT_SCALE_MXFP4 above.  Matrices are row-major; where an entry point
+ * takes a leading dimension their rows may lie apart, and they need only the
+ * alignment of their elements.  What a call writes must not overlap what it
+ * reads, except where the entry point says so.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -423,8 +426,7 @@ size_t gift_mx_bytes(int64_t rows, int64_t k);
  * gift_mx_quantize -- quantize X (rows x cols, x_dtype, element (i, j) at
  * i * ld + j, ld >= cols) in one read: along its rows into *by_row
  * (rows x cols) and/or along its columns into *by_col (cols x rows, the
- * operand of X^T).  Either may be NULL, not both.  X needs only its element
- * alignment; rows that start 16-byte aligned are read faster.  Per block of
+ * operand of X^T).  Either may be NULL, not both.  Per block of
  * 32 as in GIFT_SCALE_MXFP4: the result is what gift_euclid_fp8_roundtrip
  * gives for the same values; a block cut short by the matrix's edge is
  * quantized as if filled with zeros.  dev_flags (optional, 4-byte aligned):
@@ -476,10 +478,11 @@ size_t gift_mx_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k);
  *   LAYER: mu = mean(x), r = (mean((x - mu)^2) + eps)^-1/2, h = (x - mu) r
  *   RMS:   r = (mean(x^2) + eps)^-1/2,                      h = x r
  *   y = h * weight + bias
- * weight, bias: d fp32 (NULL: 1 and 0).  Y has X's type; mean (LAYER) and
- * rstd, fp32, one per row, may be NULL.  Statistics are fp32, the variance
- * in a second pass over the centred values.  X and Y may be the same
- * buffer.  X, Y, dY and dX need their element alignment only.
+ * weight, bias: d fp32 (NULL: 1 and 0).  Y has X's type; mean (LAYER only)
+ * and rstd, fp32, one per row, may be NULL.  Statistics are fp32, the
+ * variance in a second pass over the centred values; a row whose squares
+ * overflow fp32 gets r = 0.  X and Y may be the same buffer.  X, Y, dY and dX
+ * need their element alignment only.
  */
 enum { GIFT_NORM_LAYER = 0, GIFT_NORM_RMS = 1 };
 gift_status gift_norm_forward(const void *X, int x_dtype, int64_t rows, int64_t d, int kind,
