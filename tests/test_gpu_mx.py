@@ -208,7 +208,8 @@ def test_matmul_into_a_slice(m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 @pytest.mark.parametrize("m,n,k", [(1, 40, 64), (1, 1000, 4096), (5, 129, 1000), (16, 64, 2048), (16, 32, 8192),
-                                   (24, 100, 600), (70, 90, 260), (2, 9000, 300), (16, 5000, 513)])
+                                   (24, 100, 600), (70, 90, 260), (2, 9000, 300), (16, 5000, 513),
+                                   (1, 40, 180000), (2, 24, 90001)])
 def test_linear(m, n, k, dtype):
     say("mx linear %dx%dx%d %s" % (m, n, k, dtype))
     x, w = _draw(m, k, m + n, dtype, 3), _draw(n, k, k, torch.float32, 3)
@@ -311,3 +312,41 @@ def test_side_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0] * 2) and torch.equal(got[1], want[1])
     assert torch.equal(got[2], want[2] * 2)
+
+
+def _rows_near(c, a, b, rows, half_step):
+    """Rows of c against fp64 products of the decoded rows of a and all of b."""
+    va = fg.gift_mx_dequantize(fg.gift_mx_quantize(a[rows].contiguous(), by_row=True)[0]).double()
+    vb = fg.gift_mx_dequantize(fg.gift_mx_quantize(b, by_row=True)[0]).double()
+    want, tol = va @ vb.t(), 2 * a.shape[1] * 2.0 ** -23 * (va.abs() @ vb.abs().t())
+    return bool(((c[rows].double() - want).abs() <= tol + half_step * (want.abs() + tol)).all())
+
+
+def test_offsets_past_32_bits():
+    """An X of 4.9 G elements and its operands of 2.6 GB, and a C of 4.9 G
+    elements: rows at both ends and in the middle."""
+    say("mx large offsets")
+    rows, cols = 40000, 122000
+    x = torch.empty(rows, cols, dtype=BF16, device=DEV).normal_()
+    r, c = fg.gift_mx_quantize(x, by_row=True, by_col=True)
+    assert r.data.numel() > 2 ** 31 and c.data.numel() > 2 ** 31
+    pick = torch.tensor([0, 1, rows // 2, rows - 65, rows - 1], device=DEV)
+    back = fg.gift_mx_dequantize(r, dtype=BF16)
+    few, _ = fg.gift_mx_quantize(x[pick].contiguous(), by_row=True)
+    assert torch.equal(back[pick], fg.gift_mx_dequantize(few, dtype=BF16))
+    del back
+    back = fg.gift_mx_dequantize(c, dtype=BF16)
+    edge = x[:, cols - 200:].t().contiguous()
+    last, _ = fg.gift_mx_quantize(edge, by_row=True)
+    assert torch.equal(back[cols - 200:], fg.gift_mx_dequantize(last, dtype=BF16))
+    del back, c
+    for n in (16, 700):   # small products, and tiles
+        w = torch.randn(n, cols, device=DEV)
+        wr, _ = fg.gift_mx_quantize(w, by_row=True)
+        y = fg.gift_mx_matmul(r, wr, dtype=torch.float32)
+        assert _rows_near(y, x, w, pick, 0.0)
+    del x, r, y
+    a, b = torch.randn(70000, 96, device=DEV), torch.randn(70001, 96, device=DEV)
+    ra, rb = (fg.gift_mx_quantize(t, by_row=True)[0] for t in (a, b))
+    out = fg.gift_mx_matmul(ra, rb)
+    assert _rows_near(out, a, b, torch.tensor([0, 35000, 69999], device=DEV), 2.0 ** -8)

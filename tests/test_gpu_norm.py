@@ -201,3 +201,24 @@ def test_refuses():
         fg.gift_norm_backward(x, x, None, None, x[:, 0].contiguous(), accumulate=True)
     with pytest.raises(fg.GiftError):
         fg.gift_norm_backward(x, x, None, None, x[:, 0].contiguous())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_offsets_past_32_bits(kind):
+    """2.4 G elements: the first and last rows equal those rows alone, and the
+    gradients of the weight count every row."""
+    say("norm large offsets kind %d" % kind)
+    rows, d = 600001, 4096
+    x = torch.empty(rows, d, dtype=torch.bfloat16, device=DEV).normal_()
+    w = torch.ones(d, device=DEV)
+    y, mean, rstd = fg.gift_norm_forward(x, w, kind=kind)
+    pick = torch.tensor([0, rows // 2, rows - 1], device=DEV)
+    alone = fg.gift_norm_forward(x[pick].contiguous(), w, kind=kind)
+    assert torch.equal(y[pick], alone[0]) and torch.equal(rstd[pick], alone[2])
+    # dY = 1: d bias is the number of rows, exactly; dX in place of dY
+    dy = y.fill_(1.0)
+    m = None if mean is None else mean[pick].contiguous()
+    part = fg.gift_norm_backward(dy[pick].contiguous(), x[pick].contiguous(), w, m, rstd[pick].contiguous(),
+                                 kind=kind)
+    dx, dw, db = fg.gift_norm_backward(dy, x, w, mean, rstd, kind=kind, dx=dy, dbias=torch.empty(d, device=DEV))
+    assert torch.equal(dx[pick], part[0]) and bool((db == rows).all()) and bool(torch.isfinite(dw).all())
