@@ -209,17 +209,20 @@ __global__ __launch_bounds__(group_threads(kL)) void k_norm_fwd(NormFwd a) {
   }
 }
 
-constexpr int kWide = 1024;  // threads of the wide kernels, one row per workgroup
+// Threads of the wide kernels, one row per workgroup: rows of many vectors,
+// and rows shorter than one, which may be 2^24 (a grid holds fewer than 2^32
+// threads).
+constexpr int kWide = 1024, kThin = 64;
 
-template <class T, bool kLayer>
-__global__ __launch_bounds__(kWide) void k_norm_fwd_wide(NormFwd a) {
+template <class T, bool kLayer, int kThreads>
+__global__ __launch_bounds__(kThreads) void k_norm_fwd_wide(NormFwd a) {
   constexpr int kVec = kVecOf<T>;
-  __shared__ float buf[2][kWide / 64];
+  __shared__ float buf[2][kThreads / 64];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.X) + row * a.d;
   T* y = static_cast<T*>(a.Y) + row * a.d;
   auto each = [&](auto f) {
-    for (int at = threadIdx.x * kVec; at < a.d; at += kWide * kVec) {
+    for (int at = threadIdx.x * kVec; at < a.d; at += kThreads * kVec) {
       const int n = min(kVec, a.d - at);
       float v[kVec];
       ldn<T>(x + at, n, v);
@@ -233,7 +236,7 @@ __global__ __launch_bounds__(kWide) void k_norm_fwd_wide(NormFwd a) {
 #pragma unroll
       for (int j = 0; j < kVec; ++j) s += v[j];
     });
-    mu = group_sum<kWide>(s, buf[0]) / (float)a.d;
+    mu = group_sum<kThreads>(s, buf[0]) / (float)a.d;
   }
   float q = 0.f;
   each([&](int, int n, const float (&v)[kVec]) {
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(kWide) void k_norm_fwd_wide(NormFwd a) {
       q = __builtin_fmaf(c, c, q);
     }
   });
-  const float r = 1.0f / sqrtf(group_sum<kWide>(q, buf[1]) / (float)a.d + a.eps);
+  const float r = 1.0f / sqrtf(group_sum<kThreads>(q, buf[1]) / (float)a.d + a.eps);
   if (threadIdx.x == 0) {
     if (kLayer && a.mean) a.mean[row] = mu;
     if (a.rstd) a.rstd[row] = r;
@@ -419,10 +422,10 @@ __global__ __launch_bounds__(group_threads(kL)) void k_norm_bwd(NormBwd a) {
 
 // Rows wider than the register form: dX only, a row per workgroup; the
 // weight's and bias's gradients come from k_norm_cols.
-template <class T, bool kLayer>
-__global__ __launch_bounds__(kWide) void k_norm_bwd_wide(NormBwd a) {
+template <class T, bool kLayer, int kThreads>
+__global__ __launch_bounds__(kThreads) void k_norm_bwd_wide(NormBwd a) {
   constexpr int kVec = kVecOf<T>;
-  __shared__ float buf[2][kWide / 64];
+  __shared__ float buf[2][kThreads / 64];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(a.X) + row * a.d;
   const T* dy = static_cast<const T*>(a.dY) + row * a.d;
@@ -430,7 +433,7 @@ __global__ __launch_bounds__(kWide) void k_norm_bwd_wide(NormBwd a) {
   const float r = a.rstd[row], mu = kLayer ? a.mean[row] : 0.f;
   // g and h of a vector, zeros past the row
   auto each = [&](auto f) {
-    for (int at = threadIdx.x * kVec; at < a.d; at += kWide * kVec) {
+    for (int at = threadIdx.x * kVec; at < a.d; at += kThreads * kVec) {
       const int n = min(kVec, a.d - at);
       float h[kVec], g[kVec];
       ldn<T>(x + at, n, h);
@@ -451,8 +454,8 @@ __global__ __launch_bounds__(kWide) void k_norm_bwd_wide(NormBwd a) {
       if constexpr (kLayer) s1 += g[j];
     }
   });
-  s2 = group_sum<kWide>(s2, buf[1]) / (float)a.d;
-  if constexpr (kLayer) s1 = group_sum<kWide>(s1, buf[0]) / (float)a.d;
+  s2 = group_sum<kThreads>(s2, buf[1]) / (float)a.d;
+  if constexpr (kLayer) s1 = group_sum<kThreads>(s1, buf[0]) / (float)a.d;
   each([&](int at, float (&g)[kVec], const float (&h)[kVec]) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) g[j] = r * (__builtin_fmaf(-h[j], s2, g[j]) - s1);
@@ -553,8 +556,14 @@ hipError_t launch_norm_forward(const void* X, int dtype, int64_t rows, int64_t d
   auto typed = [&](auto zero) {
     using T = decltype(zero);
     if (d > kMaxCols || d < kVecOf<T>) {
-      if (kind == GIFT_NORM_LAYER) k_norm_fwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-      else k_norm_fwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+      auto run = [&](auto LAYER) {
+        constexpr bool kLayer = decltype(LAYER)::value;
+        const dim3 grid((uint32_t)rows);
+        if (d > kMaxCols) k_norm_fwd_wide<T, kLayer, kWide><<<grid, dim3(kWide), 0, s>>>(a);
+        else k_norm_fwd_wide<T, kLayer, kThin><<<grid, dim3(kThin), 0, s>>>(a);
+      };
+      if (kind == GIFT_NORM_LAYER) run(std::true_type{});
+      else run(std::false_type{});
       return;
     }
     by_width<kVecOf<T>>(d, [&](auto L, auto NV, auto TAIL) {
@@ -601,8 +610,14 @@ hipError_t launch_norm_backward(const void* dY, const void* X, int dtype, int64_
         else k_norm_cols<T, false><<<grid, dim3(256), 0, s>>>(a);
       }
       if (dX) {
-        if (kind == GIFT_NORM_LAYER) k_norm_bwd_wide<T, true><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
-        else k_norm_bwd_wide<T, false><<<dim3((uint32_t)rows), dim3(kWide), 0, s>>>(a);
+        auto run = [&](auto LAYER) {
+          constexpr bool kLayer = decltype(LAYER)::value;
+          const dim3 grid((uint32_t)rows);
+          if (d > kMaxCols) k_norm_bwd_wide<T, kLayer, kWide><<<grid, dim3(kWide), 0, s>>>(a);
+          else k_norm_bwd_wide<T, kLayer, kThin><<<grid, dim3(kThin), 0, s>>>(a);
+        };
+        if (kind == GIFT_NORM_LAYER) run(std::true_type{});
+        else run(std::false_type{});
       }
       return;
     }

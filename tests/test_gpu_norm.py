@@ -222,3 +222,23 @@ def test_offsets_past_32_bits(kind):
                                  kind=kind)
     dx, dw, db = fg.gift_norm_backward(dy, x, w, mean, rstd, kind=kind, dx=dy, dbias=torch.empty(d, device=DEV))
     assert torch.equal(dx[pick], part[0]) and bool((db == rows).all()) and bool(torch.isfinite(dw).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_short_rows(kind):
+    """5 M rows shorter than a vector, and the most rows there may be."""
+    say("norm many short rows kind %d" % kind)
+    rows, d = 5000001, 3
+    x, dy, w, b = _inputs(rows, d, torch.float32)
+    X, DY, W, B = (t.to(DEV) for t in (x, dy, w, b))
+    got = fg.gift_norm_forward(X, W, B, kind=kind)
+    _check_forward(x, w, b, 1e-5, kind, got)
+    grads = fg.gift_norm_backward(DY, X, W, got[1], got[2], kind=kind, dbias=torch.empty(d, device=DEV))
+    _check_backward(dy, x, w, got[1], got[2], kind, grads)
+    X = torch.full((2 ** 24, 1), 2.0, device=DEV)
+    y, mean, rstd = fg.gift_norm_forward(X, eps=0.0 if kind == fg.NORM_RMS else 1.0, kind=kind)
+    assert bool((y == (1.0 if kind == fg.NORM_RMS else 0.0)).all())
+    dx, dw, db = fg.gift_norm_backward(torch.ones_like(X), X, None, mean, rstd, kind=kind,
+                                       dbias=torch.empty(1, device=DEV))
+    assert bool((dx == 0.0).all()) and float(db) == 2 ** 24
+    assert float(dw) == (2 ** 24 if kind == fg.NORM_RMS else 0.0)
