@@ -174,6 +174,7 @@ gift_status gift_norm_forward(const void* X, int x_dtype, int64_t rows, int64_t 
   GIFT_TRY(check_vec("bias", bias));
   GIFT_TRY(check_vec("mean", mean));
   GIFT_TRY(check_vec("rstd", rstd));
+  if (mean && mean == rstd) return fail(GIFT_ERR_INVALID_ARG, "mean and rstd are the same buffer");
   return launched(launch_norm_forward(X, x_dtype, rows, d, kind, weight, bias, eps, Y, mean, rstd,
                                       (hipStream_t)stream));
 }
@@ -199,6 +200,8 @@ gift_status gift_norm_backward(const void* dY, const void* X, int x_dtype, int64
   GIFT_TRY(check_vec("rstd", rstd));
   GIFT_TRY(check_vec("dweight", dweight));
   GIFT_TRY(check_vec("dbias", dbias));
+  if (dweight && dweight == dbias)
+    return fail(GIFT_ERR_INVALID_ARG, "dweight and dbias are the same buffer");
   GIFT_TRY(check_ws(ws, ws_bytes, dweight || dbias ? norm_backward_ws(rows, d) : 0));
   return launched(launch_norm_backward(dY, X, x_dtype, rows, d, kind, weight, mean, rstd, dX, dweight,
                                        dbias, accumulate != 0, ws, (hipStream_t)stream));

@@ -497,7 +497,7 @@ gift_status gift_norm_forward(const void *X, int x_dtype, int64_t rows, int64_t 
  * dX (X's type), dweight and dbias (d fp32) may each be NULL, not all;
  * mean is required for LAYER.  dX and dY may be the same buffer.
  * accumulate != 0: dweight and dbias are added to.  The rows are summed in
- * an order that depends on (rows, d) and alignment alone.
+ * an order that depends on (rows, d) and the type alone.
  */
 gift_status gift_norm_backward(const void *dY, const void *X, int x_dtype, int64_t rows,
                                int64_t d, int kind, const float *weight, const float *mean,

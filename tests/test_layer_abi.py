@@ -141,3 +141,10 @@ def test_python_refuses_host_tensors():
         fg.gift_norm_forward(x)
     with pytest.raises(ValueError):
         fg.gift_mx_matmul(x, x)
+
+
+def test_norm_refuses_one_buffer_for_two_results():
+    lib = fg.load()
+    refused(lib.gift_norm_forward(X, BF, 4, 64, 0, W, None, 1e-5, Y, 0x50000, 0x50000, None), INVALID)
+    refused(lib.gift_norm_backward(Y, X, BF, 4, 64, 0, W, 0x50000, 0x60000, 0x70000, 0x80000, 0x80000, 0, WS,
+                                   1 << 30, None), INVALID)
