@@ -552,7 +552,7 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(
           // 34.5 us, 16384 x 11008 x 4096 448 -> 424 us
           if constexpr (kOut == kOutAcc)
             st16(p, __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, ld16(p)) + __builtin_bit_cast(f32x4, q)));
-              else if constexpr (kNt) st16_nt(p, q);
+          else if constexpr (kNt) st16_nt(p, q);
           else st16(p, q);
         } else {
           T o[kE];
