@@ -350,3 +350,55 @@ def test_offsets_past_32_bits():
     ra, rb = (fg.gift_mx_quantize(t, by_row=True)[0] for t in (a, b))
     out = fg.gift_mx_matmul(ra, rb)
     assert _rows_near(out, a, b, torch.tensor([0, 35000, 69999], device=DEV), 2.0 ** -8)
+
+
+@pytest.mark.parametrize("m,n,k", [(1100, 3001, 1100), (4000, 4090, 300), (1000, 1101, 16000)])
+def test_nan_scales_and_far_scales_in_tiles(m, n, k):
+    """As the two tests above for products cut into tiles and split sums."""
+    say("mx nan and far scales %dx%dx%d" % (m, n, k))
+    a, b = torch.zeros(m, k, device=DEV), torch.zeros(n, k, device=DEV)
+    a[:, ::7], b[:, ::7] = 3.0 * 2.0 ** -120, -1.5 * 2.0 ** 118
+    a[m // 2, k - 1], b[7, 0] = float("inf"), float("nan")
+    ra, _ = fg.gift_mx_quantize(a, by_row=True)
+    rb, _ = fg.gift_mx_quantize(b, by_row=True)
+    c = fg.gift_mx_matmul(ra, rb, dtype=torch.float32)
+    want = torch.full_like(c, -4.5 * len(range(0, k, 7)) * 2.0 ** -2)
+    want[m // 2], want[:, 7] = float("nan"), float("nan")
+    assert torch.equal(torch.isnan(c), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(c), torch.nan_to_num(want))
+
+
+def test_tiles_on_two_streams_and_in_two_graphs():
+    """Products that need a workspace, two at once on two streams, and in two
+    captured graphs that share one workspace and run one after the other."""
+    say("mx two streams, two graphs")
+    ops = [fg.gift_mx_quantize(_draw(*s).to(DEV), by_row=True)[0] for s in
+           ((1000, 16000, 1), (1101, 16000, 2), (1000, 16000, 3))]
+    need = fg.gift_mx_matmul_workspace_bytes(1000, 1101, 16000)
+    assert need > 0
+    want = [fg.gift_mx_matmul(ops[i], ops[1], dtype=torch.float32) for i in (0, 2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            got[i].append(fg.gift_mx_matmul(ops[2 * i], ops[1], dtype=torch.float32, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for i in range(2):
+        out = torch.empty(1000, 1101, device=DEV)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fg.gift_mx_matmul(ops[2 * i], ops[1], out=out, ws=ws)
+        graphs.append(graph)
+        outs.append(out)
+    for rep in range(3):
+        for out in outs:
+            out.fill_(float("nan"))
+        ws.fill_(255)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep

@@ -242,3 +242,37 @@ def test_many_short_rows(kind):
                                        dbias=torch.empty(1, device=DEV))
     assert bool((dx == 0.0).all()) and float(db) == 2 ** 24
     assert float(dw) == (2 ** 24 if kind == fg.NORM_RMS else 0.0)
+
+
+@pytest.mark.parametrize("rows,d", [(70, 1000), (5, 20000)])
+def test_side_stream_and_graph(rows, d):
+    """The calls on another stream, and captured: replays equal eager calls,
+    with eager work between them, and read the live inputs."""
+    say("norm stream and graph %dx%d" % (rows, d))
+    x, dy, w, b = (t.to(DEV) for t in _inputs(rows, d, torch.bfloat16))
+
+    def step(stream=None):
+        y, mean, rstd = fg.gift_norm_forward(x, w, b, stream=stream)
+        return (y, mean, rstd) + fg.gift_norm_backward(dy, x, w, mean, rstd, stream=stream)
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for rep in range(3):
+        for t in got:
+            t.fill_(float("nan"))
+        step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), rep
+    dy.mul_(2.0)   # a power of two: every gradient doubles, exactly
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and all(torch.equal(p, 2 * q) for p, q in zip(got[3:], want[3:]))
