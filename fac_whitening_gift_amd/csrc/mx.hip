@@ -62,31 +62,35 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
   b = __uint_as_float(w & 0xffff0000u);
 }
 
-constexpr int kQRows = 128;     // rows of a quantize tile: one k step of the operand by columns
-constexpr int kQCols = 64;      // columns: a row panel of it, half a k step of the operand by rows
-constexpr int kQThreads = 256;
+// A quantize tile: a row panel and half a k step of either operand.
+constexpr int kQRows = 64, kQCols = 64;
+constexpr int kQBlocks = kQRows * kQCols / 32;  // of one operand, a thread each
 
 // One tile of X through LDS, a block of 32 per thread; X is read once for
-// both operands.  Bound by memory: 16384 x 4096 bf16 into both 40 us, 205 MB
-// at 5.1 TB/s (a copy: 4.9); with a row segment of 128 columns a tile 45 us
-// there and half the workgroups on small matrices (1000 x 1024: 5.8 us
-// against 4.4).  By rows: 32
-// consecutive columns of a row, threads in fragment order, so 32 lanes write
-// 512 contiguous bytes of a fragment.  By columns: 32 rows of a column.  The
-// LDS row stride is 4 banks past a multiple of 32, so the 16 rows of a
-// fragment fall in 16 distinct groups of 4 banks.
+// both operands, whose blocks have threads of their own.  Bound by memory:
+// 16384 x 4096 bf16 into both 33.3 us, 205 MB at 6.2 TB/s with X in part in
+// the memory-side cache; a copy: 4.9.  Small matrices are bound by a launch
+// and the chain of load, encode and store: with 128 rows a tile and a block of
+// each operand in turn per thread 1000 x 1024 took 3.8 us, now 3.1, 2816 x 1024
+// fp32 4.9 and 4.0, 16384 x 4096 fp32 61.7 and 60.6; with 128 columns a tile
+// 16384 x 4096 bf16 took an eighth longer.  By rows: 32 consecutive columns
+// of a row, threads in fragment order, so 32 lanes write 512 contiguous bytes
+// of a fragment.  By columns: 32 rows of a column.  The LDS row stride is 4
+// banks past a multiple of 32, so the 16 rows of a fragment fall in 16
+// distinct groups of 4 banks.
 template <class T, bool kByRow, bool kByCol>
-__global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X, int64_t rows,
-                                                        int64_t cols, int64_t ld, uint8_t* R,
-                                                        uint8_t* C, int col_tiles,
-                                                        uint32_t* flags) {
+__global__ __launch_bounds__((kByRow + kByCol) * kQBlocks) void k_mx_quant(
+    const T* __restrict__ X, int64_t rows, int64_t cols, int64_t ld, uint8_t* R, uint8_t* C, int col_tiles,
+    uint32_t* flags) {
+  constexpr int kQThreads = (kByRow + kByCol) * kQBlocks;
   constexpr int kPer = 16 / sizeof(T);                  // elements of a 16-byte load
   constexpr int kStride = kQCols * sizeof(T) + 16;      // bytes of an LDS row
   constexpr int kChunks = kQCols / kPer;                // 16-byte chunks of a row
   constexpr int kLoads = kQRows * kChunks / kQThreads;  // chunks per thread
   __shared__ __attribute__((aligned(16))) char lds[kQRows * kStride];
   const int t = threadIdx.x;
-  const int tr = blockIdx.x / col_tiles, tc = blockIdx.x - tr * col_tiles;
+  const int id = blockIdx.y * gridDim.x + blockIdx.x;
+  const int tr = id / col_tiles, tc = id - tr * col_tiles;
   const int64_t r0 = (int64_t)tr * kQRows, c0 = (int64_t)tc * kQCols;
   // Loads go out together, from addresses clamped into X; what lies outside
   // becomes zero.
@@ -126,12 +130,11 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
   }
   __syncthreads();
   uint32_t fl = 0;
-  if constexpr (kByRow) {
-    // 8 fragments x 2 blocks x 16 rows; the panel's steps cover an even
+  if (kByRow && t < kQBlocks) {
+    // 4 fragments x 2 blocks x 16 rows; the panel's steps cover an even
     // number of tiles, the last of which may lie past the columns (zeros)
     const int f = t >> 5, bb = (t >> 4) & 1, r = f * 16 + (t & 15);
-    const int64_t panel = (r0 >> 6) + (f >> 2);
-    if (panel < (rows + kMxRows - 1) / kMxRows) {
+    if (r0 < rows) {
       float v[32];
       const char* src = lds + r * kStride + bb * 32 * sizeof(T);
 #pragma unroll
@@ -153,15 +156,16 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
       const uint4 w = mx_block(v, code, bf);
       if (r0 + r < rows && c0 + bb * 32 < cols) fl |= bf;
       const int lane = ((tc & 1) * 2 + bb) * 16 + (t & 15);
-      uint8_t* out = R + (panel * (col_tiles / 2) + (tc >> 1)) * (int64_t)kMxPanel;
-      *reinterpret_cast<uint4*>(out + (f & 3) * 1024 + lane * 16) = w;
-      out[4096 + lane * 4 + (f & 3)] = (uint8_t)code;
+      uint8_t* out = R + ((int64_t)tr * (col_tiles / 2) + (tc >> 1)) * kMxPanel;
+      *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16) = w;
+      out[4096 + lane * 4 + f] = (uint8_t)code;
     }
   }
-  if constexpr (kByCol) {
+  if (kByCol && t >= kQThreads - kQBlocks) {
+    // as above, an even number of tiles down the columns
     const int64_t steps = (rows + kMxStep - 1) / kMxStep;
-    const int b = t >> 6, c = t & 63;  // rows 32 b .. +31 of column c
-    if (c0 < cols) {
+    const int b = (t - (kQThreads - kQBlocks)) >> 6, c = t & 63;  // rows 32 b .. +31 of column c
+    if (c0 < cols && (tr >> 1) < steps) {
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -169,8 +173,8 @@ __global__ __launch_bounds__(kQThreads) void k_mx_quant(const T* __restrict__ X,
       uint32_t code, bf = 0;
       const uint4 w = mx_block(v, code, bf);
       if (r0 + b * 32 < rows && c0 + c < cols) fl |= bf;
-      uint8_t* out = C + (tc * steps + tr) * (int64_t)kMxPanel;
-      const int f = c >> 4, lane = b * 16 + (c & 15);
+      uint8_t* out = C + (tc * steps + (tr >> 1)) * (int64_t)kMxPanel;
+      const int f = c >> 4, lane = ((tr & 1) * 2 + b) * 16 + (c & 15);
       *reinterpret_cast<uint4*>(out + f * 1024 + lane * 16) = w;
       out[4096 + lane * 4 + f] = (uint8_t)code;
     }
@@ -743,12 +747,15 @@ bool rows_aligned(const void* p, int64_t ld, int dtype) {
 hipError_t launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld,
                               uint8_t* by_row, uint8_t* by_col, uint32_t* flags, hipStream_t s) {
   const int ct = (int)((cols + kMxStep - 1) / kMxStep) * (kMxStep / kQCols);
-  const int64_t tiles = (rows + kQRows - 1) / kQRows * ct;
+  // both halves of a step of the operand by columns, the second may lie past the rows
+  const int64_t down = by_col ? (rows + kMxStep - 1) / kMxStep * (kMxStep / kQRows) : (rows + kQRows - 1) / kQRows;
+  // a dimension of a grid holds fewer than 2^32 threads
+  const dim3 grid = down * ct <= 1 << 23 ? dim3((uint32_t)(down * ct)) : dim3((uint32_t)((down * ct + 1) / 2), 2);
   auto go = [&](auto zero) {
     using T = decltype(zero);
     auto run = [&](auto kernel) {
-      kernel<<<dim3((uint32_t)tiles), dim3(kQThreads), 0, s>>>(static_cast<const T*>(X), rows, cols, ld,
-                                                               by_row, by_col, ct, flags);
+      kernel<<<grid, dim3((by_row && by_col ? 2 : 1) * kQBlocks), 0, s>>>(
+          static_cast<const T*>(X), rows, cols, ld, by_row, by_col, ct, flags);
     };
     if (by_row && by_col) run(k_mx_quant<T, true, true>);
     else if (by_row) run(k_mx_quant<T, true, false>);

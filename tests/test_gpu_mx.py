@@ -402,3 +402,24 @@ def test_tiles_on_two_streams_and_in_two_graphs():
             graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), rep
+
+
+def test_quantize_of_very_many_tiles():
+    """34 G elements: rows at both ends and in the middle of both operands."""
+    say("mx very many tiles")
+    rows, cols = 2 ** 23 + 70, 4100
+    x = torch.ones(1, dtype=BF16, device=DEV).expand(rows, cols).contiguous()
+    pick = torch.tensor([0, 1, rows // 2, rows - 71, rows - 1], device=DEV)
+    x[pick] = _draw(5, cols, 1, BF16).to(DEV)
+    r, _ = fg.gift_mx_quantize(x, by_row=True)
+    few, _ = fg.gift_mx_quantize(x[pick].contiguous(), by_row=True)
+    want = fg.gift_mx_dequantize(few, dtype=BF16)
+    for i, row in enumerate(pick.tolist()):   # the operand's panel of that row
+        step = r.data.numel() // -(-rows // 64)
+        panel = fg.MxOperand(64, cols, data=r.data[row // 64 * step:][:step])
+        assert torch.equal(fg.gift_mx_dequantize(panel, dtype=BF16)[row % 64], want[i])
+    del r
+    _, c = fg.gift_mx_quantize(x, by_col=True)
+    edge = x[-(rows % 128) - 128:].t().contiguous()   # whole steps to the end
+    last = fg.gift_mx_quantize(edge, by_row=True)[0].data.view(-1, 2, 4352)
+    assert torch.equal(c.data.view(-1, -(-rows // 128), 4352)[:, -2:], last)
