@@ -236,15 +236,16 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
 // 16 (or 4) bytes per lane from the raw buffer (at voff) into LDS at m0 +
 // 16 (4) lane.  Written in asm so that the compiler does not make every LDS
 // read wait for all copies in flight: the kernel waits with explicit vmcnt
-// counts.  The instruction writes no VGPR.
+// counts.  The instruction writes no VGPR.  A copy reads M0 at the earliest
+// one wait state after a scalar write of it; the compiler adds none inside asm.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
 }
 #pragma clang diagnostic pop

@@ -344,12 +344,13 @@ __device__ __forceinline__ int cov_swz(int t) {
 // lane.  Written in asm so the compiler does not make every LDS read wait
 // for all LDS DMA in flight (it cannot tell the two stages apart): the kernel
 // waits with explicit vmcnt counts before its barriers.  The instruction
-// writes no VGPR; m0 is set in the same statement.
+// writes no VGPR; m0 is set in the same statement, with the wait state that a
+// copy needs after a scalar write of m0 (the compiler adds none inside asm).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void cov_dma(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff,
                                         uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds), "v"(voff), "s"(rs), "s"(soff) : "memory", "m0");
 }
 #pragma clang diagnostic pop
