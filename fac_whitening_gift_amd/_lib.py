@@ -721,9 +721,9 @@ def gift_mx_quantize(x, by_row=None, by_col=None, flags=None, stream=None):
 
 def gift_mx_dequantize(a, dtype=torch.float32, out=None, stream=None):
     """-> rows x k tensor of the values the operand stands for."""
+    ref = _operand(a, "a")
     if stream is not None:
         return _on(stream, a.device, gift_mx_dequantize, a, dtype, out)
-    ref = _operand(a, "a")
     if out is None:
         out = a.data.new_empty(a.shape, dtype=dtype)
     ptr, dt, _, _, ld = _matrix(out, "out", a.device, a.shape)
@@ -739,9 +739,9 @@ def gift_mx_matmul(a, b, bias=None, out=None, dtype=torch.bfloat16, accumulate=F
                    stream=None):
     """a (M x k), b (N x k) operands -> a b^T (+ bias), M x N of dtype (or out's);
     accumulate: out (fp32) += the product."""
+    ra, rb = _operand(a, "a"), _operand(b, "b", a.device)
     if stream is not None:
         return _on(stream, a.device, gift_mx_matmul, a, b, bias, out, dtype, accumulate, ws)
-    ra, rb = _operand(a, "a"), _operand(b, "b", a.device)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     dev = a.device
@@ -768,11 +768,11 @@ def gift_mx_linear_workspace_bytes(rows, n, k):
 def gift_mx_linear(x, w, bias=None, out=None, dtype=None, flags=None, ws=None, stream=None):
     """x (rows x k, bf16 or fp32) quantized in the call, w an operand (n x k)
     -> x w^T (+ bias), rows x n of dtype (x's when not given)."""
+    rw = _operand(w, "w")
     if stream is not None:
         return _on(stream, x.device, gift_mx_linear, x, w, bias, out, dtype, flags, ws)
     dev = x.device
     ptr, dt, rows, _, ld = _matrix(x, "x", w.device)
-    rw = _operand(w, "w", dev)
     if x.shape[1] != w.k:
         raise ValueError("x has %d columns, w sums over %d" % (x.shape[1], w.k))
     if out is None:
