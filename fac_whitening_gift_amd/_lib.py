@@ -665,6 +665,8 @@ class MxOperand:
         if nbytes == 0:
             raise ValueError("MXFP4 operand of %d x %d is out of range" % (rows, k))
         if like is not None:
+            if not like.is_cuda:
+                raise ValueError("like must be a device tensor")
             data = like.new_empty(nbytes, dtype=torch.uint8)
         else:
             if data is None:

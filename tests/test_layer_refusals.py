@@ -19,3 +19,14 @@ def test_operands_are_operands(bad, stream):
         fg.gift_mx_matmul(bad, bad, stream=stream)
     with pytest.raises(ValueError, match="a must be an MxOperand"):
         fg.gift_mx_dequantize(bad, stream=stream)
+
+
+def test_an_operand_lives_on_a_device():
+    """A host buffer behind an operand would reach the kernels as an address."""
+    x = torch.zeros(64, 128)
+    with pytest.raises(ValueError, match="device tensor"):
+        fg.MxOperand(64, 128, like=x)
+    with pytest.raises(ValueError, match="device tensor"):
+        fg.MxOperand(64, 128, device="cpu")
+    with pytest.raises(ValueError, match="device tensor"):
+        fg.MxOperand(64, 128, data=torch.zeros(4352, dtype=torch.uint8))
