@@ -2,7 +2,8 @@
 mx_plans.py: tiles with rows of C on 128-byte lines and not, split sums, the
 small form by rows and columns, the one-launch linear), on operands whose
 products are exact in fp32: whole results have to be equal to the fp64
-product, in both types, with a bias and accumulated."""
+product, in both types, with a bias and accumulated; and operands and results
+past 32-bit offsets."""
 
 import pytest
 import torch
@@ -93,3 +94,56 @@ def test_linear_is_exact(shape, x_dtype):
     wide = torch.full((rows, k + 9), float("nan"), dtype=x_dtype, device=DEV)
     wide[:, 5:5 + k] = x
     assert torch.equal(fg.gift_mx_linear(wide[:, 5:5 + k], qw, dtype=torch.float32), want.float())
+
+
+@pytest.mark.parametrize("n", [16, 700])
+def test_operands_past_32_bits(n):
+    """An operand of 4.5 GB as A and as B.  Its rows are 97 rows over and
+    over, each time times another power of two, so the whole result is known;
+    no offset that loses its upper bits meets an equal row (2^31 and 2^32
+    bytes are no whole multiples of 97 rows)."""
+    say("mx exact operands past 32 bits n=%d" % n)
+    rows, k = 70000, 122000
+    g = _gen(n)
+    base, rb = mp.exact_values(97, k, g, DEV)
+    w, rw = mp.exact_values(n, k, g, DEV)
+    small = mp.exact_product(base, rb, w, rw)
+    at = torch.arange(rows, device=DEV)
+    power = torch.exp2((at // 97 % 5 - 2).float())[:, None]
+    x = torch.empty(rows, k, dtype=BF16, device=DEV)
+    for i in range(0, rows, 10000):   # (in parts: less memory on the way)
+        x[i:i + 10000] = (base.to(BF16)[at[i:i + 10000] % 97] * power[i:i + 10000].to(BF16))
+    q, _ = fg.gift_mx_quantize(x, by_row=True)
+    del x
+    assert q.data.numel() > 2 ** 32
+    for wrap in (2 ** 31, 2 ** 32):
+        assert wrap * 64 // (-(-k // 128) * 4352) % 97 != 0
+    qw, _ = fg.gift_mx_quantize(w, by_row=True)
+    want = (small[at % 97] * power.double()).float()
+    assert torch.equal(fg.gift_mx_matmul(q, qw, dtype=torch.float32), want)
+    assert torch.equal(fg.gift_mx_matmul(qw, q, dtype=torch.float32), want.t().contiguous())
+
+
+@pytest.mark.parametrize("shape", [(5, 300, 600), (40, 300, 600), (300, 1083, 300), (1999, 4064, 300)])
+def test_rows_far_apart(shape):
+    """Rows of X and of C whose offsets pass 2^32 bytes in small matrices."""
+    say("mx rows far apart %dx%dx%d" % shape)
+    m, n, k = shape
+    ld = 2 ** 33 // m // 64 * 64 + 64   # 16 GB of bf16 from the first row to the last
+    g = _gen(m)
+    a, ra = mp.exact_values(m, k, g, DEV)
+    b, rb = mp.exact_values(n, k, g, DEV)
+    want = mp.exact_product(a, ra, b, rb)
+    wide = torch.zeros(m, ld, dtype=BF16, device=DEV)
+    wide[:, 64:64 + k] = a.to(BF16)
+    x = wide[:, 64:64 + k]
+    qa, _ = fg.gift_mx_quantize(x, by_row=True)
+    qb, _ = fg.gift_mx_quantize(b, by_row=True)
+    assert torch.equal(fg.gift_mx_dequantize(qa), a)
+    assert torch.equal(fg.gift_mx_linear(x, qb, dtype=torch.float32), want.float())
+    view = wide[:, 128:128 + n]
+    fg.gift_mx_matmul(qa, qb, out=view)
+    assert torch.equal(view, _rounded(want, BF16))
+    view = wide[:, 64:64 + k]
+    fg.gift_mx_dequantize(qa, out=view)
+    assert torch.equal(view, a.to(BF16))
