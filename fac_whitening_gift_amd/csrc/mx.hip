@@ -941,9 +941,11 @@ static size_t few_lds(int64_t M, int64_t k) {
 // In one launch every workgroup quantizes all of X, 0.75 us for each 512
 // blocks; a launch of its own takes 2.8 us (16 x 4096 -> 11008: 12.2, 10.0,
 // 7.4 us with 16, 32, 64 columns; 16 x 11008 -> 4096: 13.5 us in one launch,
-// 10.0 in two; 1 x 4096 -> 4096: 3.6 and 6.3).
+// 10.0 in two; 1 x 4096 -> 4096: 3.6 and 6.3).  The two launches' estimate is at
+// most few_us + 2.8 with the same columns, so one launch is taken only where
+// 0.75 M steps 4 / 512 < 2.8: M steps < 478, or 32.5 KB of LDS (few_lds).
 int mx_linear_cols(int64_t M, int64_t N, int64_t k) {
-  if (M > 16 || few_lds(M, k) > kMxFewLds) return 0;
+  if (M > 16) return 0;
   const int64_t steps = up_div(k, kMxStep);
   double least;
   plan_us(M, N, k, least);

@@ -33,7 +33,6 @@ __device__ __forceinline__ void st16_nt(T* p, const uint4& v) {
 constexpr int kMxRows = 64;                      // rows of an operand panel
 constexpr int kMxStep = 128;                     // k elements of a step
 constexpr int kMxPanel = GIFT_MX_PANEL_BYTES;    // bytes of a panel's step
-constexpr size_t kMxFewLds = 96 << 10;           // LDS for the rows quantized in front of a product
 
 struct MxPlan {
   int rows;       // of a workgroup: 64 (k_mx_few) or 128 (k_mx_gemm)

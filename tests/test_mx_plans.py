@@ -49,3 +49,15 @@ def test_exact_values_are_exact():
         for i in order:
             s = s + a[:, i:i + 1] * b[:, i]
         assert torch.equal(s.double(), want)
+
+
+def test_lds_of_the_one_launch_linear():
+    """Rows quantized in front of a product take 68 bytes per row and 128 k
+    elements; the cut keeps them under 32.5 KB."""
+    most = 0
+    for rows in range(1, 17):
+        for steps in list(range(400 // rows, 520 // rows + 2)) + [600, 2000]:
+            for n in (16, 1000, 4096, 8000, 11008, 20000, 100000):
+                if mp.linear_cols(rows, n, 128 * steps):
+                    most = max(most, rows * steps * 68)
+    assert 30000 < most < 32500
