@@ -68,8 +68,9 @@ constexpr int kQBlocks = kQRows * kQCols / 32;  // of one operand, a thread each
 
 // One tile of X through LDS, a block of 32 per thread; X is read once for
 // both operands, whose blocks have threads of their own.  Bound by memory:
-// 16384 x 4096 bf16 into both 33.3 us, 205 MB at 6.2 TB/s with X in part in
-// the memory-side cache; a copy: 4.9.  Small matrices are bound by a launch
+// 16384 x 4096 bf16 into both 36 to 39 us on inputs in turn, 205 MB at 5.3 to
+// 5.7 TB/s (33 us on one input, then in part in the memory-side cache); a
+// copy: 4.9.  Small matrices are bound by a launch
 // and the chain of load, encode and store: with 128 rows a tile and a block of
 // each operand in turn per thread 1000 x 1024 took 3.8 us, now 3.1, 2816 x 1024
 // fp32 4.9 and 4.0, 16384 x 4096 fp32 61.7 and 60.6; with 128 columns a tile
@@ -347,17 +348,21 @@ __device__ __forceinline__ void static_for(F f) {
 // compiler would sink the MFMAs below it, away from the copies and reads they
 // are spread among.
 //
-// Bound by power, then by LDS: on large products the matrix units are busy
-// 65% of the cycles (SQ counters) at the 1.6 GHz that the clock falls to, 4.3
-// to 4.9 PFLOP/s; a loop of these MFMAs alone on the same random codes, with
-// no loads, reaches 5.6 to 7.3 (9.7 on zeros).  LDS traffic decides among
-// tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
+// Bound by power and by the loop's copies and LDS reads: on large products the
+// matrix units are busy 65% of the cycles (SQ counters) at the 1.6 GHz that
+// the clock falls to, 3.6 to 4.6 PFLOP/s; a loop of these MFMAs alone on the
+// same random codes, with no loads, reaches 5.6 to 7.3 (9.7 on zeros), and of
+// the time of a 256 x 256 loop 15% went without its copies or without its LDS
+// reads, 25% without both.  With 12 k steps (16384 x 4096 x 1536, 62 to 70 us,
+// 2.9 to 3.3 PFLOP/s) or one round of tiles (1999 x 4096 x 4096, 20 to 22 us)
+// the three stages filled before a tile's first MFMA and the results stored
+// after its last show: nothing of the same workgroup runs beside them.
+// Accumulating reads C through the caches (11008 x 4096 x 16384 417 us, 353
+// without; 4096 x 1536 x 16384 66 and 61).  LDS traffic decides among tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
 // eight for 16.  Measured against it, 16384 x 1536 x 4096 / 16384 x 4096 x
 // 11008: 128 x 256 tiles 52.7 / 338 us (waves of 64 x 128: 53.7 / 338), two
 // waves of 128 x 128 a tile 65.7 / 348, 256 x 256 tiles, one to a CU,
-// running on from tile to tile 64 / 332, 128 x 128 tiles 55.9 / -.  Without
-// its copies or without its LDS reads that 256 x 256 loop took 85% of its
-// time, without both 75%.
+// running on from tile to tile 64 / 332, 128 x 128 tiles 55.9 / -.
 template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias, bool kNt>
 __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(MxGemm g) {
   constexpr int kWaves = WR * WC;
@@ -598,10 +603,16 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
 // in turn, straight from memory into the MFMA operands, with no LDS and no
 // barrier in the loop, and their sums are added in wave order through LDS.
 // kQuant: A is X itself (at most 16 rows), quantized into LDS first.
-// Bound by a launch and one chain of loads (1 x 4096 -> 4096 3.6 us, an empty
-// launch 2.3), by the weights' bytes (1 x 4096 -> 11008 4.4 us for 24 MB) and,
-// with many rows, by the operand bytes that every workgroup loads from the
-// second-level caches (512 x 4096 x 4096 in 16 columns 20.6 us, 347 MB).
+// Bound by a launch and chains of loads.  kQuant: one chain, B's loads before
+// the rows are quantized (1 x 4096 -> 4096 4.1 us, an empty launch 2.3), or the
+// weights' bytes (1 x 4096 -> 11008 24 MB in 6.2 us from memory, 4.8 from the
+// caches); the last block of a ragged k is loaded element by element (1 x 4095
+// -> 4096 6.2 us).  Else A's loads of a k step wait behind the branch that
+// ends the sum, where the compiler puts them, for each step in turn: 11 steps a
+// wave of 24 x 11008 -> 4096 take 10.8 us (9.4 with the weights in the caches),
+// 64 rows 4096 -> 4096 7.1, 256 rows 10.0.  With many rows also by the operand
+// bytes that every workgroup loads from the second-level caches (512 x 4096 x
+// 4096 in 16 columns 20.6 us, 347 MB).
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
@@ -615,7 +626,7 @@ struct MxFew {
 
 template <int FM, int FN, class T, bool kQuant>
 __global__ __launch_bounds__(64 * kFewWaves) void k_mx_few(MxFew q) {
-  constexpr int kUnroll = FM + FN <= 5 ? 4 : 2;  // k steps in flight per wave
+  constexpr int kUnroll = FM + FN <= 5 ? 4 : 2;  // k steps of B (kQuant: of both) in flight per wave
   constexpr int kSub = 4 / FN;                   // workgroups of a column panel
   extern __shared__ __attribute__((aligned(16))) char dyn[];
   __shared__ float sums[kFewWaves][FN][256];
@@ -791,8 +802,8 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
 // are within about 20% there.  Measured, the best and the next: 512 x 1024 x
 // 1024 4.9 us in 32-column workgroups, 6.7 in 128 x 128 tiles; 1000 x 11008 x
 // 4096 26.8 us in 128 x 128, 28.9 in 128 x 256; 16384 x 11008 x 4096 346.8 us
-// in 128 x 256, 365.9 in 128 x 128; 256 x 1024 x 11008 13.9 us in 128 x 128
-// split four ways, 22.8 unsplit.
+// in 128 x 256, 365.9 in 128 x 128; 256 x 1024 x 11008 10.8 us in 16 columns,
+// 13.9 in 128 x 128 split four ways, 22.8 unsplit.
 static int64_t up_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
 // k_mx_few with 16 fn columns a workgroup: a launch and a fixed latency, then

@@ -7,9 +7,11 @@
 // (k_norm_fwd_wide, k_norm_bwd_wide).  All sums are fp32, added in a fixed
 // order.
 //
-// Bound by memory: 16384 x 4096 bf16 forward 57 to 59 us (268 MB, 4.6 TB/s),
-// backward 82 us with the sum of its 512 partial rows (436 MB with them, 5.3
-// TB/s); a copy of 4 GB runs at 4.9 TB/s.
+// Bound by memory (16384 x 4096, inputs in turn): bf16 forward 49 to 57 us
+// (268 MB, 4.7 to 5.5 TB/s), backward 80 us and 5 for the sum of its 512
+// partial rows (with them layer norm 436 MB, 5.1 TB/s, RMS norm 419 MB, 4.9);
+// fp32 forward 102 us (537 MB, 5.3 TB/s), backward 168 and 159 us and 5 (layer
+// norm 839 MB, 4.9 TB/s, RMS norm 822, 5.0).  A copy of 4 GB runs at 4.9 TB/s.
 #include <type_traits>
 
 #include "device.hpp"
@@ -510,7 +512,11 @@ constexpr int kMaxCols = 512 * 32;  // widest row of the register form
 // Launch the instance for a width: kL lanes a row and the elements of a lane.
 // 128 lanes with 32 elements each serve 4096 columns best (16384 rows of bf16,
 // forward / backward: 57.0 / 89.8 us; 64 with 64: 60.8; 256 with 16: 59.6 /
-// 90.6; 512 with 8: 66.1 / 94.4).
+// 90.6; 512 with 8: 66.1 / 94.4).  fp32 takes the same lanes with twice the
+// vectors: its backward instances of 32 elements need 297 to 324 registers, one
+// wave a SIMD, which still keep the copy's rate (8192 columns 330 us, 1.6 GB),
+// and above 12288 columns spill up to 332 bytes (8192 x 16384 481 us, 3.4 TB/s;
+// bf16 of odd width there 76 to 92 bytes, 8192 x 16383 254 us, 215 for 16384).
 template <int kVec, class F>
 void by_width(int64_t d, F f) {
   auto go = [&](auto L, auto E) {
@@ -539,7 +545,8 @@ void by_width(int64_t d, F f) {
 }
 
 // Workgroups of the backward pass, each leaving one partial row of the
-// weight's gradient: at least 4 rows each, and about as many as are resident
+// weight's gradient: at least 4 rows each, and about as many as are resident in
+// bf16 (of fp32 rows above 2048 columns fewer: there the runs take turns)
 // (16384 rows of bf16, 256 / 512 / 1024 of them: 300 columns 28.0 / 19.9 /
 // 18.0 us, 4096 columns 104.8 / 82.3 / 91.7, 9000 columns 236 / 251 / 282).
 int norm_parts(int64_t rows, int64_t d) {

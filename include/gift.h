@@ -480,8 +480,9 @@ size_t gift_mx_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k);
  *   y = h * weight + bias
  * weight, bias: d fp32 (NULL: 1 and 0).  Y has X's type; mean (LAYER only)
  * and rstd, fp32, one per row, may be NULL.  Statistics are fp32, the
- * variance in a second pass over the centred values; a row whose squares
- * overflow fp32 gets r = 0.  X and Y may be the same buffer.  X, Y, dY and dX
+ * variance in a second pass over the centred values; a row of finite values
+ * whose squares overflow fp32 gets r = 0 (and, LAYER, NaN in Y where its sum
+ * overflows too).  X and Y may be the same buffer.  X, Y, dY and dX
  * need their element alignment only.
  */
 enum { GIFT_NORM_LAYER = 0, GIFT_NORM_RMS = 1 };

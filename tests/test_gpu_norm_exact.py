@@ -70,3 +70,23 @@ def test_gradients_count_millions_of_rows(rows, d, dtype, kind):
     """Register form and wide form past 2^31 elements, and 5 M short rows."""
     say("norm exact %dx%d %s kind %d" % (rows, d, dtype, kind))
     _check(rows, d, dtype, kind)
+
+
+@pytest.mark.parametrize("d", [200, 4096, 17000])
+def test_rows_that_overflow(d):
+    """Squares past fp32: rstd 0, Y the bias; layer norm's sum past it too: NaN."""
+    say("norm overflow d=%d" % d)
+    x = torch.full((3, d), 1e25, device=DEV)
+    x[:, ::2] = -2e25
+    x[1] = 1.0
+    b = torch.randn(d, device=DEV)
+    for kind in KINDS:
+        y, _, rstd = fg.gift_norm_forward(x, None, b, kind=kind)
+        assert float(rstd[0]) == 0 and float(rstd[2]) == 0 and bool(torch.isfinite(y).all())
+        assert torch.equal(y[0], b) and torch.equal(y[2], b)
+    x[0] = 3e38
+    y, mean, rstd = fg.gift_norm_forward(x, None, b)
+    assert float(rstd[0]) == 0 and float(mean[0]) == float("inf") and bool(torch.isnan(y[0]).all())
+    assert bool(torch.isfinite(y[1:]).all())
+    y, _, rstd = fg.gift_norm_forward(x, None, b, kind=fg.NORM_RMS)
+    assert float(rstd[0]) == 0 and torch.equal(y[0], b)
