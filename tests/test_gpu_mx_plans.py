@@ -147,3 +147,25 @@ def test_rows_far_apart(shape):
     view = wide[:, 64:64 + k]
     fg.gift_mx_dequantize(qa, out=view)
     assert torch.equal(view, a.to(BF16))
+
+
+@pytest.mark.parametrize("shape", [(7, 100, 500), (300, 2100, 900), (1999, 4064, 300), (349, 33, 26797)])
+def test_operands_at_any_16_bytes(shape):
+    """Operands that start 16 bytes past a larger alignment; nothing beside
+    them is written."""
+    say("mx operands at 16 bytes %dx%dx%d" % shape)
+    g = _gen(sum(shape))
+    m, n, k = shape
+    want, ops = [], []
+    for rows in (m, n):
+        v, r = mp.exact_values(rows, k, g, DEV)
+        size = fg.gift_mx_bytes(rows, k)
+        buf = torch.full((size + 48,), 171, dtype=torch.uint8, device=DEV)
+        op = fg.MxOperand(rows, k, data=buf[16:16 + size])
+        fg.gift_mx_quantize(v, by_row=op)
+        assert bool((buf[:16] == 171).all()) and bool((buf[16 + size:] == 171).all())
+        assert torch.equal(fg.gift_mx_dequantize(op), v)
+        want += [v, r]
+        ops.append(op)
+    assert torch.equal(fg.gift_mx_matmul(*ops, dtype=torch.float32), mp.exact_product(*want).float())
+    assert torch.equal(fg.gift_mx_linear(want[0], ops[1], dtype=torch.float32), mp.exact_product(*want).float())
