@@ -354,11 +354,11 @@ __device__ __forceinline__ void static_for(F f) {
 // same random codes, with no loads, reaches 5.6 to 7.3 (9.7 on zeros), and of
 // the time of a 256 x 256 loop 15% went without its copies or without its LDS
 // reads, 25% without both.  With 12 k steps (16384 x 4096 x 1536, 62 to 70 us,
-// 2.9 to 3.3 PFLOP/s) or one round of tiles (1999 x 4096 x 4096, 20 to 22 us)
+// 2.9 to 3.3 PFLOP/s) or one round of tiles (1999 x 4096 x 4096, 20 to 23 us)
 // the three stages filled before a tile's first MFMA and the results stored
 // after its last show: nothing of the same workgroup runs beside them.
-// Accumulating reads C through the caches (11008 x 4096 x 16384 417 us, 353
-// without; 4096 x 1536 x 16384 66 and 61).  LDS traffic decides among tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
+// Accumulating reads C through the caches (11008 x 4096 x 16384 411 us, 336
+// without; 4096 x 1536 x 16384 65 and 63).  LDS traffic decides among tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
 // eight for 16.  Measured against it, 16384 x 1536 x 4096 / 16384 x 4096 x
 // 11008: 128 x 256 tiles 52.7 / 338 us (waves of 64 x 128: 53.7 / 338), two
 // waves of 128 x 128 a tile 65.7 / 348, 256 x 256 tiles, one to a CU,
@@ -604,13 +604,13 @@ __global__ __launch_bounds__(256) void k_mx_reduce(MxGemm g) {
 // barrier in the loop, and their sums are added in wave order through LDS.
 // kQuant: A is X itself (at most 16 rows), quantized into LDS first.
 // Bound by a launch and chains of loads.  kQuant: one chain, B's loads before
-// the rows are quantized (1 x 4096 -> 4096 4.1 us, an empty launch 2.3), or the
-// weights' bytes (1 x 4096 -> 11008 24 MB in 6.2 us from memory, 4.8 from the
+// the rows are quantized (1 x 4096 -> 4096 4.0 us, an empty launch 2.3), or the
+// weights' bytes (1 x 4096 -> 11008 24 MB in 6.3 us from memory, 4.8 from the
 // caches); the last block of a ragged k is loaded element by element (1 x 4095
-// -> 4096 6.2 us).  Else A's loads of a k step wait behind the branch that
+// -> 4096 6.1 us).  Else A's loads of a k step wait behind the branch that
 // ends the sum, where the compiler puts them, for each step in turn: 11 steps a
-// wave of 24 x 11008 -> 4096 take 10.8 us (9.4 with the weights in the caches),
-// 64 rows 4096 -> 4096 7.1, 256 rows 10.0.  With many rows also by the operand
+// wave of 24 x 11008 -> 4096 take 11 us (9.4 with the weights in the caches),
+// 64 rows 4096 -> 4096 7.2, 256 rows 10.3.  With many rows also by the operand
 // bytes that every workgroup loads from the second-level caches (512 x 4096 x
 // 4096 in 16 columns 20.6 us, 347 MB).
 // ---------------------------------------------------------------------------
@@ -802,7 +802,7 @@ hipError_t launch_mx_dequantize(const uint8_t* A, int64_t rows, int64_t k, void*
 // are within about 20% there.  Measured, the best and the next: 512 x 1024 x
 // 1024 4.9 us in 32-column workgroups, 6.7 in 128 x 128 tiles; 1000 x 11008 x
 // 4096 26.8 us in 128 x 128, 28.9 in 128 x 256; 16384 x 11008 x 4096 346.8 us
-// in 128 x 256, 365.9 in 128 x 128; 256 x 1024 x 11008 10.8 us in 16 columns,
+// in 128 x 256, 365.9 in 128 x 128; 256 x 1024 x 11008 11.1 us in 16 columns,
 // 13.9 in 128 x 128 split four ways, 22.8 unsplit.
 static int64_t up_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
 

@@ -10,7 +10,7 @@
 // Bound by memory (16384 x 4096, inputs in turn): bf16 forward 49 to 57 us
 // (268 MB, 4.7 to 5.5 TB/s), backward 80 us and 5 for the sum of its 512
 // partial rows (with them layer norm 436 MB, 5.1 TB/s, RMS norm 419 MB, 4.9);
-// fp32 forward 102 us (537 MB, 5.3 TB/s), backward 168 and 159 us and 5 (layer
+// fp32 forward 102 us (537 MB, 5.3 TB/s), backward 167 and 160 us and 5 (layer
 // norm 839 MB, 4.9 TB/s, RMS norm 822, 5.0).  A copy of 4 GB runs at 4.9 TB/s.
 #include <type_traits>
 
@@ -516,7 +516,7 @@ constexpr int kMaxCols = 512 * 32;  // widest row of the register form
 // vectors: its backward instances of 32 elements need 297 to 324 registers, one
 // wave a SIMD, which still keep the copy's rate (8192 columns 330 us, 1.6 GB),
 // and above 12288 columns spill up to 332 bytes (8192 x 16384 481 us, 3.4 TB/s;
-// bf16 of odd width there 76 to 92 bytes, 8192 x 16383 254 us, 215 for 16384).
+// bf16 of odd width there 76 to 92 bytes, 8192 x 16383 254 us, 208 for 16384).
 template <int kVec, class F>
 void by_width(int64_t d, F f) {
   auto go = [&](auto L, auto E) {
