@@ -358,11 +358,12 @@ __device__ __forceinline__ void static_for(F f) {
 // the three stages filled before a tile's first MFMA and the results stored
 // after its last show: nothing of the same workgroup runs beside them.
 // Accumulating reads C through the caches (11008 x 4096 x 16384 411 us, 336
-// without; 4096 x 1536 x 16384 65 and 63).  LDS traffic decides among tiles: a wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64
-// eight for 16.  Measured against it, 16384 x 1536 x 4096 / 16384 x 4096 x
-// 11008: 128 x 256 tiles 52.7 / 338 us (waves of 64 x 128: 53.7 / 338), two
-// waves of 128 x 128 a tile 65.7 / 348, 256 x 256 tiles, one to a CU,
-// running on from tile to tile 64 / 332, 128 x 128 tiles 55.9 / -.
+// without; 4096 x 1536 x 16384 65 and 63).  LDS traffic decides among tiles: a
+// wave of 128 x 64 reads 12 fragments for 32 MFMAs, one of 64 x 64 eight for 16.
+// Measured against it, 16384 x 1536 x 4096 / 16384 x 4096 x 11008: 128 x 256
+// tiles 52.7 / 338 us (waves of 64 x 128: 53.7 / 338), two waves of 128 x 128 a
+// tile 65.7 / 348, 256 x 256 tiles, one to a CU, running on from tile to tile 64
+// / 332, 128 x 128 tiles 55.9 / -.
 template <int WR, int WC, int FA, int FB, int kStages, int kOut, bool kBias, bool kNt>
 __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(MxGemm g) {
   constexpr int kWaves = WR * WC;
