@@ -15,11 +15,13 @@ from ._lib import (  # noqa: F401
     gift_prepare_factor, gift_refresh_factors, gift_refresh_group_workspace_bytes,
     gift_whiten_quantize_static, gift_static_scratch_bytes, factor_cols, MAX_RANK,
     RANK, MAX_SKETCH, SKETCH_WIDTH, sketch_width_for, BLOCK, DTYPE_F32, DTYPE_BF16, DAMP_FLOOR, DAMP_FLOOR_PLUS_TAIL,
-    SCALE_TENSOR, SCALE_BLOCK128, SCALE_MXFP4, MX_BLOCK, FLAG_NONFINITE, FLAG_ZERO_AMAX, EXPORTS,
+    SCALE_TENSOR, SCALE_BLOCK128, SCALE_MXFP4, MX_BLOCK, FLAG_NONFINITE, FLAG_ZERO_AMAX, FLAG_TARGET, EXPORTS,
     COEF_ALPHA, COEF_BETA, COEF_LAMBDA_ISO, COEF_LAMBDA_FLOOR, COEF_TRACE, COEF_SIGMA2_TAIL,
     COEF_DW, COEF_DU, COEF_COUNT,
     MxOperand, gift_mx_bytes, gift_mx_quantize, gift_mx_dequantize, gift_mx_matmul,
     gift_mx_matmul_workspace_bytes, gift_mx_linear, gift_mx_linear_workspace_bytes,
     NORM_LAYER, NORM_RMS, gift_norm_forward, gift_norm_backward,
     gift_norm_backward_workspace_bytes,
+    gift_xent_forward, gift_xent_forward_workspace_bytes, gift_xent_backward,
+    gift_xent_backward_workspace_bytes,
 )

@@ -32,7 +32,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 DAMP_FLOOR, DAMP_FLOOR_PLUS_TAIL = 0, 1
 SCALE_TENSOR, SCALE_BLOCK128, SCALE_MXFP4 = 0, 1, 2
 MX_BLOCK = 32
-FLAG_NONFINITE, FLAG_ZERO_AMAX = 1, 2
+FLAG_NONFINITE, FLAG_ZERO_AMAX, FLAG_TARGET = 1, 2, 4
 OP_WHITEN_QUANTIZE, OP_DEQUANT_UNWHITEN, OP_EUCLID_ROUNDTRIP, OP_ROUNDTRIP_ERROR = 0, 1, 2, 3
 OP_UNWHITEN_F32 = 4
 
@@ -59,6 +59,8 @@ EXPORTS = (
     "gift_mx_bytes", "gift_mx_quantize", "gift_mx_dequantize", "gift_mx_matmul",
     "gift_mx_matmul_workspace_bytes", "gift_mx_linear", "gift_mx_linear_workspace_bytes",
     "gift_norm_forward", "gift_norm_backward", "gift_norm_backward_workspace_bytes",
+    "gift_xent_forward", "gift_xent_forward_workspace_bytes", "gift_xent_backward",
+    "gift_xent_backward_workspace_bytes",
 )
 
 
@@ -140,6 +142,11 @@ def load():
         "gift_norm_forward": (I, [P, I, I64, I64, I, P, P, F, P, P, P, P]),
         "gift_norm_backward": (I, [P, P, I, I64, I64, I, P, P, P, P, P, P, I, P, SZ, P]),
         "gift_norm_backward_workspace_bytes": (SZ, [I64, I64]),
+        "gift_xent_forward": (I, [P, I64, I64, I64, P, I64, I64, P, P, P, P, P, SZ, P]),
+        "gift_xent_forward_workspace_bytes": (SZ, [I64, I64, I64]),
+        "gift_xent_backward": (I, [P, I64, I64, I64, P, I64, I64, P, P, P, P, I64, P, I, I64, I, P, SZ,
+                                   P]),
+        "gift_xent_backward_workspace_bytes": (SZ, [I64, I64, I64, I, I, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -886,3 +893,85 @@ def gift_norm_backward(dy, x, weight, mean, rstd, kind=NORM_LAYER, dx=None, dwei
              None if mean is None else _vector(mean, rows, "mean", dev),
              _vector(rstd, rows, "rstd", dev), xp, wp, bp, 1 if accumulate else 0, sp, sb)
     return dx, dweight, dbias
+
+
+# --------------------------------------------------------------------------
+# a training step around its layers
+# --------------------------------------------------------------------------
+
+def _xent_inputs(x, w, targets):
+    """-> pointers and sizes of the tokens, the head and the targets"""
+    xp, _, rows, d, ldx = _matrix(x, "x", dtype=torch.bfloat16)
+    wp, _, vocab, have, ldw = _matrix(w, "w", x.device, dtype=torch.bfloat16)
+    if have != d:
+        raise ValueError("x has %d columns, w %d" % (d, have))
+    if targets.dtype != torch.int64 or targets.device != x.device or targets.shape != (rows,) or \
+            not targets.is_contiguous():
+        raise ValueError("targets must be %d contiguous int64 elements on %s" % (rows, x.device))
+    return (xp, rows, d, ldx, wp, vocab, ldw, targets.data_ptr()), rows, d, vocab
+
+
+def gift_xent_forward_workspace_bytes(rows, d, vocab):
+    return int(load().gift_xent_forward_workspace_bytes(rows, d, vocab))
+
+
+def gift_xent_forward(x, w, targets, loss=None, lse=None, flags=None, ws=None, stream=None):
+    """Softmax cross entropy of tokens x (rows x d) against a head w (vocab x
+    d), both bf16, logits not stored; targets: rows int64, negative ones left
+    out.  -> (loss, lse), rows fp32 each."""
+    if stream is not None:
+        return _on(stream, x.device, gift_xent_forward, x, w, targets, loss, lse, flags, ws)
+    args, rows, d, vocab = _xent_inputs(x, w, targets)
+    dev = x.device
+    if loss is None:
+        loss = _f32(rows, dev)
+    if lse is None:
+        lse = _f32(rows, dev)
+    lib = load()
+    keep, sp, sb = _scratch(lib.gift_xent_forward_workspace_bytes(rows, d, vocab), dev, ws)
+    _enqueue(dev, lib.gift_xent_forward, *args, _vector(loss, rows, "loss", dev), _vector(lse, rows, "lse", dev),
+             None if flags is None else _flags_ptr(flags, dev), sp, sb)
+    return loss, lse
+
+
+def gift_xent_backward_workspace_bytes(rows, d, vocab, dx=True, dw=True, dtype=torch.float32):
+    return int(load().gift_xent_backward_workspace_bytes(rows, d, vocab, 1 if dx else 0, 1 if dw else 0,
+                                                         _DTYPES[dtype]))
+
+
+def gift_xent_backward(x, w, targets, lse, dloss=None, dx=None, dw=None, dtype=torch.float32, accumulate=False,
+                       ws=None, stream=None):
+    """Gradients of sum(dloss * loss) for the lse of gift_xent_forward; dloss:
+    rows fp32 or None (1).  dx (bf16), dw (of dtype, or the given one's): a
+    tensor to fill, False to leave out, None to allocate; accumulate adds to
+    the given fp32 dw.  -> (dx, dw), None for what was left out."""
+    if stream is not None:
+        return _on(stream, x.device, gift_xent_backward, x, w, targets, lse, dloss, dx, dw, dtype, accumulate, ws)
+    args, rows, d, vocab = _xent_inputs(x, w, targets)
+    dev = x.device
+    if accumulate and (dw is None or dw is False):
+        raise ValueError("accumulate adds to a given dw")
+    xp = wp = None
+    ldx = ldw = 0
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("dtype must be bf16 or fp32, got %s" % dtype)
+    if dx is None:
+        dx = torch.empty((rows, d), dtype=torch.bfloat16, device=dev)
+    if dx is False:
+        dx = None
+    else:
+        xp, _, _, _, ldx = _matrix(dx, "dx", dev, (rows, d), torch.bfloat16)
+    if dw is None:
+        dw = torch.empty((vocab, d), dtype=dtype, device=dev)
+    if dw is False:
+        dw = None
+    else:
+        wp, code, _, _, ldw = _matrix(dw, "dw", dev, (vocab, d))
+    lib = load()
+    need = lib.gift_xent_backward_workspace_bytes(rows, d, vocab, 1 if xp else 0, 1 if wp else 0, code)
+    keep, sp, sb = _scratch(need, dev, ws)
+    _enqueue(dev, lib.gift_xent_backward, *args, _vector(lse, rows, "lse", dev),
+             None if dloss is None else _vector(dloss, rows, "dloss", dev), xp, ldx, wp, code, ldw,
+             1 if accumulate else 0, sp, sb)
+    return dx, dw

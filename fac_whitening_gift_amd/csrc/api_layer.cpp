@@ -1,41 +1,18 @@
 // Entry points of a layer's training step in MXFP4 and of the norm
 // (gift_mx_*, gift_norm_* of include/gift.h): argument validation, then the
 // launchers of mx.hip and norm.hip.
-#include "host.hpp"
+#include "checks.hpp"
 #include "mx.hpp"
 
 using namespace gift;
 
 namespace {
 
-bool dtype_ok(int t) { return t == GIFT_DTYPE_F32 || t == GIFT_DTYPE_BF16; }
-size_t dtype_size(int t) { return t == GIFT_DTYPE_BF16 ? 2 : 4; }
-bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
-
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m; }
-
-bool size_ok(int64_t rows, int64_t cols) {
-  return rows >= 1 && cols >= 1 && rows <= kMaxDim && cols <= kMaxDim && rows * cols <= kMaxElems;
-}
 
 // padded elements of an operand
 bool mx_size_ok(int64_t rows, int64_t k) {
   return size_ok(rows, k) && up(rows, kMxRows) * up(k, kMxStep) <= kMaxElems / (kMxRows * kMxStep);
-}
-
-// A dense or strided rows x cols matrix.
-gift_status check_matrix(const char* name, const void* p, int dtype, int64_t rows, int64_t cols,
-                         int64_t ld) {
-  if (!dtype_ok(dtype)) return fail(GIFT_ERR_INVALID_ARG, "%s: unknown dtype %d", name, dtype);
-  if (!size_ok(rows, cols))
-    return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%s: %lld x %lld out of range", name, (long long)rows,
-                (long long)cols);
-  if (ld < cols || ld > (int64_t(1) << 40))
-    return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%s: leading dimension %lld for rows of %lld", name,
-                (long long)ld, (long long)cols);
-  if (!p || !aligned_to(p, dtype_size(dtype)))
-    return fail(GIFT_ERR_INVALID_ARG, "%s is NULL or not aligned to its elements", name);
-  return GIFT_OK;
 }
 
 gift_status check_mx(const char* name, const gift_mx* m) {
@@ -47,22 +24,6 @@ gift_status check_mx(const char* name, const gift_mx* m) {
     return fail(GIFT_ERR_INVALID_ARG, "%s: data is NULL or not 16-byte aligned", name);
   return GIFT_OK;
 }
-
-gift_status check_flags(const uint32_t* f) {
-  return aligned_to(f, 4) ? GIFT_OK : fail(GIFT_ERR_INVALID_ARG, "dev_flags must be 4-byte aligned");
-}
-
-gift_status check_vec(const char* name, const float* p) {
-  return aligned_to(p, 4) ? GIFT_OK : fail(GIFT_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
-}
-
-#define GIFT_TRY(x)                        \
-  do {                                     \
-    const gift_status try_s = (x);         \
-    if (try_s != GIFT_OK) return try_s;    \
-  } while (0)
-
-gift_status launched(hipError_t e) { return e == hipSuccess ? GIFT_OK : hip_fail(e, "kernel launch"); }
 
 // Workspace of gift_mx_linear: X's operand, then the product's.
 size_t linear_ws(int64_t rows, int64_t n, int64_t k) {

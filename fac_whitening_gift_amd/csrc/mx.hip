@@ -9,10 +9,10 @@
 // the instruction picks by its byte select, so neither codes nor scales need
 // any rearranging between memory and the matrix cores.
 #include <type_traits>
-#include <utility>
 
 #include "device.hpp"
 #include "mx.hpp"
+#include "product.hpp"
 
 namespace gift {
 
@@ -234,34 +234,6 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
 // product
 // ---------------------------------------------------------------------------
 
-// 16 (or 4) bytes per lane from the raw buffer (at voff) into LDS at m0 +
-// 16 (4) lane.  Written in asm so that the compiler does not make every LDS
-// read wait for all copies in flight: the kernel waits with explicit vmcnt
-// counts.  The instruction writes no VGPR.  A copy reads M0 at the earliest
-// one wait state after a scalar write of it; the compiler adds none inside asm.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(rs) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-constexpr uint32_t kRawBufferWord3 = 0x00020000u;  // gfx9 raw buffer, 32-bit data format
-
-// s_waitcnt immediate (gfx9: vmcnt in bits 3:0 and 15:14, expcnt 6:4,
-// lgkmcnt 11:8), lgkmcnt 0
-constexpr int wait_vm_lgkm0(int vm) { return (vm & 15) | 0x70 | (vm >> 4) << 14; }
-
-__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
-  return ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32) |
-         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
-}
-
 struct MxGemm {
   const uint8_t* A;
   const uint8_t* B;
@@ -277,25 +249,6 @@ struct MxGemm {
   int mode;        // kOut*
 };
 enum { kOutBf16 = 0, kOutF32 = 1, kOutAcc = 2 };
-
-// Tile of a workgroup: workgroups go to the XCDs in turn, so XCD x takes the
-// x-th contiguous run of the tiles in an order that walks bands of 8 tile
-// rows column by column: the tiles running together on one XCD (64 of 128 x
-// 256: 8 x 8) share operand panels in its L2.
-__device__ __forceinline__ void mx_tile(int id, int tm, int tn, int& ti, int& tj) {
-  const int n = tm * tn, q = n / kXcd, rem = n % kXcd, x = id % kXcd;
-  const int u = x * q + (x < rem ? x : rem) + id / kXcd;
-  constexpr int kBand = 8;
-  const int band = u / (kBand * tn), first = band * kBand;
-  const int h = tm - first < kBand ? tm - first : kBand;
-  const int v = u - first * tn;
-  ti = first + v % h;
-  tj = v / h;
-}
-
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);
-}
 
 // Four consecutive columns n .. n + 3 of row m.
 __device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v) {
@@ -323,16 +276,6 @@ __device__ __forceinline__ void mx_store4(const MxGemm& g, int m, int n, f32x4 v
   } else {
     for (int e = 0; e < 4 && n + e < g.N; ++e) p[e] = g.mode == kOutAcc ? p[e] + v[e] : v[e];
   }
-}
-
-template <class F, int... I>
-__device__ __forceinline__ void static_for_seq(F& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-// f(0), ..., f(N - 1) with the index as a constant
-template <int N, class F>
-__device__ __forceinline__ void static_for(F f) {
-  static_for_seq(f, std::make_integer_sequence<int, N>{});
 }
 
 // The product on tiles of (WR FA 16) x (WC FB 16): WR x WC waves, each with
@@ -386,7 +329,7 @@ __global__ __launch_bounds__(64 * WR * WC, FA * FB > 16 ? 2 : 3) void k_mx_gemm(
 
   const int tiles = g.tm * g.tn, split = (int)blockIdx.x / tiles;
   int ti, tj;
-  mx_tile((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
+  tile_of((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
   const int s0 = split * g.per_split, n_steps = min(g.steps, s0 + g.per_split) - s0;
   const int steps = (n_steps + 1) & ~1;
 

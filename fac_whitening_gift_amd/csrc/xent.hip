@@ -1,0 +1,957 @@
+// Softmax cross entropy over a vocabulary (gift_xent_* of include/gift.h): the
+// logits S = X W^T are formed tile by tile on the matrix cores and never
+// stored.
+//
+//   forward    k_xe_gemm<kXeLse> leaves per row and 256 vocabulary columns the
+//              maximum and the sum of exp(s - maximum); k_xe_loss joins them.
+//   backward   per piece of the vocabulary: k_xe_gemm<kXeGrad> forms S again
+//              and stores D = exp(s - lse) - [target] as bf16 operands of the
+//              two products that follow, dX += D W and dW = D^T X.
+//
+// Operands of a product lie in memory either as the caller's rows or packed in
+// the order in which the matrix cores read them: panels of 64 rows, k steps of
+// 32, per panel and step four fragments of 1 KB, of 16 rows x 32 k each.  Lane
+// l of a wave holds row l % 16 of a fragment and eight k elements, the slots of
+// its group l / 16.  A product sums over k in any order as long as both operands
+// agree: operands along d hold k = 8 (l / 16) + e in slot e; operands along the
+// vocabulary and along the tokens hold k = 4 (l / 16) + e in slots e < 4 and
+// 16 + 4 (l / 16) + e - 4 in the rest, which is where the matrix cores leave D.
+#include <type_traits>
+
+#include "host.hpp"
+#include "mx.hpp"
+#include "product.hpp"
+#include "step.hpp"
+
+namespace gift {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(4))) short i16x4;
+typedef __attribute__((ext_vector_type(8))) short i16x8;
+
+constexpr int kFrag = 1024;           // bytes of a fragment: 16 rows x 32 k
+constexpr int kXePanel = 64;          // rows of a panel
+constexpr int kXeStep = 32;           // k elements of a step
+constexpr int kPanelStep = 4 * kFrag; // bytes of a panel's step
+constexpr int kTm = 128, kTn = 256;   // tile
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct XeOperand {
+  const uint8_t* p;
+  int64_t pitch;   // bytes from row to row, 0: packed
+  int64_t width;   // bytes of a row that may be read (not packed)
+  int64_t rows;
+  int steps;       // k steps of a panel (packed)
+};
+
+enum { kXeLse = 0, kXeGrad = 1, kXeBf16 = 2, kXeF32 = 3, kXeAcc = 4 };
+
+struct XeGemm {
+  XeOperand A, B;
+  int64_t M, N;
+  int steps;         // k steps of the sum
+  int wrap;          // B's k steps, repeated where A has more
+  int per_split;     // k steps of a split
+  int n_split;
+  int tm, tn;
+  // kXeLse, kXeGrad: rows are tokens, columns vocabulary
+  const int64_t* targets;
+  int64_t col0;      // vocabulary index of column 0
+  int64_t vocab;
+  float2* part;      // [tile column][M]
+  float* picked;     // target logits
+  const float* lse;
+  const float* dloss;       // per row, or NULL (1)
+  const float* scale;       // one word: the largest |dloss|, or NULL
+  uint8_t* P;        // packed D: rows tokens, k vocabulary; NULL: not wanted
+  int64_t p_steps;
+  uint8_t* Pt;       // packed ratio D^T: rows vocabulary, k tokens; NULL: not wanted
+  int64_t t_steps;   // k steps over the tokens
+  int parts;         // of ratio D^T: 1, or 2 (what the first rounding left behind it)
+  // the rest
+  void* C;
+  int64_t ldc;
+  bool by_row;              // rows are tokens: scaled by dloss, zero where left out; else scaled by *scale
+};
+
+__device__ __forceinline__ f32x4 xe_mfma(const uint4& a, const uint4& b, const f32x4& acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc,
+                                                 0, 0, 0);
+}
+
+// (maximum, sum of exp(s - maximum)) of two sets joined.  A set of -inf alone
+// counts nothing; NaN stays in the sum.
+__device__ __forceinline__ float2 lse_join(const float2& a, const float2& b) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == -__builtin_inff()) return make_float2(m, a.y + b.y);
+  return make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e) +
+                            b.y * __builtin_amdgcn_exp2f((b.x - m) * kLog2e));
+}
+
+// whether a token counts, and then its dloss
+__device__ __forceinline__ bool row_factor(const int64_t* targets, const float* dloss, int64_t vocab, int64_t m,
+                                           float& f) {
+  const int64_t t = targets[m];
+  f = dloss ? dloss[m] : 1.f;
+  return t >= 0 && t < vocab;
+}
+
+template <int kOut>
+__global__ __launch_bounds__(256, 2) void k_xe_gemm(XeGemm g) {
+  constexpr int FA = 8, FB = 4, kStages = 3, kWaves = 4;
+  constexpr int kStage = (kTm + kTn) * 2 * kXeStep;
+  constexpr int kCa = kTm / 16 / kWaves, kCb = kTn / 16 / kWaves, kVm = kCa + kCb;  // a wave's copies of a step
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+
+  const int tiles = g.tm * g.tn, split = (int)blockIdx.x / tiles;
+  int ti, tj;
+  tile_of((int)blockIdx.x - split * tiles, g.tm, g.tn, ti, tj);
+  const int s0 = split * g.per_split, n_steps = min(g.steps, s0 + g.per_split) - s0;
+  const int steps = (n_steps + 1) & ~1;
+
+  // Each operand's rows of the tile as a raw buffer, and for every copy of the
+  // wave its offset from there.  Rows past the operand's last repeat it (what
+  // they give is not used); steps past the last lie outside the buffer and so
+  // become zeros.
+  __amdgpu_buffer_rsrc_t rs[2];
+  uint32_t vo[kVm], stride[2];
+  auto operand = [&](int which, const XeOperand& o, int64_t row0, int frags, int per_wave, uint32_t* v) {
+    uint64_t base;
+    int64_t bytes;
+    if (o.pitch) {
+      const int64_t live = min((int64_t)frags * 16, o.rows - row0);
+      base = reinterpret_cast<uint64_t>(o.p) + row0 * o.pitch;
+      bytes = (live - 1) * o.pitch + o.width;
+      stride[which] = 2 * kXeStep;
+      for (int d = 0; d < per_wave; ++d)
+        v[d] = (uint32_t)(min((int64_t)(w * per_wave + d) * 16 + (lane & 15), live - 1) * o.pitch) + (lane >> 4) * 16;
+    } else {
+      const int64_t panels = (o.rows + kXePanel - 1) / kXePanel - row0 / kXePanel;
+      const int64_t live = min((int64_t)frags / 4, panels), len = (int64_t)o.steps * kPanelStep;
+      base = reinterpret_cast<uint64_t>(o.p) + row0 / kXePanel * len;
+      bytes = live * len;
+      stride[which] = kPanelStep;
+      for (int d = 0; d < per_wave; ++d) {
+        const int f = w * per_wave + d;
+        v[d] = (uint32_t)(min((int64_t)f / 4, live - 1) * len) + f % 4 * kFrag + lane * 16;
+      }
+    }
+    rs[which] = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(uniform64(base)), (short)0,
+                                                  __builtin_amdgcn_readfirstlane((int)(uint32_t)bytes),
+                                                  (int)kRawBufferWord3);
+  };
+  operand(0, g.A, (int64_t)ti * kTm, kTm / 16, kCa, vo);
+  operand(1, g.B, (int64_t)tj * kTn, kTn / 16, kCb, vo + kCa);
+
+  int c_step = 0, c_slot = 0, c_b = s0 % g.wrap;
+  constexpr uint32_t kOutside = 0x80000000u;  // operands of a tile end below 2^31
+  auto copy = [&](auto D) {
+    constexpr int d = decltype(D)::value;
+    const uint32_t to = lds0 + (uint32_t)c_slot * kStage;
+    const bool in = c_step < n_steps;
+    if constexpr (d < kCa)
+      dma16(rs[0], to + (w * kCa + d) * kFrag, vo[d] + (in ? (uint32_t)(s0 + c_step) * stride[0] : kOutside));
+    else
+      dma16(rs[1], to + (kTm / 16 + w * kCb + d - kCa) * kFrag, vo[d] + (in ? (uint32_t)c_b * stride[1] : kOutside));
+  };
+  auto copied = [&] {
+    c_slot = c_slot + 1 == kStages ? 0 : c_slot + 1;
+    ++c_step;
+    c_b = c_b + 1 == g.wrap ? 0 : c_b + 1;
+  };
+
+  struct Frags {
+    uint4 f[FB + FA];  // B's, then A's
+  };
+  const char* rb = lds + (kTm / 16 + w * FB) * kFrag + lane * 16;
+  const char* ra = lds + lane * 16;
+  constexpr int kReads = FA + FB;
+  auto read = [&](auto D, Frags& r, int o) {
+    constexpr int d = decltype(D)::value;
+    const char* at = (d < FB ? rb + d * kFrag : ra + (d - FB) * kFrag) + o;
+    r.f[d] = *reinterpret_cast<const uint4*>(at);
+  };
+
+  f32x4 acc[FA][FB];
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    static_for<kVm>(copy);
+    copied();
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 1) * kVm));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags fr[2];
+  static_for<kReads>([&](auto D) { read(D, fr[0], 0); });
+  int slot = 0;
+  auto step = [&](auto P) {
+    constexpr int p = decltype(P)::value;
+    const int next = slot + 1 == kStages ? 0 : slot + 1;
+    // step i's fragments are in registers, step i + 1's copies have landed
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((kStages - 2) * kVm));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const Frags& r = fr[p];
+    constexpr int kGroups = FA * FB / 4, kSide = kReads + kVm;
+    const int o = next * kStage;
+    static_for<kGroups>([&](auto G) {
+      constexpr int gr = decltype(G)::value;
+      constexpr int s0 = gr * kSide / kGroups, s1 = (gr + 1) * kSide / kGroups;
+      static_for<s1 - s0>([&](auto S) {
+        constexpr int k = s0 + decltype(S)::value;
+        constexpr int c = k * kVm / kSide;  // copies before side op k
+        if constexpr ((k + 1) * kVm / kSide > c) copy(std::integral_constant<int, c>{});
+        else read(std::integral_constant<int, k - c>{}, fr[1 - p], o);
+      });
+      constexpr int i = gr;
+      static_for<4>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        acc[i][j] = xe_mfma(r.f[j], r.f[FB + i], acc[i][j]);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    copied();
+    slot = next;
+  };
+  for (int i = 0; i < steps; i += 2) {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  }
+  // every copy has landed and every wave has read its last fragments: the
+  // stages are free
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  // A lane holds of row m0 + 16 i + lane % 16 the columns n0 + 16 j + 4 (lane / 16) + e
+  const int64_t m0 = (int64_t)ti * kTm, n0 = (int64_t)tj * kTn + w * FB * 16;
+  const int rl = lane & 15, gq = lane >> 4;
+  // of the lane's columns 16 j + e: how many lie in the vocabulary, and which is
+  // a target (one outside the vocabulary is none)
+  const int left = (int)min(g.vocab - g.col0 - n0 - 4 * gq, (int64_t)kTn);
+  auto column = [&](int64_t target) {
+    const int64_t c = target - g.col0 - n0 - 4 * gq;
+    return target < g.vocab && c >= 0 && c < kTn ? (int)c : -1;
+  };
+  if constexpr (kOut == kXeLse) {
+    float2* sums = reinterpret_cast<float2*>(lds);  // [wave][row]
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      const int64_t m = m0 + 16 * i + rl;
+      const int at = m < g.M ? column(g.targets[m]) : -1;
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (16 * j + e == at) g.picked[m] = acc[i][j][e];
+          if (16 * j + e >= left) acc[i][j][e] = -__builtin_inff();
+          top = fmaxf(top, acc[i][j][e]);
+        }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float from = top == -__builtin_inff() ? 0.f : top;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - from) * kLog2e);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (gq == 0) sums[w * kTm + 16 * i + rl] = make_float2(top, sum);
+    }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r < kTm && m0 + r < g.M) {
+      float2 v = sums[r];
+#pragma unroll
+      for (int k = 1; k < kWaves; ++k) v = lse_join(v, sums[k * kTm + r]);
+      g.part[(int64_t)tj * g.M + m0 + r] = v;
+    }
+  } else if constexpr (kOut == kXeGrad) {
+    // D of two row fragments (32 tokens) at a time.  Where it lies is already
+    // the order of P's fragments; those of D^T come out of LDS by the
+    // transposed read, through the wave's own corner of it.
+    constexpr int kRow = FB * 32 + 16;  // bytes of a token's 64 columns, rows 4 banks apart
+    char* stage = lds + w * 32 * kRow;
+    const uint32_t stage0 = lds0 + (uint32_t)(w * 32 * kRow);
+    const float scale = g.Pt && g.scale ? *g.scale : 1.f;
+#pragma unroll
+    for (int i2 = 0; i2 < FA / 2; ++i2) {
+      uint32_t hi[2][FB][2], lo[2][FB][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 2 * i2 + h;
+        const int64_t m = m0 + 16 * i + rl;
+        const int64_t t = m < g.M ? g.targets[m] : -1;
+        const bool live = t >= 0 && t < g.vocab;
+        const int at = column(t);
+        const float lse = live ? g.lse[m] : 0.f, ratio = live && g.dloss ? g.dloss[m] / scale : 1.f;
+        uint32_t d[FB][2];
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            uint32_t b[2], bh[2], bl[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int v = 16 * j + e + k;
+              float x = __builtin_amdgcn_exp2f((acc[i][j][e + k] - lse) * kLog2e);
+              if (v == at) x -= 1.f;
+              if (!live || v >= left) x = 0.f;
+              b[k] = bf16_bits(x);
+              const float y = x * ratio;
+              bh[k] = bf16_bits(y);
+              bl[k] = bf16_bits(y - __uint_as_float(bh[k] << 16));
+            }
+            d[j][e / 2] = b[0] | b[1] << 16;
+            hi[h][j][e / 2] = bh[0] | bh[1] << 16;
+            lo[h][j][e / 2] = bl[0] | bl[1] << 16;
+          }
+        if (g.P) {
+          uint8_t* to = g.P + ((m0 + 16 * i) / kXePanel * g.p_steps + n0 / kXeStep) * kPanelStep +
+                        i % 4 * kFrag + lane * 16;
+#pragma unroll
+          for (int j = 0; j < FB; j += 2)
+            *reinterpret_cast<uint4*>(to + j / 2 * kPanelStep) = make_uint4(d[j][0], d[j][1], d[j + 1][0], d[j + 1][1]);
+        }
+      }
+      if (!g.Pt) continue;
+      for (int part = 0; part < g.parts; ++part) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < FB; ++j)
+            *reinterpret_cast<uint2*>(stage + (16 * h + rl) * kRow + 32 * j + 8 * gq) =
+                part ? make_uint2(lo[h][j][0], lo[h][j][1]) : make_uint2(hi[h][j][0], hi[h][j][1]);
+        asm volatile("" ::: "memory");
+        // group gq reads tokens 4 gq .. +3 (and 16 more): lane s the four
+        // columns 4 (s % 4) of token 4 gq + s / 4, and gets column s of the four
+        const uint32_t from = stage0 + (uint32_t)((4 * gq + (rl >> 2)) * kRow + 8 * (rl & 3));
+        uint8_t* to = g.Pt + (n0 / kXePanel * (g.t_steps * g.parts) + part * g.t_steps + m0 / kXeStep + i2) * kPanelStep +
+                      lane * 16;
+#pragma unroll
+        for (int j = 0; j < FB; ++j) {
+          auto tr = [&](uint32_t at) {
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(uintptr_t)at);
+          };
+          const i16x8 v = __builtin_shufflevector(tr(from + 32 * j), tr(from + 32 * j + 16 * kRow), 0, 1, 2, 3, 4, 5, 6, 7);
+          *reinterpret_cast<uint4*>(to + j * kFrag) = __builtin_bit_cast(uint4, v);
+        }
+        asm volatile("" ::: "memory");
+      }
+    }
+  } else {
+    // Through a wave's own corner of LDS, 16 rows x 256 bytes (bf16: 128) at a
+    // time, to 16-byte stores of whole row segments.
+    constexpr int kSize = kOut == kXeBf16 ? 2 : 4;
+    constexpr int kRowData = FB * 16 * kSize, kRow = kRowData + 16;
+    constexpr int kLanes = kRowData / 16, kE = 16 / kSize;
+    using T = std::conditional_t<kOut == kXeBf16, uint16_t, float>;
+    char* stage = lds + w * 16 * kRow;
+    const int sr = lane / kLanes, sc = lane % kLanes;
+    T* C = static_cast<T*>(g.C) + (int64_t)split * g.M * g.N + (m0 + sr) * g.ldc + n0 + sc * kE;
+    const float all = !g.by_row && g.scale ? *g.scale : 1.f;
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      float f = all;
+      bool out = false;
+      if (g.by_row) out = !row_factor(g.targets, g.dloss, g.vocab, min(m0 + 16 * i + rl, g.M - 1), f);
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+        f32x4 v = acc[i][j] * f;
+        if (out) v = f32x4{0.f, 0.f, 0.f, 0.f};
+        char* to = stage + rl * kRow + (16 * j + 4 * gq) * kSize;
+        if constexpr (kOut == kXeBf16)
+          *reinterpret_cast<uint2*>(to) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                     bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+        else *reinterpret_cast<f32x4*>(to) = v;
+      }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < kLanes / 4; ++t) {
+        const int r = t * (64 / kLanes);
+        const int64_t m = m0 + 16 * i + r + sr, n = n0 + sc * kE;
+        const uint4 q = *reinterpret_cast<const uint4*>(stage + (r + sr) * kRow + sc * 16);
+        if (m >= g.M || n >= g.N) continue;
+        T* p = C + (int64_t)(16 * i + r) * g.ldc;
+        if (n + kE <= g.N) {
+          if constexpr (kOut == kXeAcc)
+            st16(p, __builtin_bit_cast(uint4, __builtin_bit_cast(f32x4, ld16(p)) + __builtin_bit_cast(f32x4, q)));
+          else st16(p, q);
+        } else {
+          T o[kE];
+          __builtin_memcpy(o, &q, 16);
+#pragma unroll
+          for (int e = 0; e < kE; ++e)
+            if (n + e < g.N) {
+              if constexpr (kOut == kXeAcc) p[e] += o[e];
+              else p[e] = o[e];
+            }
+        }
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// operands
+// ---------------------------------------------------------------------------
+
+// The operand of M^T: rows of it are M's columns, k M's rows first, first + 1,
+// ...; rows past `end`, and those of tokens left out, are zeros whatever M holds.
+// A 64 x 64 tile of M per workgroup through LDS and its transposed read.
+__global__ __launch_bounds__(256) void k_xe_pack_t(XeMatrix a, int64_t first, int64_t end, const int64_t* targets,
+                                                   int64_t vocab, uint8_t* out, int64_t steps) {
+  constexpr int kRow = 144;
+  __shared__ __attribute__((aligned(16))) char lds[64 * kRow];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int64_t c0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 64;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (t + 256 * i) >> 3, c = (t & 7) * 8;
+    const int64_t row = first + r0 + r;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    bool in = row < end;
+    if (in && targets) {
+      const int64_t x = targets[row];
+      in = x >= 0 && x < vocab;
+    }
+    if (in) {
+      const uint16_t* p = a.p + row * a.ld + c0 + c;
+      if (c0 + c + 8 <= a.cols) {
+        v = ld16(p);
+      } else {
+        uint16_t e[8] = {};
+        for (int j = 0; j < 8; ++j)
+          if (c0 + c + j < a.cols) e[j] = p[j];
+        __builtin_memcpy(&v, e, 16);
+      }
+    }
+    *reinterpret_cast<uint4*>(lds + r * kRow + c * 2) = v;
+  }
+  __syncthreads();
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  const uint32_t from = lds0 + (uint32_t)((4 * (lane >> 4) + (lane & 15) / 4) * kRow + 32 * w + 8 * (lane & 3));
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int64_t step = (int64_t)blockIdx.y * 2 + s;
+    if (step >= steps) break;
+    auto tr = [&](uint32_t at) {
+      return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(uintptr_t)at);
+    };
+    const i16x8 v = __builtin_shufflevector(tr(from + 32 * s * kRow), tr(from + (32 * s + 16) * kRow), 0, 1, 2, 3, 4, 5, 6, 7);
+    *reinterpret_cast<uint4*>(out + ((int64_t)blockIdx.x * steps + step) * kPanelStep + w * kFrag + lane * 16) =
+        __builtin_bit_cast(uint4, v);
+  }
+}
+
+// The operand of M's rows first, ..., end - 1 along their columns, for matrices
+// whose rows the copies cannot read where they lie: a 16-byte chunk per thread.
+__global__ __launch_bounds__(256) void k_xe_pack(XeMatrix a, int64_t first, int64_t end, uint8_t* out, int64_t steps) {
+  const int64_t panel = blockIdx.y, step = blockIdx.x;
+  const int t = threadIdx.x;
+  const int64_t row = first + panel * kXePanel + (t >> 6) * 16 + (t & 15);
+  const int64_t k = step * kXeStep + ((t & 63) >> 4) * 8;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (row < end) {
+    const uint16_t* p = a.p + row * a.ld + k;
+    if (k + 8 <= a.cols) {
+      v = ld16(p);
+    } else {
+      uint16_t e[8] = {};
+      for (int j = 0; j < 8; ++j)
+        if (k + j < a.cols) e[j] = p[j];
+      __builtin_memcpy(&v, e, 16);
+    }
+  }
+  *reinterpret_cast<uint4*>(out + (panel * steps + step) * kPanelStep + t * 16) = v;
+}
+
+// ---------------------------------------------------------------------------
+// the rest
+// ---------------------------------------------------------------------------
+
+// lse and loss of 32 rows per workgroup: eight threads a row join its parts in
+// turn, then the first of them the eight.
+__global__ __launch_bounds__(256) void k_xe_loss(const float2* part, int64_t parts, int64_t rows, const int64_t* targets,
+                                                 int64_t vocab, const float* picked, float* loss, float* lse,
+                                                 uint32_t* flags) {
+  __shared__ float2 s[8][32];
+  const int r = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int64_t m = (int64_t)blockIdx.x * 32 + r;
+  float2 v = make_float2(-__builtin_inff(), 0.f);
+  if (m < rows)
+    for (int64_t i = k; i < parts; i += 8) v = lse_join(v, part[i * rows + m]);
+  s[k][r] = v;
+  __syncthreads();
+  if (k || m >= rows) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v = lse_join(v, s[i][r]);
+  const float more = logf(v.y);
+  const int64_t t = targets[m];
+  const bool live = t >= 0 && t < vocab;
+  const float l = live ? v.x - picked[m] + more : 0.f;
+  if (lse) lse[m] = v.x + more;
+  if (loss) loss[m] = l;
+  const uint32_t f = (live && abs_bits(l) >= 0x7f800000u ? GIFT_FLAG_NONFINITE : 0) | (t >= vocab ? GIFT_FLAG_TARGET : 0);
+  if (flags && f) atomicOr(flags, f);
+}
+
+// The largest |dloss| of the tokens that count, 1 where it is 0 or not finite.
+// D is rounded to bf16 as it is for dX, whose rows take dloss in fp32; for dW
+// dloss multiplies each token's D before the rounding, divided by this, so that
+// equal weights (a mean's 1 / n) do not shift every value by the same rounding.
+__global__ __launch_bounds__(1024) void k_xe_scale(const float* dloss, const int64_t* targets, int64_t rows, int64_t vocab,
+                                                   float* scale) {
+  __shared__ uint32_t s[16];
+  uint32_t top = 0;
+  for (int64_t m = threadIdx.x; m < rows; m += 1024) {
+    const int64_t t = targets[m];
+    if (t >= 0 && t < vocab) top = max(top, abs_bits(dloss[m]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < 16; ++i) top = max(top, s[i]);
+  *scale = top == 0 || top >= 0x7f800000u ? 1.f : __uint_as_float(top);
+}
+
+// C = the slots' sums, added in order, scaled (and added to C).  Four columns a
+// thread.
+template <int kOut>
+__global__ __launch_bounds__(256) void k_xe_reduce(XeGemm g, const float* slots) {
+  const int64_t n4 = (g.N + 3) / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4 * g.M; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / n4, n = (i - m * n4) * 4;
+    const bool whole = n + 4 <= g.N;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < g.n_split; ++s) {
+      const float* p = slots + ((int64_t)s * g.M + m) * g.N + n;
+      if (whole) v += __builtin_bit_cast(f32x4, ld16(p));
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) v[e] += p[e];
+    }
+    float f = !g.by_row && g.scale ? *g.scale : 1.f;
+    const bool in = !g.by_row || row_factor(g.targets, g.dloss, g.vocab, m, f);
+    v *= f;
+    if (!in) v = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (kOut == kXeBf16) {
+      uint16_t* p = static_cast<uint16_t*>(g.C) + m * g.ldc + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < g.N) p[e] = (uint16_t)bf16_bits(v[e]);
+    } else {
+      float* p = static_cast<float*>(g.C) + m * g.ldc + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < g.N) p[e] = kOut == kXeAcc ? p[e] + v[e] : v[e];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (a token scored, a small batch): a wave owns 16 vocabulary columns
+// and all of d, straight from memory into the matrix operands.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 64, kFewWaves = 8;
+
+template <int FM>
+__global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, XeMatrix W, const int64_t* targets, float2* part,
+                                                           float* picked) {
+  constexpr int kU = FM == 4 ? 4 : 8;  // k steps in flight
+  __shared__ float2 sums[kFewWaves][16 * FM];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, rl = lane & 15, gq = lane >> 4;
+  const int64_t v0 = ((int64_t)blockIdx.x * kFewWaves + w) * 16;
+  const int64_t d = X.cols;
+  f32x4 acc[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (v0 < W.rows) {
+    const uint16_t* wp = W.p + min(v0 + rl, W.rows - 1) * W.ld + 8 * gq;
+    const uint16_t* xp[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) xp[i] = X.p + min((int64_t)16 * i + rl, X.rows - 1) * X.ld + 8 * gq;
+    const int whole = (int)(d / kXeStep);
+    int s = 0;
+    for (; s + kU <= whole; s += kU) {
+      uint4 b[kU], a[kU][FM];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        b[u] = ld16(wp + (s + u) * kXeStep);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[u][i] = ld16(xp[i] + (s + u) * kXeStep);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b[u], a[u][i], acc[i]);
+    }
+    for (; s * kXeStep < d; ++s) {
+      auto load = [&](const uint16_t* p) {
+        const int64_t n = d - (int64_t)s * kXeStep - 8 * gq;  // elements left
+        if (n >= 8) return ld16(p + s * kXeStep);
+        uint16_t e[8] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) e[j] = p[s * kXeStep + j];
+        return __builtin_bit_cast(uint4, *reinterpret_cast<i16x8*>(e));
+      };
+      const uint4 b = load(wp);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b, load(xp[i]), acc[i]);
+    }
+  }
+  const int64_t left = W.rows - v0 - 4 * gq;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = 16 * i + rl;
+    const int64_t t = m < X.rows ? targets[m] : -1;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e >= left) acc[i][e] = -__builtin_inff();
+      else if (t >= 0 && v0 + 4 * gq + e == t) picked[m] = acc[i][e];
+      top = fmaxf(top, acc[i][e]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float from = top == -__builtin_inff() ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((acc[i][e] - from) * kLog2e);
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (gq == 0) sums[w][m] = make_float2(top, sum);
+  }
+  __syncthreads();
+  const int m = threadIdx.x;
+  if (m < 16 * FM && m < X.rows) {
+    float2 v = sums[0][m];
+#pragma unroll
+    for (int k = 1; k < kFewWaves; ++k) v = lse_join(v, sums[k][m]);
+    part[(int64_t)blockIdx.x * X.rows + m] = v;
+  }
+}
+
+hipError_t done() { return hipGetLastError(); }
+
+int64_t up_div(int64_t x, int64_t m) { return (x + m - 1) / m; }
+size_t operand_bytes(int64_t rows, int64_t steps) { return align_up((size_t)(up_div(rows, kXePanel) * steps) * kPanelStep); }
+
+// Rows that the copies can read where they lie: 16-byte chunks, whole k steps,
+// and a tile of them within a buffer of 2^31 bytes.
+bool readable(const XeMatrix& a) {
+  return (uintptr_t)a.p % 16 == 0 && a.ld % 8 == 0 && a.cols % kXeStep == 0 && a.ld < (1 << 21);
+}
+XeOperand as_rows(const XeMatrix& a, int64_t first, int64_t rows) {
+  XeOperand o{};
+  o.p = reinterpret_cast<const uint8_t*>(a.p + first * a.ld);
+  o.pitch = 2 * a.ld;
+  o.width = 2 * a.cols;
+  o.rows = rows;
+  return o;
+}
+XeOperand as_packed(const uint8_t* p, int64_t rows, int64_t steps) {
+  XeOperand o{};
+  o.p = p;
+  o.rows = rows;
+  o.steps = (int)steps;
+  return o;
+}
+
+// A matrix as an operand along its columns: where it lies, or packed into ws.
+XeOperand row_operand(const XeMatrix& a, int64_t first, int64_t rows, uint8_t* ws, hipStream_t s) {
+  if (readable(a)) return as_rows(a, first, rows);
+  const int64_t steps = up_div(a.cols, kXeStep);
+  k_xe_pack<<<dim3((uint32_t)steps, (uint32_t)up_div(rows, kXePanel)), dim3(256), 0, s>>>(a, first, first + rows, ws, steps);
+  return as_packed(ws, rows, steps);
+}
+
+void sized(XeGemm& g, int64_t M, int64_t N, int64_t steps, int split) {
+  g.M = M;
+  g.N = N;
+  g.steps = (int)steps;
+  g.wrap = (int)steps;
+  g.per_split = (int)up_div(steps, split);
+  g.n_split = (int)up_div(steps, g.per_split);
+  g.tm = (int)up_div(M, kTm);
+  g.tn = (int)up_div(N, kTn);
+}
+template <int kOut>
+void launch_gemm(const XeGemm& g, hipStream_t s) {
+  k_xe_gemm<kOut><<<dim3((uint32_t)(g.tm * g.tn * g.n_split)), dim3(256), 0, s>>>(g);
+}
+
+// Ways to split a sum of `steps` k steps: enough workgroups to fill the chip
+// (two a CU), at least 8 steps each.
+int splits(int64_t M, int64_t N, int64_t steps) {
+  const int64_t tiles = up_div(M, kTm) * up_div(N, kTn);
+  int64_t n = 512 / tiles;
+  if (n > steps / 8) n = steps / 8;
+  if (n > 32) n = 32;
+  return n < 1 ? 1 : (int)n;
+}
+
+// rows of a forward launch: their parts of the sums stay within 256 MB
+int64_t chunk_rows(int64_t rows, int64_t vocab) {
+  const int64_t most = (int64_t(1) << 25) / up_div(vocab, kTn) / kTm * kTm;
+  return rows < most ? rows : most;
+}
+
+struct Carve {
+  uint8_t* p;
+  size_t at;
+  template <class T>
+  T* take(size_t bytes) {
+    T* r = p ? reinterpret_cast<T*>(p + at) : nullptr;
+    at += align_up(bytes);
+    return r;
+  }
+};
+
+struct XeFwdWs {
+  float2* part;
+  float* picked;
+  uint8_t* x;
+  uint8_t* w;
+};
+XeFwdWs forward_plan(int64_t rows, int64_t d, int64_t vocab, Carve& c) {
+  XeFwdWs r{};
+  r.picked = c.take<float>(rows * 4);
+  if (rows <= kFewRows) {
+    r.part = c.take<float2>(up_div(vocab, 16 * kFewWaves) * rows * 8);
+    return r;
+  }
+  r.part = c.take<float2>(up_div(vocab, kTn) * chunk_rows(rows, vocab) * 8);
+  r.x = c.take<uint8_t>(operand_bytes(rows, up_div(d, kXeStep)));
+  r.w = c.take<uint8_t>(operand_bytes(vocab, up_div(d, kXeStep)));
+  return r;
+}
+
+struct XeBwdPlan {
+  int64_t piece;     // vocabulary columns at a time
+  int n_piece;
+  int parts;         // of the dW operand
+  int dx_split, dw_split;
+  float* scale;
+  uint8_t *P, *Pt, *Wt, *Xt, *x, *w;
+  float *dx_slots, *dw_slots;
+};
+XeBwdPlan backward_plan(int64_t rows, int64_t d, int64_t vocab, bool dx, bool dw, int dw_dtype, Carve& c) {
+  XeBwdPlan r{};
+  const int64_t tall = up_div(rows, kTm) * kTm, wide = up_div(vocab, kTn) * kTn, tokens = tall / kXeStep;
+  const int64_t k = up_div(d, kXeStep);
+  // pieces of equal width, D of about 2^28 elements
+  int64_t most = (int64_t(1) << 28) / tall / kTn * kTn;
+  if (most < kTn) most = kTn;
+  r.n_piece = (int)up_div(wide, most);
+  r.piece = up_div(up_div(wide, r.n_piece), kTn) * kTn;
+  r.n_piece = (int)up_div(wide, r.piece);
+  r.parts = dw_dtype == GIFT_DTYPE_F32 ? 2 : 1;
+  r.scale = c.take<float>(4);
+  r.x = c.take<uint8_t>(operand_bytes(rows, k));
+  r.w = c.take<uint8_t>(operand_bytes(r.piece, k));
+  if (dx) {
+    r.P = c.take<uint8_t>(operand_bytes(tall, r.piece / kXeStep));
+    r.Wt = c.take<uint8_t>(operand_bytes(d, r.piece / kXeStep));
+    r.dx_split = splits(rows, d, r.piece / kXeStep);
+    if (r.dx_split > 1 || r.n_piece > 1) r.dx_slots = c.take<float>((size_t)r.dx_split * rows * d * 4);
+  }
+  if (dw) {
+    r.Pt = c.take<uint8_t>(operand_bytes(r.piece, tokens * r.parts));
+    r.Xt = c.take<uint8_t>(operand_bytes(d, tokens));
+    r.dw_split = splits(r.piece, d, tokens * r.parts);
+    if (r.dw_split > 1) r.dw_slots = c.take<float>((size_t)r.dw_split * r.piece * d * 4);
+  }
+  return r;
+}
+
+uint32_t quads(int64_t M, int64_t N) {
+  const int64_t n = up_div(M * up_div(N, 4), 256);
+  return (uint32_t)(n < 1 << 20 ? n : 1 << 20);
+}
+
+}  // namespace
+
+size_t xent_forward_ws(int64_t rows, int64_t d, int64_t vocab) {
+  Carve c{nullptr, 0};
+  forward_plan(rows, d, vocab, c);
+  return c.at;
+}
+
+hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64_t* targets, float* loss, float* lse,
+                               uint32_t* flags, void* ws, hipStream_t s) {
+  Carve c{static_cast<uint8_t*>(ws), 0};
+  const int64_t rows = X.rows, vocab = W.rows;
+  const XeFwdWs p = forward_plan(rows, X.cols, vocab, c);
+  auto join = [&](int64_t first, int64_t n, int64_t parts) {
+    k_xe_loss<<<dim3((uint32_t)up_div(n, 32)), dim3(256), 0, s>>>(p.part, parts, n, targets + first, vocab, p.picked + first,
+                                                                  loss ? loss + first : nullptr,
+                                                                  lse ? lse + first : nullptr, flags);
+  };
+  if (rows <= kFewRows) {
+    const int64_t groups = up_div(vocab, 16 * kFewWaves);
+    const dim3 grid((uint32_t)groups), block(64 * kFewWaves);
+    if (rows <= 16) k_xe_few<1><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
+    else if (rows <= 32) k_xe_few<2><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
+    else k_xe_few<4><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
+    hipError_t e = done();
+    if (e != hipSuccess) return e;
+    join(0, rows, groups);
+    return done();
+  }
+  const XeOperand w = row_operand(W, 0, vocab, p.w, s);
+  const XeOperand x = row_operand(X, 0, rows, p.x, s);
+  const int64_t chunk = chunk_rows(rows, vocab);
+  for (int64_t first = 0; first < rows; first += chunk) {
+    const int64_t n = rows - first < chunk ? rows - first : chunk;
+    XeGemm g{};
+    sized(g, n, vocab, up_div(X.cols, kXeStep), 1);
+    g.A = x;
+    g.A.rows = n;
+    g.A.p += x.pitch ? first * x.pitch : first / kXePanel * x.steps * kPanelStep;
+    g.B = w;
+    g.targets = targets + first;
+    g.vocab = vocab;
+    g.part = p.part;
+    g.picked = p.picked + first;
+    launch_gemm<kXeLse>(g, s);
+    hipError_t e = done();
+    if (e != hipSuccess) return e;
+    join(first, n, g.tn);
+  }
+  return done();
+}
+
+size_t xent_backward_ws(int64_t rows, int64_t d, int64_t vocab, bool dx, bool dw, int dw_dtype) {
+  Carve c{nullptr, 0};
+  backward_plan(rows, d, vocab, dx, dw, dw_dtype, c);
+  return c.at;
+}
+
+hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int64_t* targets, const float* lse,
+                                const float* dloss, const XeGrad& o, void* ws, hipStream_t s) {
+  Carve c{static_cast<uint8_t*>(ws), 0};
+  const int64_t rows = X.rows, d = X.cols, vocab = W.rows;
+  const XeBwdPlan p = backward_plan(rows, d, vocab, o.dX, o.dW, o.dw_dtype, c);
+  const int64_t tokens = up_div(rows, kTm) * kTm / kXeStep, k = up_div(d, kXeStep);
+  const float* scale = o.dW && dloss ? p.scale : nullptr;
+  if (scale) k_xe_scale<<<dim3(1), dim3(1024), 0, s>>>(dloss, targets, rows, vocab, p.scale);
+  const XeOperand x = row_operand(X, 0, rows, p.x, s);
+  auto transposed = [&](const XeMatrix& a, int64_t first, int64_t end, const int64_t* t, uint8_t* out, int64_t steps) {
+    k_xe_pack_t<<<dim3((uint32_t)up_div(a.cols, 64), (uint32_t)up_div(steps, 2)), dim3(256), 0, s>>>(a, first, end, t, vocab,
+                                                                                                   out, steps);
+  };
+  if (o.dW) transposed(X, 0, rows, targets, p.Xt, tokens);
+  hipError_t e = done();
+  if (e != hipSuccess) return e;
+  for (int i = 0; i < p.n_piece; ++i) {
+    const int64_t first = i * p.piece, n = vocab - first < p.piece ? vocab - first : p.piece;
+    const int64_t steps = up_div(n, kTn) * kTn / kXeStep;  // k steps over the piece
+    XeGemm g{};
+    sized(g, rows, n, k, 1);
+    g.A = x;
+    g.B = row_operand(W, first, n, p.w, s);
+    g.targets = targets;
+    g.col0 = first;
+    g.vocab = vocab;
+    g.lse = lse;
+    g.dloss = dloss;
+    g.scale = scale;
+    g.P = o.dX ? p.P : nullptr;
+    g.p_steps = steps;
+    g.Pt = o.dW ? p.Pt : nullptr;
+    g.t_steps = tokens;
+    g.parts = p.parts;
+    launch_gemm<kXeGrad>(g, s);
+    e = done();
+    if (e != hipSuccess) return e;
+    if (o.dX) {
+      transposed(W, first, first + n, nullptr, p.Wt, steps);
+      XeGemm h{};
+      sized(h, rows, d, steps, p.dx_split);
+      h.A = as_packed(p.P, rows, steps);
+      h.B = as_packed(p.Wt, d, steps);
+      if (p.dx_slots) {
+        // each split of every piece adds to its own slot; a short last piece
+        // may need fewer of them
+        h.C = p.dx_slots;
+        h.ldc = d;
+        if (i == 0) launch_gemm<kXeF32>(h, s);
+        else launch_gemm<kXeAcc>(h, s);
+      } else {
+        h.C = o.dX;
+        h.ldc = o.ld_dx;
+        h.by_row = true;
+        h.targets = targets;
+        h.vocab = vocab;
+        h.dloss = dloss;
+        launch_gemm<kXeBf16>(h, s);
+      }
+      e = done();
+      if (e != hipSuccess) return e;
+    }
+    if (o.dW) {
+      XeGemm h{};
+      sized(h, n, d, tokens * p.parts, p.dw_split);
+      h.wrap = (int)tokens;
+      h.A = as_packed(p.Pt, n, tokens * p.parts);
+      h.B = as_packed(p.Xt, d, tokens);
+      const bool bf16 = o.dw_dtype == GIFT_DTYPE_BF16;
+      void* C = static_cast<uint8_t*>(o.dW) + first * o.ld_dw * (bf16 ? 2 : 4);
+      if (p.dw_slots) {
+        h.C = p.dw_slots;
+        h.ldc = d;
+        launch_gemm<kXeF32>(h, s);
+        h.C = C;
+        h.ldc = o.ld_dw;
+        h.scale = scale;
+        const dim3 grid(quads(n, d)), block(256);
+        if (bf16) k_xe_reduce<kXeBf16><<<grid, block, 0, s>>>(h, p.dw_slots);
+        else if (o.accumulate) k_xe_reduce<kXeAcc><<<grid, block, 0, s>>>(h, p.dw_slots);
+        else k_xe_reduce<kXeF32><<<grid, block, 0, s>>>(h, p.dw_slots);
+      } else {
+        h.C = C;
+        h.ldc = o.ld_dw;
+        h.scale = scale;
+        if (bf16) launch_gemm<kXeBf16>(h, s);
+        else if (o.accumulate) launch_gemm<kXeAcc>(h, s);
+        else launch_gemm<kXeF32>(h, s);
+      }
+      e = done();
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (o.dX && p.dx_slots) {
+    XeGemm h{};
+    sized(h, rows, d, p.piece / kXeStep, p.dx_split);
+    h.C = o.dX;
+    h.ldc = o.ld_dx;
+    h.by_row = true;
+    h.targets = targets;
+    h.vocab = vocab;
+    h.dloss = dloss;
+    k_xe_reduce<kXeBf16><<<dim3(quads(rows, d)), dim3(256), 0, s>>>(h, p.dx_slots);
+  }
+  return done();
+}
+
+}  // namespace gift

@@ -101,6 +101,7 @@ enum { GIFT_SCALE_TENSOR = 0, GIFT_SCALE_BLOCK128 = 1, GIFT_SCALE_MXFP4 = 2 };
                                    trace of A was, i.e. X held a NaN or an
                                    infinity, or a square overflowed fp32     */
 #define GIFT_FLAG_ZERO_AMAX 2u  /* a tensor / block was all zero: scale = 1 */
+#define GIFT_FLAG_TARGET 4u     /* a target lay past the vocabulary           */
 
 /* Layout of gift_factor.coef (fp32, GIFT_COEF_COUNT entries) for a factor of
  * 32 storage columns; a factor of 64 columns (rank above 32) has D_w at 8
@@ -505,6 +506,56 @@ gift_status gift_norm_backward(const void *dY, const void *X, int x_dtype, int64
                                const float *rstd, void *dX, float *dweight, float *dbias,
                                int accumulate, void *ws, size_t ws_bytes, void *stream);
 size_t gift_norm_backward_workspace_bytes(int64_t rows, int64_t d);
+
+/* ------------------------------------------------------------------------
+ * A training step around its layers: the loss over the vocabulary, where the
+ * backward pass starts and the head's gradient G comes from.  Matrices as
+ * above: rows may lie apart, element alignment, no overlap of what a call
+ * writes with what it reads.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * gift_xent_forward -- softmax cross entropy of rows x d tokens X against a
+ * head W of vocab x d, both bf16 (element (i, j) at i * ldx + j), without
+ * storing the logits S = X W^T (fp32 sums of the exact products):
+ *   lse[n]  = log sum_v exp(S[n, v])
+ *   loss[n] = lse[n] - S[n, targets[n]]
+ * targets: rows int64.  A row whose target is negative (padding) or past the
+ * vocabulary is left out: its loss is 0 and it takes no part in the
+ * gradients.  loss, lse: rows fp32, either may be NULL, not both.  An
+ * infinite logit of either sign at the target, +inf or NaN anywhere, makes
+ * the row's loss NaN or infinite.  dev_flags (optional): NONFINITE where the
+ * loss of a row that counts is, TARGET where a target lies past the
+ * vocabulary.
+ * 1 <= rows, vocab <= 2^20, 1 <= d <= 2^16.  Up to 64 rows read W once,
+ * straight from memory (the serving form).
+ */
+gift_status gift_xent_forward(const void *X, int64_t rows, int64_t d, int64_t ldx,
+                              const void *W, int64_t vocab, int64_t ldw,
+                              const int64_t *targets, float *loss, float *lse,
+                              uint32_t *dev_flags, void *ws, size_t ws_bytes, void *stream);
+size_t gift_xent_forward_workspace_bytes(int64_t rows, int64_t d, int64_t vocab);
+
+/*
+ * gift_xent_backward -- gradients of sum_n dloss[n] loss[n] for the lse of
+ * the forward pass, the logits formed again piece by piece of the
+ * vocabulary:
+ *   D[n, v] = exp(S[n, v] - lse[n]) - [v = targets[n]]
+ *   dX[n] = dloss[n] sum_v D[n, v] W[v]           (bf16, 0 for rows left out)
+ *   dW[v] = sum_n dloss[n] D[n, v] X[n]           (bf16 or fp32)
+ * dloss: rows fp32, NULL: 1.  dX and dW may each be NULL, not both.
+ * accumulate != 0 (fp32 dW): dW is added to.  Sums are fp32; D enters the
+ * products as bf16, for an fp32 dW as the sum of two.  What a row left out
+ * holds, NaN and infinities among it, is not used.  The order of the sums
+ * depends on the sizes and dW's type alone: equal calls give equal bits.
+ */
+gift_status gift_xent_backward(const void *X, int64_t rows, int64_t d, int64_t ldx,
+                               const void *W, int64_t vocab, int64_t ldw,
+                               const int64_t *targets, const float *lse, const float *dloss,
+                               void *dX, int64_t ld_dx, void *dW, int dw_dtype, int64_t ld_dw,
+                               int accumulate, void *ws, size_t ws_bytes, void *stream);
+size_t gift_xent_backward_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int want_dx,
+                                          int want_dw, int dw_dtype);
 
 const char *gift_status_string(int status);
 /* Thread-local detail of the last failing call on this thread. */
