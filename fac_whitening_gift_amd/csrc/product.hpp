@@ -37,13 +37,13 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t x) {
 }
 
 // Tile of a workgroup: workgroups go to the XCDs in turn, so XCD x takes the
-// x-th contiguous run of the tiles in an order that walks bands of 8 tile
+// x-th contiguous run of the tiles in an order that walks bands of kBand tile
 // rows column by column: the tiles running together on one XCD (64 of 128 x
-// 256: 8 x 8) share operand panels in its L2.
+// 256: 8 x 8; 32 of 256 x 256: 4 x 8) share operand panels in its L2.
+template <int kBand = 8>
 __device__ __forceinline__ void tile_of(int id, int tm, int tn, int& ti, int& tj) {
   const int n = tm * tn, q = n / kXcd, rem = n % kXcd, x = id % kXcd;
   const int u = x * q + (x < rem ? x : rem) + id / kXcd;
-  constexpr int kBand = 8;
   const int band = u / (kBand * tn), first = band * kBand;
   const int h = tm - first < kBand ? tm - first : kBand;
   const int v = u - first * tn;
