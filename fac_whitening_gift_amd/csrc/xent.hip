@@ -75,6 +75,7 @@ struct XeGemm {
   // the rest
   void* C;
   int64_t ldc;
+  const float* add;         // kXeBf16: M x N fp32 sums to add before scaling, or NULL
   bool by_row;              // rows are tokens: scaled by dloss, zero where left out; else scaled by *scale
 };
 
@@ -103,6 +104,18 @@ __device__ __forceinline__ bool row_factor(const int64_t* targets, const float* 
   const int64_t t = targets[m];
   f = dloss ? dloss[m] : 1.f;
   return t >= 0 && t < vocab;
+}
+
+// four of g.add's sums, zeros past the matrix
+__device__ __forceinline__ f32x4 sums_at(const XeGemm& g, int64_t m, int64_t n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  const float* p = g.add + m * g.N + n;
+  if (m >= g.M) return v;
+  if (n + 4 <= g.N) return __builtin_bit_cast(f32x4, ld16(p));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < g.N) v[e] = p[e];
+  return v;
 }
 
 // A workgroup's tile: WR x WC waves of FA x FB fragments.
@@ -403,7 +416,10 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
       if (g.by_row) out = !row_factor(g.targets, g.dloss, g.vocab, min(m0 + 16 * i + rl, g.M - 1), f);
 #pragma unroll
       for (int j = 0; j < FB; ++j) {
-        f32x4 v = acc[i][j] * f;
+        f32x4 v = acc[i][j];
+        if constexpr (kOut == kXeBf16)
+          if (g.add) v += sums_at(g, m0 + 16 * i + rl, n0 + 16 * j + 4 * gq);
+        v *= f;
         if (out) v = f32x4{0.f, 0.f, 0.f, 0.f};
         char* to = stage + rl * kRow + (16 * j + 4 * gq) * kSize;
         if constexpr (kOut == kXeBf16)
@@ -442,24 +458,63 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
 // operands
 // ---------------------------------------------------------------------------
 
-// The operand of M^T: rows of it are M's columns, k M's rows first, first + 1,
-// ...; rows past `end`, and those of tokens left out, are zeros whatever M holds.
-// A 64 x 64 tile of M per workgroup through LDS and its transposed read.
-__global__ __launch_bounds__(256) void k_xe_pack_t(XeMatrix a, int64_t first, int64_t end, const int64_t* targets,
-                                                   int64_t vocab, uint8_t* out, int64_t steps) {
+struct XePack {
+  XeMatrix a;
+  int64_t first, end;       // M: rows first, ..., end - 1 of the matrix
+  const int64_t* targets;   // of M's rows, NULL: all count
+  int64_t vocab;
+  uint8_t* out;             // the operand of M^T
+  int64_t steps;
+  uint8_t* by_row;          // the operand of M beside it, or NULL
+  const float* dloss;       // k_xe_scale's, in a workgroup of its own, or NULL
+  float* scale;
+};
+
+// The largest |dloss| of the tokens that count, 1 where it is 0 or not finite.
+// D is rounded to bf16 as it is for dX, whose rows take dloss in fp32; for dW
+// dloss multiplies each token's D before the rounding, divided by this, so that
+// equal weights (a mean's 1 / n) do not shift every value by the same rounding.
+__device__ __forceinline__ void scale_of(const XePack& q) {
+  __shared__ uint32_t s[4];
+  uint32_t top = 0;
+#pragma unroll 8
+  for (int64_t m = threadIdx.x; m < q.end; m += 256) {
+    const uint32_t b = abs_bits(q.dloss[m]);
+    const int64_t t = q.targets[m];
+    top = max(top, t >= 0 && t < q.vocab ? b : 0);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x) return;
+  top = max(max(s[0], s[1]), max(s[2], s[3]));
+  *q.scale = top == 0 || top >= 0x7f800000u ? 1.f : __uint_as_float(top);
+}
+
+// The operand of M^T: rows of it are M's columns, k M's rows; rows past `end`,
+// and those of tokens left out, are zeros whatever M holds.  A 64 x 64 tile of M
+// per workgroup through LDS and its transposed read; the operand of M along its
+// columns, where asked for, from the same read.
+__global__ __launch_bounds__(256) void k_xe_pack_t(XePack q) {
   constexpr int kRow = 144;
   __shared__ __attribute__((aligned(16))) char lds[64 * kRow];
+  const XeMatrix& a = q.a;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 64;
+  if (c0 >= a.cols) {  // the extra column of the grid
+    if (blockIdx.y == 0) scale_of(q);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = (t + 256 * i) >> 3, c = (t & 7) * 8;
-    const int64_t row = first + r0 + r;
+    const int64_t row = q.first + r0 + r;
     uint4 v = make_uint4(0, 0, 0, 0);
-    bool in = row < end;
-    if (in && targets) {
-      const int64_t x = targets[row];
-      in = x >= 0 && x < vocab;
+    bool in = row < q.end;
+    if (in && q.targets) {
+      const int64_t x = q.targets[row];
+      in = x >= 0 && x < q.vocab;
     }
     if (in) {
       const uint16_t* p = a.p + row * a.ld + c0 + c;
@@ -473,6 +528,10 @@ __global__ __launch_bounds__(256) void k_xe_pack_t(XeMatrix a, int64_t first, in
       }
     }
     *reinterpret_cast<uint4*>(lds + r * kRow + c * 2) = v;
+    const int64_t steps = (a.cols + kXeStep - 1) / kXeStep, step = (c0 + c) / kXeStep;
+    if (q.by_row && step < steps && r0 < q.end - q.first)
+      *reinterpret_cast<uint4*>(q.by_row + ((int64_t)blockIdx.y * steps + step) * kPanelStep + r / 16 * kFrag +
+                                (c % kXeStep / 8 * 16 + r % 16) * 16) = v;
   }
   __syncthreads();
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
@@ -480,12 +539,12 @@ __global__ __launch_bounds__(256) void k_xe_pack_t(XeMatrix a, int64_t first, in
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int64_t step = (int64_t)blockIdx.y * 2 + s;
-    if (step >= steps) break;
+    if (step >= q.steps) break;
     auto tr = [&](uint32_t at) {
       return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(uintptr_t)at);
     };
     const i16x8 v = __builtin_shufflevector(tr(from + 32 * s * kRow), tr(from + (32 * s + 16) * kRow), 0, 1, 2, 3, 4, 5, 6, 7);
-    *reinterpret_cast<uint4*>(out + ((int64_t)blockIdx.x * steps + step) * kPanelStep + w * kFrag + lane * 16) =
+    *reinterpret_cast<uint4*>(q.out + ((int64_t)blockIdx.x * q.steps + step) * kPanelStep + w * kFrag + lane * 16) =
         __builtin_bit_cast(uint4, v);
   }
 }
@@ -516,22 +575,34 @@ __global__ __launch_bounds__(256) void k_xe_pack(XeMatrix a, int64_t first, int6
 // the rest
 // ---------------------------------------------------------------------------
 
-// lse and loss of 32 rows per workgroup: eight threads a row join its parts in
-// turn, then the first of them the eight.
+// lse and loss of kR rows per workgroup: the row's 256 / kR threads join its
+// parts in turn, four loads at a time, then the first of them theirs.  One chain
+// of joins a row would wait for every load and exponential (1 row over 32000 of
+// 250 parts: 10 us with 8 threads a row).
+template <int kR>
 __global__ __launch_bounds__(256) void k_xe_loss(const float2* part, int64_t parts, int64_t rows, const int64_t* targets,
                                                  int64_t vocab, const float* picked, float* loss, float* lse,
                                                  uint32_t* flags) {
-  __shared__ float2 s[8][32];
-  const int r = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int64_t m = (int64_t)blockIdx.x * 32 + r;
+  constexpr int kK = 256 / kR;
+  __shared__ float2 s[kK][kR];
+  const int r = threadIdx.x % kR, k = threadIdx.x / kR;
+  const int64_t m = (int64_t)blockIdx.x * kR + r;
   float2 v = make_float2(-__builtin_inff(), 0.f);
   if (m < rows)
-    for (int64_t i = k; i < parts; i += 8) v = lse_join(v, part[i * rows + m]);
-  s[k][r] = v;
-  __syncthreads();
-  if (k || m >= rows) return;
+    for (int64_t i = k; i < parts; i += 4 * kK) {
+      float2 p[4];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v = lse_join(v, s[i][r]);
+      for (int j = 0; j < 4; ++j)
+        p[j] = i + j * kK < parts ? part[(i + j * kK) * rows + m] : make_float2(-__builtin_inff(), 0.f);
+      v = lse_join(v, lse_join(lse_join(p[0], p[1]), lse_join(p[2], p[3])));
+    }
+  s[k][r] = v;
+#pragma unroll
+  for (int half = kK / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (k < half) s[k][r] = v = lse_join(v, s[k + half][r]);
+  }
+  if (k || m >= rows) return;
   const float more = logf(v.y);
   const int64_t t = targets[m];
   const bool live = t >= 0 && t < vocab;
@@ -540,27 +611,6 @@ __global__ __launch_bounds__(256) void k_xe_loss(const float2* part, int64_t par
   if (loss) loss[m] = l;
   const uint32_t f = (live && abs_bits(l) >= 0x7f800000u ? GIFT_FLAG_NONFINITE : 0) | (t >= vocab ? GIFT_FLAG_TARGET : 0);
   if (flags && f) atomicOr(flags, f);
-}
-
-// The largest |dloss| of the tokens that count, 1 where it is 0 or not finite.
-// D is rounded to bf16 as it is for dX, whose rows take dloss in fp32; for dW
-// dloss multiplies each token's D before the rounding, divided by this, so that
-// equal weights (a mean's 1 / n) do not shift every value by the same rounding.
-__global__ __launch_bounds__(1024) void k_xe_scale(const float* dloss, const int64_t* targets, int64_t rows, int64_t vocab,
-                                                   float* scale) {
-  __shared__ uint32_t s[16];
-  uint32_t top = 0;
-  for (int64_t m = threadIdx.x; m < rows; m += 1024) {
-    const int64_t t = targets[m];
-    if (t >= 0 && t < vocab) top = max(top, abs_bits(dloss[m]));
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = top;
-  __syncthreads();
-  if (threadIdx.x) return;
-  for (int i = 1; i < 16; ++i) top = max(top, s[i]);
-  *scale = top == 0 || top >= 0x7f800000u ? 1.f : __uint_as_float(top);
 }
 
 // C = the slots' sums, added in order, scaled (and added to C).  Four columns a
@@ -572,6 +622,7 @@ __global__ __launch_bounds__(256) void k_xe_reduce(XeGemm g, const float* slots)
     const int64_t m = i / n4, n = (i - m * n4) * 4;
     const bool whole = n + 4 <= g.N;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int s = 0; s < g.n_split; ++s) {
       const float* p = slots + ((int64_t)s * g.M + m) * g.N + n;
       if (whole) v += __builtin_bit_cast(f32x4, ld16(p));
@@ -586,14 +637,22 @@ __global__ __launch_bounds__(256) void k_xe_reduce(XeGemm g, const float* slots)
     if (!in) v = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (kOut == kXeBf16) {
       uint16_t* p = static_cast<uint16_t*>(g.C) + m * g.ldc + n;
+      using any8 = unsigned __attribute__((ext_vector_type(2), aligned(2)));
+      if (whole) *reinterpret_cast<any8*>(p) = any8{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      else
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < g.N) p[e] = (uint16_t)bf16_bits(v[e]);
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) p[e] = (uint16_t)bf16_bits(v[e]);
     } else {
       float* p = static_cast<float*>(g.C) + m * g.ldc + n;
+      if (whole) {
+        if constexpr (kOut == kXeAcc) v += __builtin_bit_cast(f32x4, ld16(p));
+        st16(p, __builtin_bit_cast(uint4, v));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < g.N) p[e] = kOut == kXeAcc ? p[e] + v[e] : v[e];
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) p[e] = kOut == kXeAcc ? p[e] + v[e] : v[e];
+      }
     }
   }
 }
@@ -708,13 +767,17 @@ XeOperand as_packed(const uint8_t* p, int64_t rows, int64_t steps) {
   return o;
 }
 
-// A matrix as an operand along its columns: where it lies, or packed into ws.
-// Packing reads and writes it once, a copy of rows takes longer per use.
-XeOperand row_operand(const XeMatrix& a, int64_t first, int64_t rows, int64_t uses, uint8_t* ws, hipStream_t s) {
-  if (readable(a) && uses < 2600) return as_rows(a, first, rows);
+// Whether a matrix is packed along its columns for so many rows of the other
+// operand: packing reads and writes it once, copies of rows take longer per use.
+bool packed(const XeMatrix& a, int64_t uses) { return !readable(a) || uses >= 2600; }
+
+void pack_rows(const XeMatrix& a, int64_t first, int64_t rows, uint8_t* out, hipStream_t s) {
   const int64_t steps = up_div(a.cols, kXeStep);
-  k_xe_pack<<<dim3((uint32_t)steps, (uint32_t)up_div(rows, kXePanel)), dim3(256), 0, s>>>(a, first, first + rows, ws, steps);
-  return as_packed(ws, rows, steps);
+  k_xe_pack<<<dim3((uint32_t)steps, (uint32_t)up_div(rows, kXePanel)), dim3(256), 0, s>>>(a, first, first + rows, out, steps);
+}
+
+XeOperand row_operand(const XeMatrix& a, int64_t first, int64_t rows, bool is_packed, const uint8_t* ws) {
+  return is_packed ? as_packed(ws, rows, up_div(a.cols, kXeStep)) : as_rows(a, first, rows);
 }
 
 // Whether a product takes 256 x 256 tiles, one to a CU, or 128 x 256, two to a
@@ -857,9 +920,15 @@ hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64
   const int64_t rows = X.rows, vocab = W.rows;
   const XeFwdWs p = forward_plan(rows, X.cols, vocab, c);
   auto join = [&](int64_t first, int64_t n, int64_t parts) {
-    k_xe_loss<<<dim3((uint32_t)up_div(n, 32)), dim3(256), 0, s>>>(p.part, parts, n, targets + first, vocab, p.picked + first,
-                                                                  loss ? loss + first : nullptr,
-                                                                  lse ? lse + first : nullptr, flags);
+    auto run = [&](auto kernel, int kR) {
+      kernel<<<dim3((uint32_t)up_div(n, kR)), dim3(256), 0, s>>>(p.part, parts, n, targets + first, vocab, p.picked + first,
+                                                                 loss ? loss + first : nullptr,
+                                                                 lse ? lse + first : nullptr, flags);
+    };
+    // threads a row by the rows that there are to fill the chip with
+    if (n <= 64) run(k_xe_loss<1>, 1);
+    else if (n <= 4096) run(k_xe_loss<4>, 4);
+    else run(k_xe_loss<16>, 16);
   };
   if (rows <= kFewRows) {
     const int64_t groups = up_div(vocab, 16 * kFewWaves);
@@ -872,8 +941,10 @@ hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64
     join(0, rows, groups);
     return done();
   }
-  const XeOperand w = row_operand(W, 0, vocab, rows, p.w, s);
-  const XeOperand x = row_operand(X, 0, rows, vocab, p.x, s);
+  const bool pw = packed(W, rows), px = packed(X, vocab);
+  if (pw) pack_rows(W, 0, vocab, p.w, s);
+  if (px) pack_rows(X, 0, rows, p.x, s);
+  const XeOperand w = row_operand(W, 0, vocab, pw, p.w), x = row_operand(X, 0, rows, px, p.x);
   const int64_t chunk = chunk_rows(rows, vocab);
   for (int64_t first = 0; first < rows; first += chunk) {
     const int64_t n = rows - first < chunk ? rows - first : chunk;
@@ -909,13 +980,16 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
   const int64_t tokens = p.tall / kXeStep, k = up_div(d, kXeStep);
   const bool big = big_tiles(rows, p.piece);
   const float* scale = o.dW && dloss ? p.scale : nullptr;
-  if (scale) k_xe_scale<<<dim3(1), dim3(1024), 0, s>>>(dloss, targets, rows, vocab, p.scale);
-  const XeOperand x = row_operand(X, 0, rows, vocab, p.x, s);
-  auto transposed = [&](const XeMatrix& a, int64_t first, int64_t end, const int64_t* t, uint8_t* out, int64_t steps) {
-    k_xe_pack_t<<<dim3((uint32_t)up_div(a.cols, 64), (uint32_t)up_div(steps, 2)), dim3(256), 0, s>>>(a, first, end, t, vocab,
-                                                                                                   out, steps);
+  const bool pw = packed(W, rows), px = packed(X, vocab);
+  // an operand along the matrix's rows, and beside it the one along its columns
+  auto transposed = [&](XePack q) {
+    const uint32_t tiles = (uint32_t)up_div(q.a.cols, 64);
+    k_xe_pack_t<<<dim3(tiles + (q.scale ? 1 : 0), (uint32_t)up_div(q.steps, 2)), dim3(256), 0, s>>>(q);
   };
-  if (o.dW) transposed(X, 0, rows, targets, p.Xt, tokens);
+  if (o.dW) transposed(XePack{X, 0, rows, targets, vocab, p.Xt, tokens, px ? p.x : nullptr, scale ? dloss : nullptr,
+                              scale ? p.scale : nullptr});
+  else if (px) pack_rows(X, 0, rows, p.x, s);
+  const XeOperand x = row_operand(X, 0, rows, px, p.x);
   hipError_t e = done();
   if (e != hipSuccess) return e;
   for (int i = 0; i < p.n_piece; ++i) {
@@ -924,7 +998,9 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     XeGemm g{};
     sized(g, rows, n, k, 1, big);
     g.A = x;
-    g.B = row_operand(W, first, n, rows, p.w, s);
+    if (o.dX) transposed(XePack{W, first, first + n, nullptr, vocab, p.Wt, steps, pw ? p.w : nullptr, nullptr, nullptr});
+    else if (pw) pack_rows(W, first, n, p.w, s);
+    g.B = row_operand(W, first, n, pw, p.w);
     g.targets = targets;
     g.col0 = first;
     g.vocab = vocab;
@@ -940,12 +1016,11 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     e = done();
     if (e != hipSuccess) return e;
     if (o.dX) {
-      transposed(W, first, first + n, nullptr, p.Wt, steps);
       XeGemm h{};
       sized(h, rows, d, steps, p.dx_split, big_tiles(rows, d));
       h.A = as_packed(p.P, rows, steps);
       h.B = as_packed(p.Wt, d, steps);
-      if (p.dx_slots) {
+      if (p.dx_slots && (p.dx_split > 1 || i + 1 < p.n_piece)) {
         // each split of every piece adds to its own slot; a short last piece
         // may need fewer of them
         h.C = p.dx_slots;
@@ -955,6 +1030,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
       } else {
         h.C = o.dX;
         h.ldc = o.ld_dx;
+        h.add = i ? p.dx_slots : nullptr;
         h.by_row = true;
         h.targets = targets;
         h.vocab = vocab;
@@ -995,7 +1071,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
       if (e != hipSuccess) return e;
     }
   }
-  if (o.dX && p.dx_slots) {
+  if (o.dX && p.dx_split > 1) {
     XeGemm h{};
     sized(h, rows, d, p.piece / kXeStep, p.dx_split, false);
     h.C = o.dX;
