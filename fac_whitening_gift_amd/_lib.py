@@ -60,7 +60,8 @@ EXPORTS = (
     "gift_mx_matmul_workspace_bytes", "gift_mx_linear", "gift_mx_linear_workspace_bytes",
     "gift_norm_forward", "gift_norm_backward", "gift_norm_backward_workspace_bytes",
     "gift_xent_forward", "gift_xent_forward_workspace_bytes", "gift_xent_backward",
-    "gift_xent_backward_workspace_bytes",
+    "gift_xent_backward_workspace_bytes", "gift_block_norm_forward", "gift_block_norm_backward",
+    "gift_block_norm_backward_workspace_bytes",
 )
 
 
@@ -91,6 +92,18 @@ class _Layer(ctypes.Structure):
 
 class _Mx(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class _BlockNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("kind", ctypes.c_int32), ("post", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("h_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("post_bias", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
+class _BlockNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dweight", "dbias", "dpost_weight", "dpost_bias", "dgate")]
 
 
 _lib = None
@@ -147,6 +160,10 @@ def load():
         "gift_xent_backward": (I, [P, I64, I64, I64, P, I64, I64, P, P, P, P, I64, P, I, I64, I, P, SZ,
                                    P]),
         "gift_xent_backward_workspace_bytes": (SZ, [I64, I64, I64, I, I, I]),
+        "gift_block_norm_forward": (I, [ctypes.POINTER(_BlockNorm), P, P, P, P, P, P]),
+        "gift_block_norm_backward": (I, [ctypes.POINTER(_BlockNorm), P, P, P, P, P, P, P,
+                                         ctypes.POINTER(_BlockNormGrads), I, P, SZ, P]),
+        "gift_block_norm_backward_workspace_bytes": (SZ, [I64, I64, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -975,3 +992,120 @@ def gift_xent_backward(x, w, targets, lse, dloss=None, dx=None, dw=None, dtype=t
              None if dloss is None else _vector(dloss, rows, "dloss", dev), xp, ldx, wp, code, ldw,
              1 if accumulate else 0, sp, sb)
     return dx, dw
+
+
+def _block_norm(y, h, weight, bias, eps, post, post_weight, post_bias, gate, scale, kind):
+    """-> (the descriptor, pointers of y and h, rows, d)"""
+    yp, ydt, rows, d = _dense(y, "y")
+    dev = y.device
+    hp, hdt, _, _ = _dense(h, "h", dev, (rows, d))
+    p = _BlockNorm(rows, d, rows, kind, 1 if post else 0, ydt, hdt, scale, eps,
+                   None if weight is None else _vector(weight, d, "weight", dev),
+                   None if bias is None else _vector(bias, d, "bias", dev),
+                   None if post_weight is None else _vector(post_weight, d, "post_weight", dev),
+                   None if post_bias is None else _vector(post_bias, d, "post_bias", dev), None)
+    if gate is not None:
+        if gate.dtype != torch.float32 or gate.device != dev or not gate.is_contiguous() or \
+                gate.shape[-1:] != (d,) or gate.dim() > 2 or gate.numel() == 0 or rows % (gate.numel() // d):
+            raise ValueError("gate must be %d contiguous fp32 elements on %s, or as many rows of them as divide the %d "
+                             "rows" % (d, dev, rows))
+        p.gate = gate.data_ptr()
+        p.gate_rows = rows // (gate.numel() // d)
+    return p, yp, hp, rows, d
+
+
+def gift_block_norm_forward(y, h, weight=None, bias=None, eps=1e-5, post=True, post_weight=None, post_bias=None,
+                            gate=None, scale=1.0, kind=NORM_RMS, x=None, h_out=None, stats=None, stream=None):
+    """h' = scale h + gate norm(y) (post False: gate y), x = norm(h'): y (rows x
+    d, bf16 or fp32) a block's output, h (y's type or fp32) the residual stream;
+    weights, biases: d fp32 or None; gate: d fp32, or one for each of as many
+    runs of rows.  -> (x, h', stats (4 x rows, for the backward pass))."""
+    if stream is not None:
+        return _on(stream, y.device, gift_block_norm_forward, y, h, weight, bias, eps, post, post_weight, post_bias,
+                   gate, scale, kind, x, h_out, stats)
+    p, yp, hp, rows, d = _block_norm(y, h, weight, bias, eps, post, post_weight, post_bias, gate, scale, kind)
+    dev = y.device
+    if x is None:
+        x = torch.empty_like(y)
+        xp = x.data_ptr()
+    else:
+        xp = _dense(x, "x", dev, (rows, d), y.dtype)[0]
+    if h_out is None:
+        h_out = torch.empty_like(h)
+        op = h_out.data_ptr()
+    else:
+        op = _dense(h_out, "h_out", dev, (rows, d), h.dtype)[0]
+    if stats is None:
+        stats = torch.empty((4, rows), dtype=torch.float32, device=dev)
+        sp = stats.data_ptr()
+    else:
+        sp = _dense(stats, "stats", dev, (4, rows), torch.float32)[0]
+    _enqueue(dev, load().gift_block_norm_forward, ctypes.byref(p), yp, hp, op, xp, sp)
+    return x, h_out, stats
+
+
+def gift_block_norm_backward_workspace_bytes(rows, d, gates=1):
+    return int(load().gift_block_norm_backward_workspace_bytes(rows, d, gates))
+
+
+_BLOCK_NORM_GRADS = ("dweight", "dbias", "dpost_weight", "dpost_bias", "dgate")
+
+
+def gift_block_norm_backward(dx, dh, y, h_out, stats, weight=None, bias=None, post=True, post_weight=None,
+                             post_bias=None, gate=None, scale=1.0, kind=NORM_RMS, grads=None, accumulate=False,
+                             ws=None, stream=None):
+    """Gradients of gift_block_norm_forward for dx and dh (of h', or None) and its
+    statistics.  -> dict of dy, dh and, for the vectors that are given, dweight,
+    dbias, dpost_weight, dpost_bias and dgate (None for the others).  grads: dict
+    of tensors to fill (False: left out); accumulate adds to the given vectors'."""
+    if stream is not None:
+        return _on(stream, y.device, gift_block_norm_backward, dx, dh, y, h_out, stats, weight, bias, post, post_weight,
+                   post_bias, gate, scale, kind, grads, accumulate, ws)
+    p, yp, op, rows, d = _block_norm(y, h_out, weight, bias, 0.0, post, post_weight, post_bias, gate, scale, kind)
+    dev = y.device
+    gp = _dense(dx, "dx", dev, (rows, d), y.dtype)[0]
+    hp = None if dh is None else _dense(dh, "dh", dev, (rows, d), h_out.dtype)[0]
+    sp = _dense(stats, "stats", dev, (4, rows), torch.float32)[0]
+    given = {} if grads is None else dict(grads)
+    out = {}
+
+    def result(name, like):
+        t = given.pop(name, None)
+        if t is None:
+            t = torch.empty_like(like)
+        elif t is False:
+            out[name] = None
+            return None
+        else:
+            t_p = _dense(t, name, dev, (rows, d), like.dtype)[0]
+            out[name] = t
+            return t_p
+        out[name] = t
+        return t.data_ptr()
+
+    yg, hg = result("dy", y), result("dh", h_out)
+    g = _BlockNormGrads()
+    vectors = False
+    for name, of in zip(_BLOCK_NORM_GRADS, (weight, bias, post_weight, post_bias, gate)):
+        t = given.pop(name, None)
+        if t is None and of is not None:
+            if accumulate:
+                raise ValueError("accumulate adds to given gradients: %s" % name)
+            t = torch.empty_like(of)
+        if t is None or t is False:
+            out[name] = None
+            continue
+        shape = of.shape if of is not None else (d,)
+        if t.dtype != torch.float32 or t.device != dev or t.shape != shape or not t.is_contiguous():
+            raise ValueError("%s must be %s contiguous fp32 on %s" % (name, tuple(shape), dev))
+        setattr(g, name, t.data_ptr())
+        out[name] = t
+        vectors = True
+    if given:
+        raise ValueError("unknown gradients: %s" % ", ".join(sorted(given)))
+    lib = load()
+    need = lib.gift_block_norm_backward_workspace_bytes(rows, d, rows // p.gate_rows) if vectors else 0
+    keep, wp, wb = _scratch(need, dev, ws)
+    _enqueue(dev, lib.gift_block_norm_backward, ctypes.byref(p), gp, hp, yp, op, sp, yg, hg, ctypes.byref(g),
+             1 if accumulate else 0, wp, wb)
+    return out

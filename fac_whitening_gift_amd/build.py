@@ -25,7 +25,8 @@ PROBE_HEADER = os.path.join(ROOT, "include", "gift_probe.h")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "api_layer.cpp", "roundtrip.hip", "roundtrip_rt2.hip", "refresh.hip", "mx.hip",
-           "norm.hip", "api_step.cpp", "xent.hip"]
+           "norm.hip", "api_step.cpp", "xent.hip",
+           "block_norm.hip"]
 
 # -packed-fp32-ops: keep hipcc from forming packed fp32 VALU ops (the host
 # pass does not know the feature and warns; that is expected).

@@ -1,5 +1,6 @@
-// Entry points of a training step around its layers (gift_xent_* of
-// include/gift.h): argument validation, then the launchers of xent.hip.
+// Entry points of a training step around its layers (gift_xent_*,
+// gift_block_norm_* of include/gift.h): argument validation, then the launchers
+// of xent.hip and block_norm.hip.
 #include "checks.hpp"
 #include "step.hpp"
 
@@ -25,6 +26,42 @@ gift_status check_xent(const void* X, int64_t rows, int64_t d, int64_t ldx, cons
 
 XeMatrix matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   return XeMatrix{static_cast<const uint16_t*>(p), rows, cols, ld};
+}
+
+bool block_norm_size_ok(int64_t rows, int64_t d) { return size_ok(rows, d) && d <= kBlockNormMaxD; }
+
+int64_t gates_of(const gift_block_norm& p) { return p.gate ? (p.rows + p.gate_rows - 1) / p.gate_rows : 1; }
+
+gift_status check_block_norm(const gift_block_norm* p) {
+  if (!p) return fail(GIFT_ERR_INVALID_ARG, "the block norm is NULL");
+  if (!block_norm_size_ok(p->rows, p->d))
+    return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%lld x %lld out of range", (long long)p->rows, (long long)p->d);
+  if (p->kind != GIFT_NORM_LAYER && p->kind != GIFT_NORM_RMS)
+    return fail(GIFT_ERR_INVALID_ARG, "unknown norm kind %d", p->kind);
+  if (!dtype_ok(p->y_dtype) || !dtype_ok(p->h_dtype) ||
+      (p->y_dtype == GIFT_DTYPE_F32 && p->h_dtype == GIFT_DTYPE_BF16))
+    return fail(GIFT_ERR_INVALID_ARG, "dtypes %d beside a stream of %d", p->y_dtype, p->h_dtype);
+  if (!(p->eps >= 0.f && p->eps < 1e30f)) return fail(GIFT_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!(p->scale > -1e30f && p->scale < 1e30f)) return fail(GIFT_ERR_INVALID_ARG, "scale must be finite");
+  if (p->gate && (p->gate_rows < 1 || p->gate_rows > p->rows))
+    return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "gate rows of %lld for %lld rows", (long long)p->gate_rows,
+                (long long)p->rows);
+  if (!p->post && (p->post_weight || p->post_bias))
+    return fail(GIFT_ERR_INVALID_ARG, "post_weight and post_bias belong to the norm of y");
+  GIFT_TRY(check_vec("weight", p->weight));
+  GIFT_TRY(check_vec("bias", p->bias));
+  GIFT_TRY(check_vec("post_weight", p->post_weight));
+  GIFT_TRY(check_vec("post_bias", p->post_bias));
+  return check_vec("gate", p->gate);
+}
+
+// two of the gradients in one buffer
+bool any_alike(const gift_block_norm_grads& g) {
+  const float* const v[5] = {g.dweight, g.dbias, g.dpost_weight, g.dpost_bias, g.dgate};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (v[i] && v[i] == v[j]) return true;
+  return false;
 }
 
 }  // namespace
@@ -79,6 +116,54 @@ gift_status gift_xent_backward(const void* X, int64_t rows, int64_t d, int64_t l
   g.accumulate = accumulate != 0;
   return launched(launch_xent_backward(matrix(X, rows, d, ldx), matrix(W, vocab, d, ldw), targets, lse, dloss, g, ws,
                                        (hipStream_t)stream));
+}
+
+gift_status gift_block_norm_forward(const gift_block_norm* p, const void* Y, const void* H, void* H_out, void* X,
+                                    float* stats, void* stream) {
+  GIFT_TRY(check_block_norm(p));
+  GIFT_TRY(check_matrix("Y", Y, p->y_dtype, p->rows, p->d, p->d));
+  GIFT_TRY(check_matrix("H", H, p->h_dtype, p->rows, p->d, p->d));
+  GIFT_TRY(check_matrix("H_out", H_out, p->h_dtype, p->rows, p->d, p->d));
+  GIFT_TRY(check_matrix("X", X, p->y_dtype, p->rows, p->d, p->d));
+  if (X == H_out) return fail(GIFT_ERR_INVALID_ARG, "X and H_out are the same buffer");
+  if (!stats) return fail(GIFT_ERR_INVALID_ARG, "stats is NULL");
+  GIFT_TRY(check_vec("stats", stats));
+  return launched(launch_block_norm_forward(*p, Y, H, H_out, X, stats, (hipStream_t)stream));
+}
+
+size_t gift_block_norm_backward_workspace_bytes(int64_t rows, int64_t d, int64_t gates) {
+  return block_norm_size_ok(rows, d) && gates >= 1 && gates <= rows ? block_norm_backward_ws(rows, d, gates) : 0;
+}
+
+gift_status gift_block_norm_backward(const gift_block_norm* p, const void* dX, const void* dH_out, const void* Y,
+                                     const void* H_out, const float* stats, void* dY, void* dH,
+                                     const gift_block_norm_grads* grads, int accumulate, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  GIFT_TRY(check_block_norm(p));
+  GIFT_TRY(check_matrix("dX", dX, p->y_dtype, p->rows, p->d, p->d));
+  if (dH_out) GIFT_TRY(check_matrix("dH_out", dH_out, p->h_dtype, p->rows, p->d, p->d));
+  GIFT_TRY(check_matrix("Y", Y, p->y_dtype, p->rows, p->d, p->d));
+  GIFT_TRY(check_matrix("H_out", H_out, p->h_dtype, p->rows, p->d, p->d));
+  if (dY) GIFT_TRY(check_matrix("dY", dY, p->y_dtype, p->rows, p->d, p->d));
+  if (dH) GIFT_TRY(check_matrix("dH", dH, p->h_dtype, p->rows, p->d, p->d));
+  if (dY && dY == dH) return fail(GIFT_ERR_INVALID_ARG, "dY and dH are the same buffer");
+  if (!stats) return fail(GIFT_ERR_INVALID_ARG, "the forward pass's statistics are NULL");
+  GIFT_TRY(check_vec("stats", stats));
+  const gift_block_norm_grads g = grads ? *grads : gift_block_norm_grads{};
+  const bool vectors = g.dweight || g.dbias || g.dpost_weight || g.dpost_bias || g.dgate;
+  if (!dY && !dH && !vectors) return fail(GIFT_ERR_INVALID_ARG, "every gradient is NULL");
+  if (!p->post && (g.dpost_weight || g.dpost_bias))
+    return fail(GIFT_ERR_INVALID_ARG, "dpost_weight and dpost_bias belong to the norm of y");
+  if (!p->gate && g.dgate) return fail(GIFT_ERR_INVALID_ARG, "dgate without a gate");
+  if (any_alike(g)) return fail(GIFT_ERR_INVALID_ARG, "two of the vectors' gradients are the same buffer");
+  GIFT_TRY(check_vec("dweight", g.dweight));
+  GIFT_TRY(check_vec("dbias", g.dbias));
+  GIFT_TRY(check_vec("dpost_weight", g.dpost_weight));
+  GIFT_TRY(check_vec("dpost_bias", g.dpost_bias));
+  GIFT_TRY(check_vec("dgate", g.dgate));
+  GIFT_TRY(check_ws(ws, ws_bytes, vectors ? block_norm_backward_ws(p->rows, p->d, gates_of(*p)) : 0));
+  return launched(launch_block_norm_backward(*p, dX, dH_out, Y, H_out, stats, dY, dH, g, accumulate != 0, ws,
+                                             (hipStream_t)stream));
 }
 
 }  // extern "C"

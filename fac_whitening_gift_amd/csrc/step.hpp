@@ -36,4 +36,14 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
                                 const float* lse, const float* dloss, const XeGrad& g, void* ws,
                                 hipStream_t s);
 
+
+// block_norm.hip
+constexpr int64_t kBlockNormMaxD = 16384;  // widest row that its lanes hold
+hipError_t launch_block_norm_forward(const gift_block_norm& p, const void* Y, const void* H, void* H2, void* X,
+                                     float* stats, hipStream_t s);
+size_t block_norm_backward_ws(int64_t rows, int64_t d, int64_t gates);
+hipError_t launch_block_norm_backward(const gift_block_norm& p, const void* dX, const void* dH2, const void* Y,
+                                      const void* H2, const float* stats, void* dY, void* dH,
+                                      const gift_block_norm_grads& g, bool accumulate, void* ws, hipStream_t s);
+
 }  // namespace gift

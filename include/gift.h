@@ -557,6 +557,67 @@ gift_status gift_xent_backward(const void *X, int64_t rows, int64_t d, int64_t l
 size_t gift_xent_backward_workspace_bytes(int64_t rows, int64_t d, int64_t vocab, int want_dx,
                                           int want_dw, int dw_dtype);
 
+/*
+ * gift_block_norm -- what lies between two blocks, in one pass: the norm after
+ * a block, its gate and the residual scale, and the norm in front of the next
+ * block (norms as gift_norm_forward's, of one kind and eps):
+ *   n  = norm(y) * post_weight + post_bias   (post == 0: n = y)
+ *   h' = scale * h + gate * n
+ *   x  = norm(h') * weight + bias
+ * y: the block's output, h: the residual stream, x: the next block's input;
+ * y and x have y_dtype, h and h' h_dtype (both alike, or bf16 beside an fp32
+ * stream).  Dense rows x d, d <= 16384, element alignment.  Weights and
+ * biases: d fp32 (NULL: 1 and 0).  gate: fp32, row i / gate_rows of it serves
+ * row i, so a vector (gate_rows = rows), or one for each sequence of
+ * gate_rows tokens; NULL: 1.  x comes from h' before its rounding.
+ * HOST struct.
+ */
+typedef struct gift_block_norm {
+    int64_t rows;
+    int64_t d;
+    int64_t gate_rows;           /* 1 <= gate_rows <= rows, ignored without a gate */
+    int32_t kind;                /* GIFT_NORM_* */
+    int32_t post;                /* whether y is normed */
+    int32_t y_dtype;
+    int32_t h_dtype;
+    float scale;                 /* finite */
+    float eps;
+    const float *weight;
+    const float *bias;
+    const float *post_weight;
+    const float *post_bias;
+    const float *gate;           /* ceil(rows / gate_rows) x d, dense */
+} gift_block_norm;
+
+/* stats: 4 x rows fp32, the means and reciprocal deviations of y (0 and 1
+ * without post) and of h'; means are 0 for RMS.  H_out may be H, X may be Y
+ * (the buffer itself). */
+gift_status gift_block_norm_forward(const gift_block_norm *p, const void *Y, const void *H,
+                                    void *H_out, void *X, float *stats, void *stream);
+
+/*
+ * gift_block_norm_backward -- gradients for dX and dH_out (NULL: 0) and the
+ * statistics of the forward pass, with H_out what it wrote:
+ *   t = dH_out + dnorm(dX; H_out),  dH = scale * t,  dY = dnorm(gate * t; Y)
+ * and the vectors' gradients summed over their rows, in an order that
+ * depends on the sizes alone.  dY (y_dtype), dH (h_dtype) and the members of
+ * *grads may be NULL, not all; dgate has the gate's shape.  dY may be dX's
+ * buffer and dH dH_out's.  accumulate != 0: the members of *grads are added
+ * to.
+ */
+typedef struct gift_block_norm_grads {
+    float *dweight;
+    float *dbias;
+    float *dpost_weight;         /* post != 0 only, as dpost_bias */
+    float *dpost_bias;
+    float *dgate;                /* with a gate only */
+} gift_block_norm_grads;
+gift_status gift_block_norm_backward(const gift_block_norm *p, const void *dX, const void *dH_out,
+                                     const void *Y, const void *H_out, const float *stats,
+                                     void *dY, void *dH, const gift_block_norm_grads *grads,
+                                     int accumulate, void *ws, size_t ws_bytes, void *stream);
+size_t gift_block_norm_backward_workspace_bytes(int64_t rows, int64_t d, int64_t gates);
+
 const char *gift_status_string(int status);
 /* Thread-local detail of the last failing call on this thread. */
 const char *gift_last_error(void);

@@ -1,0 +1,317 @@
+"""The norms between two blocks on the device (gift_block_norm_*) against fp64.
+
+Tolerances, with u = 2^-24 and d the row length: a sum of n terms is off by at
+most n u times the sum of their magnitudes, in any order; every product and sum
+of two by u of its magnitude; a result in the type it is stored in by half a
+step of it.  The errors of what goes into an operation are carried through it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fac_whitening_gift_amd as fg
+from oracle import step as os_
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+KINDS = [fg.NORM_LAYER, fg.NORM_RMS]
+TYPES = [(F32, F32), (BF16, F32), (BF16, BF16)]   # of y and of the stream
+VECTORS = ("weight", "bias", "post_weight", "post_bias", "gate")
+
+
+def _np(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def _half(t):
+    return torch.finfo(t.dtype).eps / 2
+
+
+def _draw(rows, d, types, groups=1, seed=0):
+    rng = np.random.default_rng(seed + 7 * rows + d + 31 * groups)
+
+    def normal(*shape):
+        return torch.from_numpy(rng.standard_normal(shape).astype(np.float32))
+    v = {"weight": 1 + 0.2 * normal(d), "bias": normal(d), "post_weight": 1 + 0.2 * normal(d), "post_bias": 0.3 * normal(d),
+         "gate": 0.3 + 0.5 * normal(groups, d)}
+    return ((normal(rows, d) + 0.1).to(types[0]), (2 * normal(rows, d) + 0.2).to(types[1]),
+            normal(rows, d).to(types[0]), normal(rows, d).to(types[1]), v)
+
+
+def _norm_error(v, e, w, b, eps, layer):
+    """Errors of the mean, the reciprocal deviation and the result of a norm of
+    values v that are off by e."""
+    d = v.shape[1]
+    mu = v.mean(1) if layer else np.zeros(v.shape[0])
+    em = e.mean(1) + (d + 1) * U * (np.abs(v) + e).mean(1) if layer else np.zeros(v.shape[0])
+    c = v - mu[:, None]
+    ec = e + em[:, None] + U * (np.abs(c) + e + em[:, None])
+    var = (c * c).mean(1) + eps
+    ev = (2 * np.abs(c) * ec + ec * ec).mean(1) + (d + 3) * U * var
+    r = var ** -0.5
+    er = r * (0.5 * ev / var * (1 + ev / var) + 3 * U)
+    wa = 1.0 if w is None else np.abs(w)
+    ba = 0.0 if b is None else np.abs(b)
+    ey = wa * (ec * r[:, None] + np.abs(c) * er[:, None]) * 1.01 + 3 * U * (wa * np.abs(c) * r[:, None] + ba)
+    return em, er, ey
+
+
+def _check_forward(y, h, v, how, got):
+    x, h2, stats = got
+    layer = how["kind"] == fg.NORM_LAYER
+    post, scale, eps = how.get("post", True), how.get("scale", 1.0), how.get("eps", 1e-5)
+    a = {k: _np(t) for k, t in v.items()}
+    Y, H = _np(y), _np(h)
+    rx, rh, rs = os_.block_norm_forward(Y, H, **a, eps=eps, post=post, scale=scale, layer=layer)
+    z = np.zeros_like(Y)
+    epm, epr, en = _norm_error(Y, z, a.get("post_weight"), a.get("post_bias"), eps, layer) if post else (0.0, 0.0, z)
+    k = os_._gates(a.get("gate"), *Y.shape)
+    n = rh - scale * H   # gate n
+    eh = np.abs(k) * en + 3 * U * (np.abs(scale * H) + np.abs(n) + np.abs(k) * en)
+    em, er, ex = _norm_error(rh, eh, a.get("weight"), a.get("bias"), eps, layer)
+    assert np.all(np.abs(_np(h2) - rh) <= eh + _half(h2) * (np.abs(rh) + eh))
+    assert np.all(np.abs(_np(x) - rx) <= ex + _half(x) * (np.abs(rx) + ex))
+    assert np.all(np.abs(_np(stats) - rs) <= np.stack([epm + z[:, 0], epr + z[:, 0], em, er]) + U * np.abs(rs))
+
+
+def _check_backward(dx, dh, y, h2, stats, v, how, got):
+    layer = how["kind"] == fg.NORM_LAYER
+    post, scale = how.get("post", True), how.get("scale", 1.0)
+    a = {k: _np(t) for k, t in v.items()}
+    g = os_.block_norm_backward(_np(dx), _np(dh), _np(y), _np(h2), _np(stats), **{k: t for k, t in a.items() if k != "bias"},
+                                post=post, scale=scale, layer=layer)
+    rows, d = y.shape
+    pm, pr, m, r = (s[:, None] for s in _np(stats))
+    u = np.abs((_np(h2) - m) * r)
+    one = np.ones(d)
+    w = np.abs(a["weight"]) if a.get("weight") is not None else one
+    pw = np.abs(a["post_weight"]) if post and a.get("post_weight") is not None else one
+    pb = np.abs(a["post_bias"]) if post and a.get("post_bias") is not None else 0 * one
+    dxa = np.abs(_np(dx))
+
+    def back(f, ef, u, r):
+        """error of r (f - u mean(f u) - mean(f)) for f off by ef"""
+        along, level = (f * u).mean(1, keepdims=True), f.mean(1, keepdims=True)
+        carried = ef + u * (ef * u).mean(1, keepdims=True) + ef.mean(1, keepdims=True)
+        return r * (carried + (d + 8) * U * (u * along + level) + 8 * U * (f + u * along + level))
+    f = dxa * w
+    t = np.abs(g["t"])
+    et = back(f, 2 * U * f, u, r) + 3 * U * (t + (0 if dh is None else np.abs(_np(dh))))
+    if got["dh"] is not None:
+        e = abs(scale) * et + 2 * U * np.abs(g["dh"])
+        assert np.all(np.abs(_np(got["dh"]) - g["dh"]) <= e + _half(got["dh"]) * (np.abs(g["dh"]) + e))
+    k = np.abs(os_._gates(a.get("gate"), rows, d))
+    yh = np.abs((_np(y) - pm) * pr) if post else np.abs(_np(y))
+    if got["dy"] is not None:
+        e = back(k * t * pw, k * pw * (et + 4 * U * t), yh, pr) if post else k * (et + 4 * U * t)
+        assert np.all(np.abs(_np(got["dy"]) - g["dy"]) <= e + _half(got["dy"]) * (np.abs(g["dy"]) + e))
+    many = (rows + 12) * U
+    if got["dweight"] is not None:
+        assert np.all(np.abs(_np(got["dweight"]) - g["dweight"]) <= many * (dxa * u).sum(0) + 1e-300)
+    if got["dbias"] is not None:
+        assert np.all(np.abs(_np(got["dbias"]) - g["dbias"]) <= many * dxa.sum(0) + 1e-300)
+    ea, eb = et * yh + many * (t + et) * yh, et + many * (t + et)
+    if got["dpost_weight"] is not None:
+        assert np.all(np.abs(_np(got["dpost_weight"]) - g["dpost_weight"]) <= (k * (ea + 4 * U * t * yh)).sum(0) + 1e-300)
+    if got["dpost_bias"] is not None:
+        assert np.all(np.abs(_np(got["dpost_bias"]) - g["dpost_bias"]) <= (k * (eb + 4 * U * t)).sum(0) + 1e-300)
+    if got["dgate"] is not None:
+        groups = got["dgate"].numel() // d
+        e = (pw * (ea + 4 * U * t * yh) + pb * (eb + 4 * U * t)).reshape(groups, rows // groups, d).sum(1)
+        assert np.all(np.abs(_np(got["dgate"]).reshape(groups, d) - g["dgate"]) <= e + 1e-300)
+
+
+def _dev(v):
+    return {k: None if t is None else t.to(DEV) for k, t in v.items()}
+
+
+SIZES = [(1, 1), (1, 4096), (2, 8), (3, 7), (5, 64), (9, 130), (33, 256), (40, 400), (7, 1024), (70, 1000), (6, 2048),
+         (5, 2050), (4, 4096), (3, 5000), (2, 8192), (2, 12000), (3, 16384), (2, 16383), (1000, 96)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("rows,d", SIZES)
+def test_forward_and_backward(rows, d, types, kind):
+    say("block norm %dx%d %s kind %d" % (rows, d, types, kind))
+    y, h, dx, dh, v = _draw(rows, d, types)
+    Y, H, DX, DH, V = y.to(DEV), h.to(DEV), dx.to(DEV), dh.to(DEV), _dev(v)
+    for how, names in ((dict(kind=kind, scale=0.7), VECTORS), (dict(kind=kind, post=False), ("weight", "gate")),
+                       (dict(kind=kind, scale=-1.5), ()), (dict(kind=kind, scale=0.0), ("weight", "post_weight"))):
+        w, W = {k: v[k] for k in names}, {k: V[k] for k in names}
+        got = fg.gift_block_norm_forward(Y, H, **W, **how)
+        assert got[0].dtype == types[0] and got[1].dtype == types[1]
+        _check_forward(y, h, w, how, got)
+        for gh in (DH, None):
+            grads = fg.gift_block_norm_backward(DX, gh, Y, got[1], got[2], **W, **how)
+            assert sorted(k for k in grads if grads[k] is not None) == sorted(["dy", "dh"] + ["d" + k for k in names])
+            _check_backward(dx, None if gh is None else dh, y, got[1], got[2], w, how, grads)
+    # one output at a time: the same bits
+    how, W = dict(kind=kind, scale=0.7), V
+    got = fg.gift_block_norm_forward(Y, H, **W, **how)
+    want = fg.gift_block_norm_backward(DX, DH, Y, got[1], got[2], **W, **how)
+    for name in want:
+        only = {k: False for k in want if k != name}
+        one = fg.gift_block_norm_backward(DX, DH, Y, got[1], got[2], **W, **how, grads=only)
+        assert torch.equal(one[name], want[name]) and all(one[k] is None for k in only)
+
+
+@pytest.mark.parametrize("groups,per,d", [(2, 1, 64), (3, 5, 96), (7, 33, 200), (40, 1, 1000), (5, 400, 40), (4, 250, 1536),
+                                          (64, 16, 128), (2, 1024, 64), (300, 7, 17), (9, 3, 4100)])
+def test_a_gate_for_each_sequence(groups, per, d):
+    """Gates whose rows end inside and at the end of what a workgroup takes."""
+    say("block norm gates %d x %d rows of %d" % (groups, per, d))
+    rows = groups * per
+    y, h, dx, dh, v = _draw(rows, d, (BF16, F32), groups)
+    V = _dev(v)
+    for kind in KINDS:
+        how = dict(kind=kind, scale=1.0)
+        got = fg.gift_block_norm_forward(y.to(DEV), h.to(DEV), **V, **how)
+        _check_forward(y, h, v, how, got)
+        grads = fg.gift_block_norm_backward(dx.to(DEV), dh.to(DEV), y.to(DEV), got[1], got[2], **V, **how)
+        assert grads["dgate"].shape == (groups, d)
+        _check_backward(dx, dh, y, got[1], got[2], v, how, grads)
+        again = fg.gift_block_norm_backward(dx.to(DEV), dh.to(DEV), y.to(DEV), got[1], got[2], **V, **how)
+        assert all(torch.equal(again[k], grads[k]) for k in grads)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("d", [100, 1024, 4099, 9000])
+def test_unaligned_and_in_place(d, types):
+    """Rows that start anywhere; X over Y, H' over H, dY over dX, dH over dH';
+    nothing written beside."""
+    say("block norm unaligned d=%d %s" % (d, types))
+    rows = 9
+    y, h, dx, dh, v = _draw(rows, d, types)
+    V = _dev(v)
+    for how in (dict(kind=fg.NORM_LAYER, scale=0.5), dict(kind=fg.NORM_RMS, post=False)):
+        W = {k: t for k, t in V.items() if how.get("post", True) or not k.startswith("post")}
+        want = fg.gift_block_norm_forward(y.to(DEV), h.to(DEV), **W, **how)
+        ref = fg.gift_block_norm_backward(dx.to(DEV), dh.to(DEV), y.to(DEV), want[1], want[2], **W, **how)
+
+        def guarded(t):
+            flat = torch.full((rows * d + 3,), 5.0, dtype=t.dtype, device=DEV)
+            view = flat[1:1 + rows * d].view(rows, d)
+            view.copy_(t)
+            return flat, view
+        (fy, Y), (fh, H), (fx, DX), (fd, DH) = guarded(y), guarded(h), guarded(dx), guarded(dh)
+        got = fg.gift_block_norm_forward(Y, H, **W, **how, x=Y, h_out=H)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        _, Y2 = guarded(y)
+        grads = fg.gift_block_norm_backward(DX, DH, Y2, H, got[2], **W, **how, grads={"dy": DX, "dh": DH})
+        assert all(p is q is None or torch.equal(p, q) for p, q in ((grads[k], ref[k]) for k in ref))
+        for flat in (fy, fh, fx, fd):
+            assert float(flat[0]) == 5.0 and float(flat[-2]) == 5.0 and float(flat[-1]) == 5.0
+
+
+def test_nan_rows_stay_alone():
+    """A NaN and an infinity reach their rows, the vectors' sums over them, and
+    the gate that serves them."""
+    say("block norm nan rows")
+    rows, d, groups = 24, 200, 8
+    y, h, dx, dh, v = _draw(rows, d, (F32, F32), groups)
+    V = _dev(v)
+    how = dict(kind=fg.NORM_LAYER)
+    clean = fg.gift_block_norm_forward(y.to(DEV), h.to(DEV), **V, **how)
+    cg = fg.gift_block_norm_backward(dx.to(DEV), dh.to(DEV), y.to(DEV), clean[1], clean[2], **V, **how)
+    y[4, 5], h[9, 0] = float("nan"), float("inf")
+    got = fg.gift_block_norm_forward(y.to(DEV), h.to(DEV), **V, **how)
+    keep = [i for i in range(rows) if i not in (4, 9)]
+    assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][keep], clean[1][keep])
+    assert bool(torch.isnan(got[0][4]).all()) and bool(torch.isnan(got[0][9]).any())
+    grads = fg.gift_block_norm_backward(dx.to(DEV), dh.to(DEV), y.to(DEV), got[1], got[2], **V, **how)
+    assert torch.equal(grads["dy"][keep], cg["dy"][keep]) and torch.equal(grads["dh"][keep], cg["dh"][keep])
+    gates = [g for g in range(groups) if g not in (1, 3)]   # rows 3..5 and 9..11
+    assert torch.equal(grads["dgate"][gates], cg["dgate"][gates])
+    assert bool(torch.isnan(grads["dgate"][1]).all())
+
+
+@pytest.mark.parametrize("rows,d,groups", [(60, 100, 1), (600, 1024, 6)])
+def test_accumulate_stream_and_graph(rows, d, groups):
+    say("block norm accumulate, stream, graph %dx%d" % (rows, d))
+    y, h, dx, dh, v = _draw(rows, d, (BF16, BF16), groups)
+    Y, H, DX, DH, V = y.to(DEV), h.to(DEV), dx.to(DEV), dh.to(DEV), _dev(v)
+    how = dict(kind=fg.NORM_LAYER, scale=0.9)
+
+    def step(stream=None):
+        x, h2, st = fg.gift_block_norm_forward(Y, H, **V, **how, stream=stream)
+        g = fg.gift_block_norm_backward(DX, DH, Y, h2, st, **V, **how, stream=stream)
+        return [x, h2, st] + [g[k] for k in sorted(g)]
+    want = [t.clone() for t in step()]
+    names = sorted(("dy", "dh") + tuple("d" + k for k in VECTORS))
+    acc = {"d" + k: torch.full_like(V[k], 0.25) for k in VECTORS}
+    fg.gift_block_norm_backward(DX, DH, Y, want[1], want[2], **V, **how, grads=acc, accumulate=True)
+    for name, t in zip(names, want[3:]):
+        assert name not in acc or torch.equal(acc[name], t + 0.25)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for rep in range(3):
+        for t in got:
+            t.fill_(float("nan"))
+        step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), rep
+    DX.mul_(2.0)
+    DH.mul_(2.0)   # a power of two: every gradient doubles, exactly
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got[:3], want[:3]))
+    assert all(torch.equal(p, 2 * q) for p, q in zip(got[3:], want[3:]))
+
+
+def test_offsets_past_32_bits():
+    """2.4 G elements: rows at both ends and in the middle equal those rows alone."""
+    say("block norm large offsets")
+    rows, d = 600000, 4096
+    y = torch.empty(rows, d, dtype=BF16, device=DEV).normal_()
+    h = torch.empty(rows, d, dtype=BF16, device=DEV).normal_()
+    w, gate = torch.ones(d, device=DEV), torch.full((d,), 0.5, device=DEV)
+    pick = torch.tensor([0, rows // 2, rows - 1], device=DEV)
+    x, h2, st = fg.gift_block_norm_forward(y, h, w, gate=gate)
+    alone = fg.gift_block_norm_forward(y[pick].contiguous(), h[pick].contiguous(), w, gate=gate)
+    assert torch.equal(x[pick], alone[0]) and torch.equal(h2[pick], alone[1]) and torch.equal(st[:, pick], alone[2])
+    part = fg.gift_block_norm_backward(x[pick].contiguous(), h[pick].contiguous(), y[pick].contiguous(), alone[1], alone[2], w,
+                                       gate=gate)
+    g = fg.gift_block_norm_backward(x, h, y, h2, st, w, gate=gate, grads={"dy": x, "dh": h})
+    assert torch.equal(g["dy"][pick], part["dy"]) and torch.equal(g["dh"][pick], part["dh"])
+    assert bool(torch.isfinite(g["dweight"]).all()) and bool(torch.isfinite(g["dgate"]).all())
+
+
+def test_refuses():
+    y, h = torch.zeros(4, 64, device=DEV), torch.zeros(4, 64, device=DEV)
+    w = torch.ones(64, device=DEV)
+    for bad in (y[:, ::2], y.half(), y[0], y.t(), y[:3]):
+        with pytest.raises(ValueError):
+            fg.gift_block_norm_forward(bad, h)
+    with pytest.raises(fg.GiftError):
+        fg.gift_block_norm_forward(y, h.bfloat16())
+    for gate in (w[:63], w.bfloat16(), torch.ones(3, 64, device=DEV), torch.ones(0, 64, device=DEV),
+                 torch.ones(1, 4, 64, device=DEV)):
+        with pytest.raises(ValueError):
+            fg.gift_block_norm_forward(y, h, gate=gate)
+    with pytest.raises(fg.GiftError):
+        fg.gift_block_norm_forward(y, h, post=False, post_weight=w)
+    x, h2, st = fg.gift_block_norm_forward(y, h, w)
+    with pytest.raises(ValueError):
+        fg.gift_block_norm_backward(y, h, y, h2, st[:2], w)
+    with pytest.raises(ValueError):
+        fg.gift_block_norm_backward(y, h, y, h2, st, w, accumulate=True)
+    with pytest.raises(ValueError):
+        fg.gift_block_norm_backward(y, h, y, h2, st, w, grads={"dscale": w})
+    with pytest.raises(fg.GiftError):
+        fg.gift_block_norm_backward(y, h, y, h2, st, w, grads={"dgate": w.clone()})
+    with pytest.raises(fg.GiftError):
+        fg.gift_block_norm_backward(y, h, y, h2, st, grads={"dy": False, "dh": False})

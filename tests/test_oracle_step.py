@@ -2,6 +2,7 @@
 differences, and rows left out."""
 
 import numpy as np
+import pytest
 
 from oracle import step
 
@@ -35,3 +36,32 @@ def test_rows_left_out_count_for_nothing():
     assert np.array_equal(dx[keep], dx2) and np.allclose(dw, dw2, atol=1e-15) and not dx[1:3].any()
     x[1] = np.nan
     assert np.array_equal(step.xent_backward(x, w, t, lse, np.ones(4))[1], dw)
+
+
+@pytest.mark.parametrize("groups", [0, 1, 3])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("is_layer", [True, False])
+def test_block_norm_gradients_match_differences(is_layer, post, groups):
+    """As above, along random directions of every input and vector at once."""
+    rng = np.random.default_rng(2)
+    rows, d = 6, 10
+    v = {"y": rng.standard_normal((rows, d)), "h": rng.standard_normal((rows, d)),
+         "weight": 1 + 0.3 * rng.standard_normal(d), "bias": rng.standard_normal(d)}
+    if post:
+        v["post_weight"], v["post_bias"] = 1 + 0.3 * rng.standard_normal(d), rng.standard_normal(d)
+    if groups:
+        v["gate"] = rng.standard_normal((groups, d))
+    dx, dh = rng.standard_normal((rows, d)), rng.standard_normal((rows, d))
+    how = dict(post=post, scale=0.7, layer=is_layer)
+
+    def f(v):
+        x, h2, _ = step.block_norm_forward(**v, **how)
+        return (dx * x).sum() + (dh * h2).sum()
+    _, h2, stats = step.block_norm_forward(**v, **how)
+    vec = {k: v.get(k) for k in ("weight", "post_weight", "post_bias", "gate")}
+    g = step.block_norm_backward(dx, dh, v["y"], h2, stats, **vec, **how)
+    h = 1e-5
+    for _ in range(5):
+        to = {k: rng.standard_normal(a.shape) for k, a in v.items()}
+        num = (f({k: a + h * to[k] for k, a in v.items()}) - f({k: a - h * to[k] for k, a in v.items()})) / (2 * h)
+        assert abs(num - sum((g["d" + k] * to[k]).sum() for k in v)) < 1e-7

@@ -2,10 +2,13 @@
 and bad arguments refused synchronously (before any HIP call, so no GPU is
 needed)."""
 
+import ctypes
+
 import pytest
 import torch
 
 import fac_whitening_gift_amd as fg
+from fac_whitening_gift_amd import _lib
 
 X, W, T, LOSS, LSE, DX, DW, WS = (0x100000 * i for i in range(1, 9))
 BF, F32 = fg.DTYPE_BF16, fg.DTYPE_F32
@@ -71,3 +74,59 @@ def test_python_refuses_host_tensors_and_types():
             fg.gift_xent_forward(bad, w.bfloat16(), t)
         with pytest.raises(ValueError):
             fg.gift_xent_backward(bad, w.bfloat16(), t, x[:, 0].contiguous())
+
+
+def block_norm(**case):
+    a = dict(rows=4, d=64, gate_rows=4, kind=0, post=1, y_dtype=BF, h_dtype=F32, scale=1.0, eps=1e-5, weight=W, bias=None,
+             post_weight=W, post_bias=None, gate=None)
+    a.update(case)
+    return ctypes.pointer(_lib._BlockNorm(*[a[n] for n, _ in _lib._BlockNorm._fields_]))
+
+
+BAD_BLOCK_NORMS = [
+    (SHAPE, dict(rows=0)), (SHAPE, dict(d=0)), (SHAPE, dict(d=16385)), (SHAPE, dict(rows=1 << 25)),
+    (INVALID, dict(kind=2)), (INVALID, dict(y_dtype=3)), (INVALID, dict(h_dtype=-1)),
+    (INVALID, dict(y_dtype=F32, h_dtype=BF)), (INVALID, dict(eps=-1.0)), (INVALID, dict(eps=float("nan"))),
+    (INVALID, dict(scale=float("inf"))), (INVALID, dict(scale=float("nan"))), (INVALID, dict(weight=W + 1)),
+    (INVALID, dict(gate=W + 2)), (SHAPE, dict(gate=W, gate_rows=0)), (SHAPE, dict(gate=W, gate_rows=5)),
+    (INVALID, dict(post=0)), (INVALID, dict(post=0, post_weight=None, post_bias=W)),
+]
+
+
+@pytest.mark.parametrize("want,case", BAD_BLOCK_NORMS)
+def test_block_norm_refuses(want, case):
+    lib = fg.load()
+    refused(lib.gift_block_norm_forward(block_norm(**case), X, T, DX, DW, LSE, None), want)
+    g = _lib._BlockNormGrads(0x900000)
+    refused(lib.gift_block_norm_backward(block_norm(**case), X, T, DX, DW, LSE, LOSS, W, ctypes.pointer(g), 0, WS, 1 << 30,
+                                         None), want)
+
+
+@pytest.mark.parametrize("case", [dict(y=None), dict(h=None), dict(h2=None), dict(x=None), dict(st=None), dict(y=X + 1),
+                                  dict(h=T + 2), dict(st=LSE + 2), dict(x=DX), dict(p=None)])
+def test_block_norm_forward_refuses(case):
+    a = dict(p=block_norm(), y=X, h=T, h2=DX, x=DW, st=LSE)
+    a.update(case)
+    refused(fg.load().gift_block_norm_forward(a["p"], a["y"], a["h"], a["h2"], a["x"], a["st"], None), INVALID)
+
+
+@pytest.mark.parametrize("want,case", [
+    (INVALID, dict(dx=None)), (INVALID, dict(y=None)), (INVALID, dict(h2=None)), (INVALID, dict(st=None)),
+    (INVALID, dict(dh2=T + 2)), (INVALID, dict(dy=LOSS + 1)), (INVALID, dict(dy=W, dh=W)),
+    (INVALID, dict(dy=None, dh=None, g=())), (INVALID, dict(g=(0x900000, 0x900000))), (INVALID, dict(g=(0x900002,))),
+    (INVALID, dict(g=(None, None, None, None, 0x900000))), (SMALL, dict(n=64)), (INVALID, dict(ws=None)),
+    (INVALID, dict(ws=WS + 16)), (INVALID, dict(p=dict(post=0, post_weight=None), g=(None, None, 0x900000))),
+])
+def test_block_norm_backward_refuses(want, case):
+    a = dict(p={}, dx=X, dh2=T, y=DX, h2=DW, st=LSE, dy=LOSS, dh=W, g=(0x900000,), ws=WS, n=1 << 30)
+    a.update(case)
+    g = _lib._BlockNormGrads(*a["g"])
+    refused(fg.load().gift_block_norm_backward(block_norm(**a["p"]), a["dx"], a["dh2"], a["y"], a["h2"], a["st"], a["dy"],
+                                               a["dh"], ctypes.pointer(g), 0, a["ws"], a["n"], None), want)
+
+
+def test_block_norm_sizes():
+    assert fg.gift_block_norm_backward_workspace_bytes(1000, 64) > 0
+    assert fg.gift_block_norm_backward_workspace_bytes(1000, 64, 10) > fg.gift_block_norm_backward_workspace_bytes(1000, 64)
+    for rows, d, gates in [(0, 64, 1), (4, 0, 1), (4, 16385, 1), (4, 64, 0), (4, 64, 5)]:
+        assert fg.gift_block_norm_backward_workspace_bytes(rows, d, gates) == 0
