@@ -25,4 +25,5 @@ from ._lib import (  # noqa: F401
     gift_xent_forward, gift_xent_forward_workspace_bytes, gift_xent_backward,
     gift_xent_backward_workspace_bytes,
     gift_block_norm_forward, gift_block_norm_backward, gift_block_norm_backward_workspace_bytes,
+    TensorGroup, gift_grad_norm, gift_grad_clip, gift_grad_workspace_bytes,
 )

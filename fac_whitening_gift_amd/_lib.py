@@ -61,7 +61,7 @@ EXPORTS = (
     "gift_norm_forward", "gift_norm_backward", "gift_norm_backward_workspace_bytes",
     "gift_xent_forward", "gift_xent_forward_workspace_bytes", "gift_xent_backward",
     "gift_xent_backward_workspace_bytes", "gift_block_norm_forward", "gift_block_norm_backward",
-    "gift_block_norm_backward_workspace_bytes",
+    "gift_block_norm_backward_workspace_bytes", "gift_grad_norm", "gift_grad_clip", "gift_grad_workspace_bytes",
 )
 
 
@@ -104,6 +104,10 @@ class _BlockNorm(ctypes.Structure):
 
 class _BlockNormGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dweight", "dbias", "dpost_weight", "dpost_bias", "dgate")]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -164,6 +168,9 @@ def load():
         "gift_block_norm_backward": (I, [ctypes.POINTER(_BlockNorm), P, P, P, P, P, P, P,
                                          ctypes.POINTER(_BlockNormGrads), I, P, SZ, P]),
         "gift_block_norm_backward_workspace_bytes": (SZ, [I64, I64, I64]),
+        "gift_grad_norm": (I, [ctypes.POINTER(_Tensor), I, P, P, P, P, SZ, P]),
+        "gift_grad_clip": (I, [ctypes.POINTER(_Tensor), ctypes.POINTER(_Tensor), I, P, F, F, P, P, P, SZ, P]),
+        "gift_grad_workspace_bytes": (SZ, [I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -1109,3 +1116,85 @@ def gift_block_norm_backward(dx, dh, y, h_out, stats, weight=None, bias=None, po
     _enqueue(dev, lib.gift_block_norm_backward, ctypes.byref(p), gp, hp, yp, op, sp, yg, hg, ctypes.byref(g),
              1 if accumulate else 0, wp, wb)
     return out
+
+
+class TensorGroup:
+    """Contiguous device tensors (fp32 or bf16, on one device) that are worked on
+    together, their descriptors made once: the gradients of a model, which stay
+    where they are from step to step."""
+
+    __slots__ = ("tensors", "device", "_array")
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.device = self.tensors[0].device
+        self._array = (_Tensor * len(self.tensors))()
+        for i, t in enumerate(self.tensors):
+            code = _DTYPES.get(t.dtype)
+            if code is None:
+                raise ValueError("tensor %d must be bf16 or fp32, got %s" % (i, t.dtype))
+            if not t.is_cuda or t.device != self.device:
+                raise ValueError("tensor %d is on %s, expected a device tensor on %s" % (i, t.device, self.device))
+            if not t.is_contiguous():
+                raise ValueError("tensor %d must be contiguous" % i)
+            self._array[i] = _Tensor(t.data_ptr(), t.numel(), code)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _group(tensors):
+    return tensors if isinstance(tensors, TensorGroup) else TensorGroup(tensors)
+
+
+def _word(t, dtype, name, device):
+    if t.dtype != dtype or t.device != device or t.numel() != 1:
+        raise ValueError("%s must be one %s element on %s" % (name, dtype, device))
+    return t.data_ptr()
+
+
+def gift_grad_workspace_bytes(n):
+    return int(load().gift_grad_workspace_bytes(n))
+
+
+def gift_grad_norm(tensors, norm=None, sumsq=None, flags=None, ws=None, stream=None):
+    """The 2-norm of all elements of tensors (a list, or a TensorGroup).  sumsq:
+    one fp64 element to take the sum of squares too.  -> norm (1 fp32 element)."""
+    group = _group(tensors)
+    dev = group.device
+    if stream is not None:
+        return _on(stream, dev, gift_grad_norm, group, norm, sumsq, flags, ws)
+    if norm is None:
+        norm = _f32(1, dev)
+    lib = load()
+    keep, wp, wb = _scratch(lib.gift_grad_workspace_bytes(len(group)), dev, ws)
+    _enqueue(dev, lib.gift_grad_norm, group._array, len(group),
+             None if sumsq is None else _word(sumsq, torch.float64, "sumsq", dev),
+             _word(norm, torch.float32, "norm", dev), None if flags is None else _flags_ptr(flags, dev), wp, wb)
+    return norm
+
+
+def gift_grad_clip(tensors, max_norm, eps=1e-6, out=None, sumsq=None, norm=None, flags=None, ws=None, stream=None):
+    """Scale tensors (a list, or a TensorGroup) by min(1, max_norm / (norm +
+    eps)), in place or into out (as many of the same sizes and types).  sumsq:
+    one fp64 element to go by instead of the tensors' own sum of squares.
+    -> norm (1 fp32 element)."""
+    group = _group(tensors)
+    dev = group.device
+    into = None if out is None else _group(out)
+    if into is not None and into.device != dev:
+        raise ValueError("out is on %s, expected %s" % (into.device, dev))
+    if into is not None and len(into) != len(group):
+        raise ValueError("out has %d tensors, expected %d" % (len(into), len(group)))
+    if stream is not None:
+        return _on(stream, dev, gift_grad_clip, group, max_norm, eps, into, sumsq, norm, flags, ws)
+    if norm is None:
+        norm = _f32(1, dev)
+    lib = load()
+    keep, wp, wb = _scratch(lib.gift_grad_workspace_bytes(len(group)), dev, ws)
+    _enqueue(dev, lib.gift_grad_clip, group._array, None if into is None else into._array, len(group),
+             None if sumsq is None else _word(sumsq, torch.float64, "sumsq", dev), max_norm, eps,
+             _word(norm, torch.float32, "norm", dev), None if flags is None else _flags_ptr(flags, dev), wp, wb)
+    return norm

@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "api_layer.cpp", "roundtrip.hip", "roundtrip_rt2.hip", "refresh.hip", "mx.hip",
            "norm.hip", "api_step.cpp", "xent.hip",
-           "block_norm.hip"]
+           "block_norm.hip", "grad_clip.hip"]
 
 # -packed-fp32-ops: keep hipcc from forming packed fp32 VALU ops (the host
 # pass does not know the feature and warns; that is expected).

@@ -1,6 +1,6 @@
 // Entry points of a training step around its layers (gift_xent_*,
-// gift_block_norm_* of include/gift.h): argument validation, then the launchers
-// of xent.hip and block_norm.hip.
+// gift_block_norm_*, gift_grad_* of include/gift.h): argument validation, then
+// the launchers of xent.hip, block_norm.hip and grad_clip.hip.
 #include "checks.hpp"
 #include "step.hpp"
 
@@ -53,6 +53,24 @@ gift_status check_block_norm(const gift_block_norm* p) {
   GIFT_TRY(check_vec("post_weight", p->post_weight));
   GIFT_TRY(check_vec("post_bias", p->post_bias));
   return check_vec("gate", p->gate);
+}
+
+gift_status check_tensors(const char* name, const gift_tensor* t, int n) {
+  if (!t) return fail(GIFT_ERR_INVALID_ARG, "%s is NULL", name);
+  if (n < 1 || n > kGradMaxTensors) return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%d tensors", n);
+  for (int i = 0; i < n; ++i) {
+    if (!dtype_ok(t[i].dtype)) return fail(GIFT_ERR_INVALID_ARG, "%s %d: unknown dtype %d", name, i, t[i].dtype);
+    if (t[i].n < 0 || t[i].n > (int64_t(1) << 45) / (int64_t)dtype_size(t[i].dtype))
+      return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%s %d: %lld elements", name, i, (long long)t[i].n);
+    if (t[i].n && (!t[i].data || !aligned_to(t[i].data, dtype_size(t[i].dtype))))
+      return fail(GIFT_ERR_INVALID_ARG, "%s %d is NULL or not aligned to its elements", name, i);
+  }
+  if (!grad_size_ok(t, n)) return fail(GIFT_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^45 bytes", name);
+  return GIFT_OK;
+}
+
+gift_status check_sum(const double* p) {
+  return aligned_to(p, 8) ? GIFT_OK : fail(GIFT_ERR_INVALID_ARG, "sumsq must be 8-byte aligned");
 }
 
 // two of the gradients in one buffer
@@ -164,6 +182,39 @@ gift_status gift_block_norm_backward(const gift_block_norm* p, const void* dX, c
   GIFT_TRY(check_ws(ws, ws_bytes, vectors ? block_norm_backward_ws(p->rows, p->d, gates_of(*p)) : 0));
   return launched(launch_block_norm_backward(*p, dX, dH_out, Y, H_out, stats, dY, dH, g, accumulate != 0, ws,
                                              (hipStream_t)stream));
+}
+
+size_t gift_grad_workspace_bytes(int n) { return n < 1 || n > kGradMaxTensors ? 0 : grad_ws(n); }
+
+gift_status gift_grad_norm(const gift_tensor* tensors, int n, double* sumsq, float* norm, uint32_t* dev_flags, void* ws,
+                           size_t ws_bytes, void* stream) {
+  GIFT_TRY(check_tensors("tensor", tensors, n));
+  if (!sumsq && !norm) return fail(GIFT_ERR_INVALID_ARG, "sumsq and norm are both NULL");
+  GIFT_TRY(check_sum(sumsq));
+  GIFT_TRY(check_vec("norm", norm));
+  GIFT_TRY(check_flags(dev_flags));
+  GIFT_TRY(check_ws(ws, ws_bytes, grad_ws(n)));
+  return launched(launch_grad(tensors, nullptr, n, nullptr, false, 0.f, 0.f, sumsq, norm, dev_flags, ws,
+                              (hipStream_t)stream));
+}
+
+gift_status gift_grad_clip(const gift_tensor* tensors, const gift_tensor* out, int n, const double* sumsq, float max_norm,
+                           float eps, float* norm, uint32_t* dev_flags, void* ws, size_t ws_bytes, void* stream) {
+  GIFT_TRY(check_tensors("tensor", tensors, n));
+  if (out) {
+    GIFT_TRY(check_tensors("out", out, n));
+    for (int i = 0; i < n; ++i)
+      if (out[i].n != tensors[i].n || out[i].dtype != tensors[i].dtype)
+        return fail(GIFT_ERR_INVALID_ARG, "out %d has another size or type than its tensor", i);
+  }
+  GIFT_TRY(check_sum(sumsq));
+  if (!(max_norm >= 0.f && max_norm < __builtin_inff())) return fail(GIFT_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
+  if (!(eps >= 0.f && eps < 1e30f)) return fail(GIFT_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  GIFT_TRY(check_vec("norm", norm));
+  GIFT_TRY(check_flags(dev_flags));
+  GIFT_TRY(check_ws(ws, ws_bytes, grad_ws(n)));
+  return launched(launch_grad(tensors, out, n, sumsq, true, max_norm, eps, nullptr, norm, dev_flags, ws,
+                              (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,272 @@
+// The norm of many gradients together, and clipping by it (gift_grad_* of
+// include/gift.h).  The tensors are cut into tiles of 32 KB, the tiles dealt to
+// the workgroups in contiguous runs.
+//
+//   k_grad_square  the run's sum of squares in fp64 (no square of an fp32 value
+//                  overflows or vanishes there), one partial a workgroup
+//   k_grad_norm    the partials added in a fixed order: sum and norm
+//   k_grad_scale   every workgroup adds the partials itself, in the same order,
+//                  so that clipping takes two launches; then scales its run
+#include "device.hpp"
+#include "host.hpp"
+#include "mx.hpp"
+#include "step.hpp"
+
+namespace gift {
+
+namespace {
+
+constexpr int kThreads = 256, kVecs = 8;                       // 16-byte vectors of a thread and tile
+constexpr int64_t kTileBytes = (int64_t)kThreads * kVecs * 16;
+constexpr int kMostRuns = 2048;
+constexpr int kInline = 64;                                    // descriptors in a launch's arguments
+
+struct GradTensor {
+  const void* in;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t tile;   // its first tile
+};
+
+struct GradArgs {
+  const GradTensor* table;   // NULL: d
+  int n;
+  int tiles;
+  int per;                   // tiles of a run
+  int runs;
+  double* part;              // [runs]
+  const double* given;       // the sum of squares, NULL: the partials'
+  double* sum;
+  float* norm;
+  uint32_t* flags;
+  float max_norm;
+  float eps;
+  bool in_place;
+  GradTensor d[kInline];
+};
+
+struct GradPut {
+  GradTensor* to;
+  int n;
+  GradTensor d[kInline];
+};
+
+__global__ __launch_bounds__(kInline) void k_grad_put(GradPut q) {
+  if ((int)threadIdx.x < q.n) q.to[threadIdx.x] = q.d[threadIdx.x];
+}
+
+// f(tensor, its tile) for the tiles of a run, backwards for the second pass
+template <bool kBack, class F>
+__device__ __forceinline__ void each_tile(const GradArgs& a, int run, F f) {
+  const GradTensor* d = a.table ? a.table : a.d;
+  const int begin = run * a.per, end = min(a.tiles, begin + a.per);
+  if (begin >= end) return;
+  const int first = kBack ? end - 1 : begin;
+  int lo = 0, hi = a.n - 1;   // the last tensor that begins at or before the tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (d[mid].tile <= first) lo = mid;
+    else hi = mid - 1;
+  }
+  GradTensor t = d[lo];
+  if constexpr (kBack) {
+    for (int i = end - 1; i >= begin; --i) {
+      while (i < t.tile) t = d[--lo];
+      f(t, i - t.tile);
+    }
+  } else {
+    int next = lo + 1 < a.n ? d[lo + 1].tile : a.tiles;
+    for (int i = begin; i < end; ++i) {
+      while (i >= next) {
+        t = d[++lo];
+        next = lo + 1 < a.n ? d[lo + 1].tile : a.tiles;
+      }
+      f(t, i - t.tile);
+    }
+  }
+}
+
+// the sum over the workgroup, in a fixed order
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double s[kThreads / 64];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = s[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 64; ++i) v += s[i];
+  return v;
+}
+
+template <class T>
+struct Lane {
+  static constexpr int kE = 16 / sizeof(T);
+  static __device__ __forceinline__ void open(const uint4& q, float (&o)[kE]) {
+    T v[kE];
+    __builtin_memcpy(v, &q, 16);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) o[i] = (float)v[i];
+  }
+};
+
+// sum of squares of a tile; the elements past its whole vectors go to the first
+// threads
+template <class T>
+__device__ __forceinline__ double tile_square(const T* p, int64_t n) {
+  constexpr int kE = Lane<T>::kE;
+  const int t = threadIdx.x;
+  const int vecs = (int)(n / kE);
+  uint4 q[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    q[i] = make_uint4(0, 0, 0, 0);
+    if (t + i * kThreads < vecs) q[i] = ld16(p + (int64_t)(t + i * kThreads) * kE);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    float v[kE];
+    Lane<T>::open(q[i], v);
+#pragma unroll
+    for (int j = 0; j < kE; ++j) s = __builtin_fma((double)v[j], (double)v[j], s);
+  }
+  if (vecs * kE + t < n) {
+    const double v = (double)(float)p[vecs * kE + t];
+    s = __builtin_fma(v, v, s);
+  }
+  return s;
+}
+
+template <class T>
+__device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c) {
+  constexpr int kE = Lane<T>::kE;
+  const int t = threadIdx.x;
+  const int vecs = (int)(n / kE);
+  uint4 q[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    if (t + i * kThreads < vecs) q[i] = ld16(p + (int64_t)(t + i * kThreads) * kE);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    if (t + i * kThreads >= vecs) continue;
+    float v[kE];
+    Lane<T>::open(q[i], v);
+    T r[kE];
+#pragma unroll
+    for (int j = 0; j < kE; ++j) r[j] = (T)(v[j] * c);
+    uint4 w;
+    __builtin_memcpy(&w, r, 16);
+    st16(o + (int64_t)(t + i * kThreads) * kE, w);
+  }
+  if (vecs * kE + t < n) o[vecs * kE + t] = (T)((float)p[vecs * kE + t] * c);
+}
+
+constexpr int64_t tile_elems(int32_t dtype) { return kTileBytes / (dtype == GIFT_DTYPE_BF16 ? 2 : 4); }
+
+__global__ __launch_bounds__(kThreads) void k_grad_square(GradArgs a) {
+  double s = 0.0;
+  each_tile<false>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
+    const int64_t at = tile * tile_elems(t.dtype), n = min(t.n - at, tile_elems(t.dtype));
+    if (t.dtype == GIFT_DTYPE_BF16) s += tile_square(static_cast<const __bf16*>(t.in) + at, n);
+    else s += tile_square(static_cast<const float*>(t.in) + at, n);
+  });
+  s = block_sum(s);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = s;
+}
+
+// the sum of squares, by every workgroup alike; the first one reports it
+__device__ __forceinline__ double grad_sum(const GradArgs& a) {
+  double s = 0.0;
+  if (a.given) {
+    s = *a.given;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kMostRuns / kThreads; ++i) {
+      const int r = threadIdx.x + i * kThreads;
+      if (r < a.runs) s += a.part[r];
+    }
+    s = block_sum(s);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (a.sum) *a.sum = s;
+    if (a.norm) *a.norm = (float)sqrt(s);
+    if (a.flags && !(s < __builtin_inf())) atomicOr(a.flags, GIFT_FLAG_NONFINITE);
+  }
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a) { grad_sum(a); }
+
+__global__ __launch_bounds__(kThreads) void k_grad_scale(GradArgs a) {
+  const double q = grad_sum(a), f = (double)a.max_norm / (sqrt(q) + (double)a.eps);
+  const float c = f >= 1.0 || q == 0.0 ? 1.f : (float)f;
+  if (c == 1.f && a.in_place) return;
+  each_tile<true>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
+    const int64_t at = tile * tile_elems(t.dtype), n = min(t.n - at, tile_elems(t.dtype));
+    if (t.dtype == GIFT_DTYPE_BF16)
+      tile_scale(static_cast<const __bf16*>(t.in) + at, static_cast<__bf16*>(t.out) + at, n, c);
+    else tile_scale(static_cast<const float*>(t.in) + at, static_cast<float*>(t.out) + at, n, c);
+  });
+}
+
+int64_t tiles_of(const gift_tensor* t, int n) {
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += (t[i].n + tile_elems(t[i].dtype) - 1) / tile_elems(t[i].dtype);
+  return tiles;
+}
+
+}  // namespace
+
+bool grad_size_ok(const gift_tensor* t, int n) { return tiles_of(t, n) < (int64_t(1) << 30); }
+
+size_t grad_ws(int n) {
+  return align_up(kMostRuns * sizeof(double)) + (n > kInline ? align_up((size_t)n * sizeof(GradTensor)) : 0);
+}
+
+hipError_t launch_grad(const gift_tensor* t, const gift_tensor* out, int n, const double* given, bool scale,
+                       float max_norm, float eps, double* sum, float* norm, uint32_t* flags, void* ws, hipStream_t s) {
+  GradArgs a{};
+  a.n = n;
+  a.tiles = (int)tiles_of(t, n);
+  a.per = (a.tiles + kMostRuns - 1) / kMostRuns;
+  if (a.per < 1) a.per = 1;
+  a.runs = a.tiles ? (a.tiles + a.per - 1) / a.per : 1;
+  a.part = static_cast<double*>(ws);
+  a.given = given;
+  a.sum = sum;
+  a.norm = norm;
+  a.flags = flags;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.in_place = true;
+  GradTensor* table = n > kInline ? reinterpret_cast<GradTensor*>(static_cast<uint8_t*>(ws) + align_up(kMostRuns * sizeof(double)))
+                                  : nullptr;
+  GradPut q{};
+  int tile = 0;
+  for (int i = 0; i < n; ++i) {
+    GradTensor d{t[i].data, out ? out[i].data : t[i].data, t[i].n, t[i].dtype, tile};
+    a.in_place = a.in_place && d.in == d.out;
+    tile += (int)((d.n + tile_elems(d.dtype) - 1) / tile_elems(d.dtype));
+    if (!table) {
+      a.d[i] = d;
+      continue;
+    }
+    q.d[q.n++] = d;
+    if (q.n == kInline || i + 1 == n) {
+      q.to = table + (i + 1 - q.n);
+      k_grad_put<<<dim3(1), dim3(kInline), 0, s>>>(q);
+      q.n = 0;
+    }
+  }
+  a.table = table;
+  const dim3 grid((uint32_t)a.runs), block(kThreads);
+  if (!given) k_grad_square<<<grid, block, 0, s>>>(a);
+  if (scale) k_grad_scale<<<grid, block, 0, s>>>(a);
+  else k_grad_norm<<<dim3(1), block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace gift

@@ -46,4 +46,11 @@ hipError_t launch_block_norm_backward(const gift_block_norm& p, const void* dX, 
                                       const void* H2, const float* stats, void* dY, void* dH,
                                       const gift_block_norm_grads& g, bool accumulate, void* ws, hipStream_t s);
 
+// grad_clip.hip
+constexpr int kGradMaxTensors = 1 << 16;
+bool grad_size_ok(const gift_tensor* t, int n);
+size_t grad_ws(int n);
+hipError_t launch_grad(const gift_tensor* t, const gift_tensor* out, int n, const double* given, bool scale,
+                       float max_norm, float eps, double* sum, float* norm, uint32_t* flags, void* ws, hipStream_t s);
+
 }  // namespace gift

@@ -618,6 +618,36 @@ gift_status gift_block_norm_backward(const gift_block_norm *p, const void *dX, c
                                      int accumulate, void *ws, size_t ws_bytes, void *stream);
 size_t gift_block_norm_backward_workspace_bytes(int64_t rows, int64_t d, int64_t gates);
 
+/*
+ * gift_grad_norm -- the 2-norm of all elements of n tensors together (the
+ * gradients of a model): sumsq = their sum of squares, fp64, norm = its root,
+ * fp32, either may be NULL, not both.  Squares and sums are fp64, added in an
+ * order that depends on the tensors' sizes and types alone.  dev_flags
+ * (optional): NONFINITE where the sum is NaN or infinite.  The tensors are a
+ * HOST array, dense, element aligned; one may be empty (its data is not read).
+ * At most 2^16 tensors, 2^45 bytes.
+ *
+ * gift_grad_clip -- every element times c = min(1, max_norm / (norm + eps)),
+ * one rounding to its type.  sumsq: the sum of squares to go by, device fp64
+ * (gift_grad_norm's, summed over the ranks of a data-parallel job); NULL: the
+ * tensors' own.  out: n tensors of the same sizes and types to write, which
+ * must not overlap the tensors but may be they; NULL: in place, where nothing
+ * is written if c is 1.  norm (optional): as above.  A sum that is NaN makes
+ * every element NaN, an infinite one gives c = 0 (0, and NaN for what was
+ * infinite).
+ */
+typedef struct gift_tensor {
+    void *data;
+    int64_t n;
+    int32_t dtype;               /* GIFT_DTYPE_* */
+} gift_tensor;
+gift_status gift_grad_norm(const gift_tensor *tensors, int n, double *sumsq, float *norm,
+                           uint32_t *dev_flags, void *ws, size_t ws_bytes, void *stream);
+gift_status gift_grad_clip(const gift_tensor *tensors, const gift_tensor *out, int n,
+                           const double *sumsq, float max_norm, float eps, float *norm,
+                           uint32_t *dev_flags, void *ws, size_t ws_bytes, void *stream);
+size_t gift_grad_workspace_bytes(int n);
+
 const char *gift_status_string(int status);
 /* Thread-local detail of the last failing call on this thread. */
 const char *gift_last_error(void);

@@ -1,5 +1,5 @@
-"""The loss over a vocabulary and the norms between blocks, with their gradients
-(oracle; test infrastructure only), fp64 formulas.
+"""The loss over a vocabulary and the norms between blocks, with their gradients,
+and gradient clipping (oracle; test infrastructure only), fp64 formulas.
 
 A row whose target is negative or past the vocabulary is left out: loss 0, no
 part in the gradients, whatever it holds.
@@ -92,3 +92,12 @@ def block_norm_backward(dx, dh, y, h2, stats, weight=None, post=True, post_weigh
     groups = 1 if gate is None else np.asarray(gate).size // d
     out["dgate"] = (t * n).reshape(groups, rows // groups, d).sum(axis=1)
     return out
+
+
+def grad_clip(tensors, max_norm=None, eps=1e-6, sumsq=None):
+    """-> (sum of squares, norm, clipped tensors) in fp64."""
+    tensors = [np.asarray(t, dtype=np.float64) for t in tensors]
+    q = sum((t * t).sum() for t in tensors) if sumsq is None else sumsq
+    norm = np.sqrt(q)
+    c = 1.0 if max_norm is None or q == 0 else min(1.0, max_norm / (norm + eps))
+    return q, norm, [t * c for t in tensors]

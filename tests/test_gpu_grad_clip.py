@@ -1,0 +1,193 @@
+"""The norm of many gradients and clipping by it on the device (gift_grad_*)
+against fp64.
+
+Squares and sums are fp64 on both sides: N terms in another order differ by at
+most 2 N 2^-53 of a sum of squares.  The norm is rounded to fp32 (2^-24), the
+factor c too (2^-24, with the sum's error), and an element times c to its type
+(half a step of it).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fac_whitening_gift_amd as fg
+from oracle import step as os_
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _draw(shapes, seed=0, types=(F32,), scale=1e-3):
+    rng = np.random.default_rng(seed)
+    return [torch.from_numpy((scale * rng.standard_normal(s)).astype(np.float32)).to(types[i % len(types)])
+            for i, s in enumerate(shapes)]
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _check(tensors, max_norm, eps, norm, out, sumsq=None):
+    q, want, ref = os_.grad_clip([_np(t) for t in tensors], max_norm, eps, sumsq)
+    n = sum(t.numel() for t in tensors)
+    e = 2 * n * 2.0 ** -53 + 2.0 ** -50
+    assert abs(float(norm) - want) <= (U + e) * want
+    for t, o, r in zip(tensors, out, ref):
+        assert o.dtype == t.dtype and o.shape == t.shape
+        tol = (U + 2 * e) * np.abs(r)
+        assert np.all(np.abs(_np(o) - r) <= tol + torch.finfo(t.dtype).eps / 2 * (np.abs(r) + tol) + 1e-45)
+
+
+LISTS = [[(1,)], [(3, 5), (7,), (1,)], [(0,), (4,), (0, 3), (5,)], [(8192,), (8193,), (8191,)], [(16384,), (16385,)],
+         [(300, 257)] * 3 + [(1000,)] * 5, [(i + 1,) for i in range(64)], [(2 * i,) for i in range(65)],
+         [(17, 31)] * 200, [(3,)] * 1000, [(2000, 3001)]]
+
+
+@pytest.mark.parametrize("types", [(F32,), (BF16,), (F32, BF16)])
+@pytest.mark.parametrize("shapes", LISTS, ids=[str(i) for i in range(len(LISTS))])
+def test_norm_and_clip(shapes, types):
+    say("grad clip %d tensors, first %s, %s" % (len(shapes), shapes[0], types))
+    tensors = _draw(shapes, len(shapes), types)
+    dev = [t.to(DEV) for t in tensors]
+    sumsq = torch.empty(1, dtype=torch.float64, device=DEV)
+    norm = fg.gift_grad_norm(dev, sumsq=sumsq)
+    q, want, _ = os_.grad_clip([_np(t) for t in tensors])
+    n = sum(t.numel() for t in tensors)
+    assert abs(float(sumsq) - q) <= (2 * n * 2.0 ** -53 + 1e-15) * q
+    assert abs(float(norm) - want) <= (U + 2 * n * 2.0 ** -53 + 1e-15) * want
+    for max_norm in (0.3 * want, 5 * want, 0.0):
+        out = [torch.full_like(t, 9.0) for t in dev]
+        got = fg.gift_grad_clip(dev, max_norm, out=out)
+        _check(tensors, np.float32(max_norm), np.float32(1e-6), got, out)
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(dev, tensors))   # read, not written
+        inside = [t.clone() for t in dev]
+        assert torch.equal(fg.gift_grad_clip(fg.TensorGroup(inside), max_norm), got)
+        assert all(torch.equal(a, b) for a, b in zip(inside, out))
+    again = fg.gift_grad_norm(dev)
+    assert torch.equal(again, norm)
+
+
+def test_tensors_at_any_element_of_a_buffer():
+    """One behind the other, in place: nothing between or beside them is written."""
+    say("grad clip views")
+    for dtype in (F32, BF16):
+        flat = torch.full((50000,), 3.0, dtype=dtype, device=DEV)
+        views, at, left = [], 1, []
+        for n in (1, 7, 8, 9, 4097, 1, 20000, 13):
+            views.append(flat[at:at + n])
+            left.append(at + n)
+            at += n + 1
+        for i, v in enumerate(views):
+            v.copy_(_draw([tuple(v.shape)], i)[0])
+        before = [v.cpu().clone() for v in views]
+        norm = fg.gift_grad_clip(views, 1e-2, eps=0.0)
+        _check(before, np.float32(1e-2), 0.0, norm, views)
+        assert float(flat[0]) == 3.0 and all(float(flat[i]) == 3.0 for i in left)
+
+
+def test_a_sum_from_elsewhere():
+    """Clipping by the sum over ranks: two halves' sums added."""
+    say("grad clip given sum")
+    a, b = _draw([(300, 40), (5,)], 1), _draw([(77,), (900, 9)], 2)
+    qs = [torch.empty(1, dtype=torch.float64, device=DEV) for _ in range(2)]
+    for t, q in zip((a, b), qs):
+        fg.gift_grad_norm([x.to(DEV) for x in t], sumsq=q)
+    total = qs[0] + qs[1]
+    out = [x.to(DEV) for x in a]
+    norm = fg.gift_grad_clip(out, 1e-2, sumsq=total)
+    _check(a, np.float32(1e-2), np.float32(1e-6), norm, out, sumsq=float(total))
+
+
+def test_far_values_and_nonfinite():
+    """Squares past fp32's range at both ends; NaN and infinities flagged."""
+    say("grad clip far values")
+    for scale in (1e30, 1e-30):
+        t = _draw([(5000,), (33,)], 4, scale=scale)
+        dev = [x.to(DEV) for x in t]
+        norm = fg.gift_grad_clip(dev, scale, eps=0.0)
+        _check(t, np.float32(scale), 0.0, norm, dev)
+    flags = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x = torch.ones(100, device=DEV)
+    fg.gift_grad_clip([x], 1.0, flags=flags)
+    assert int(flags) == 0
+    x[3] = float("inf")
+    norm = fg.gift_grad_clip([x], 1.0, flags=flags)
+    assert int(flags) == fg.FLAG_NONFINITE and bool(torch.isinf(norm))
+    assert bool(torch.isnan(x[3])) and float(x.nan_to_num().abs().sum()) == 0.0
+    x.fill_(1.0)
+    x[5] = float("nan")
+    norm = fg.gift_grad_clip([x], 1.0, flags=flags)
+    assert bool(torch.isnan(norm)) and bool(torch.isnan(x).all())
+    z = torch.zeros(70, device=DEV)
+    assert float(fg.gift_grad_clip([z], 0.0, eps=0.0)) == 0.0 and not bool(z.any())
+
+
+@pytest.mark.parametrize("n", [3, 150])
+def test_stream_and_graph(n):
+    """On another stream; captured: replays, with eager work between them, equal
+    the eager calls and read the live gradients."""
+    say("grad clip stream and graph n=%d" % n)
+    dev = [t.to(DEV) for t in _draw([(200, 33)] * n, 5, (F32, BF16))]
+    out = [torch.empty_like(t) for t in dev]
+    group, into = fg.TensorGroup(dev), fg.TensorGroup(out)
+    norm = fg.gift_grad_clip(group, 1e-2, out=into)
+    want = [norm.clone()] + [t.clone() for t in out]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for t in out:
+        t.fill_(7.0)
+    side.wait_stream(torch.cuda.current_stream())
+    got = fg.gift_grad_clip(group, 1e-2, out=into, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip([got] + out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fg.gift_grad_clip(group, 1e-2, out=into)
+    for rep in range(3):
+        for t in out:
+            t.fill_(float("nan"))
+        fg.gift_grad_norm(group)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([got] + out, want)), rep
+    for t in dev:
+        t.mul_(2.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, 2 * want[0])
+
+
+def test_offsets_past_32_bits():
+    """A tensor of 4.4 G elements beside small ones: its end is counted and scaled."""
+    say("grad clip large offsets")
+    n = 2 ** 32 + 100000
+    x = torch.zeros(n, dtype=BF16, device=DEV)
+    x[n - 3:] = 2.0
+    y = torch.full((5,), 4.0, device=DEV)
+    norm = fg.gift_grad_clip([y, x, y.clone()], 1.0, eps=0.0)
+    assert float(norm) == float(np.float32(np.sqrt(12.0 + 160.0)))
+    c = np.float32(1.0 / np.sqrt(172.0))
+    assert torch.equal(x[n - 3:].float().cpu(), torch.full((3,), float(torch.tensor(2.0 * float(c)).to(BF16))))
+    assert not bool(x[:1000].any()) and abs(float(y[0]) - 4.0 * c) <= 4.0 * c * 2.0 ** -23
+
+
+def test_refuses():
+    x = torch.zeros(4, 64, device=DEV)
+    for bad in ([], [x.half()], [x.cpu()], [x.t()], [x, x.double()]):
+        with pytest.raises(ValueError):
+            fg.gift_grad_norm(bad)
+    with pytest.raises(ValueError):
+        fg.gift_grad_clip([x], 1.0, out=[x, x])
+    with pytest.raises(ValueError):
+        fg.gift_grad_clip([x], 1.0, sumsq=torch.zeros(1, device=DEV))
+    for out in ([x.bfloat16()], [x[:2].contiguous()]):
+        with pytest.raises(fg.GiftError):
+            fg.gift_grad_clip([x], 1.0, out=out)
+    for bad in (-1.0, float("nan"), float("inf")):
+        with pytest.raises(fg.GiftError):
+            fg.gift_grad_clip([x], bad)

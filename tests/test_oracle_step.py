@@ -65,3 +65,14 @@ def test_block_norm_gradients_match_differences(is_layer, post, groups):
         to = {k: rng.standard_normal(a.shape) for k, a in v.items()}
         num = (f({k: a + h * to[k] for k, a in v.items()}) - f({k: a - h * to[k] for k, a in v.items()})) / (2 * h)
         assert abs(num - sum((g["d" + k] * to[k]).sum() for k in v)) < 1e-7
+
+
+def test_grad_clip():
+    rng = np.random.default_rng(3)
+    t = [rng.standard_normal((3, 4)), np.zeros((0, 5)), rng.standard_normal(7)]
+    flat = np.concatenate([v.ravel() for v in t])
+    q, norm, out = step.grad_clip(t, 0.5, 0.0)
+    assert np.isclose(q, flat @ flat) and np.isclose(norm, np.linalg.norm(flat))
+    assert np.isclose(np.sqrt(sum((v * v).sum() for v in out)), 0.5)
+    assert all(np.array_equal(a, b) for a, b in zip(step.grad_clip(t, 100.0)[2], t))
+    assert not step.grad_clip([np.zeros(3)], 0.0, 0.0)[2][0].any()

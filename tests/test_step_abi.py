@@ -130,3 +130,54 @@ def test_block_norm_sizes():
     assert fg.gift_block_norm_backward_workspace_bytes(1000, 64, 10) > fg.gift_block_norm_backward_workspace_bytes(1000, 64)
     for rows, d, gates in [(0, 64, 1), (4, 0, 1), (4, 16385, 1), (4, 64, 0), (4, 64, 5)]:
         assert fg.gift_block_norm_backward_workspace_bytes(rows, d, gates) == 0
+
+
+def tensors(*specs):
+    return (_lib._Tensor * len(specs))(*[_lib._Tensor(*s) for s in specs])
+
+
+GOOD = (X, 100, F32)
+
+
+@pytest.mark.parametrize("want,t,n", [
+    (INVALID, None, 1), (SHAPE, tensors(GOOD), 0), (SHAPE, tensors(GOOD), -1), (SHAPE, tensors(GOOD), (1 << 16) + 1),
+    (INVALID, tensors((None, 100, F32)), 1), (INVALID, tensors((X + 2, 100, F32)), 1), (INVALID, tensors((X + 1, 100, BF)), 1),
+    (INVALID, tensors((X, 100, 2)), 1), (SHAPE, tensors((X, -1, F32)), 1), (SHAPE, tensors((X, 1 << 44, F32)), 1),
+    (SHAPE, tensors((X, 1 << 43, F32), (X, 1 << 43, F32)), 2), (INVALID, tensors(GOOD, (None, 1, BF)), 2),
+])
+def test_grad_refuses_tensors(want, t, n):
+    lib = fg.load()
+    refused(lib.gift_grad_norm(t, n, LSE, None, None, WS, 1 << 30, None), want)
+    refused(lib.gift_grad_clip(t, None, n, None, 1.0, 0.0, None, None, WS, 1 << 30, None), want)
+    if t is not None:
+        refused(lib.gift_grad_clip(tensors(GOOD, GOOD), t, n, None, 1.0, 0.0, None, None, WS, 1 << 30, None), want)
+
+
+@pytest.mark.parametrize("want,case", [
+    (INVALID, dict(sumsq=None, norm=None)), (INVALID, dict(sumsq=LSE + 4)), (INVALID, dict(norm=LOSS + 2)),
+    (INVALID, dict(flags=0x50002)), (SMALL, dict(n=16)), (INVALID, dict(ws=None)), (INVALID, dict(ws=WS + 8)),
+])
+def test_grad_norm_refuses(want, case):
+    a = dict(sumsq=LSE, norm=LOSS, flags=None, ws=WS, n=1 << 30)
+    a.update(case)
+    refused(fg.load().gift_grad_norm(tensors(GOOD), 1, a["sumsq"], a["norm"], a["flags"], a["ws"], a["n"], None), want)
+
+
+@pytest.mark.parametrize("want,case", [
+    (INVALID, dict(out=tensors((W, 99, F32)))), (INVALID, dict(out=tensors((W, 100, BF)))), (INVALID, dict(sumsq=LSE + 1)),
+    (INVALID, dict(max_norm=-1.0)), (INVALID, dict(max_norm=float("inf"))), (INVALID, dict(max_norm=float("nan"))),
+    (INVALID, dict(eps=-1.0)), (INVALID, dict(eps=float("nan"))), (INVALID, dict(norm=LOSS + 1)),
+    (INVALID, dict(flags=0x50001)), (SMALL, dict(n=16)), (INVALID, dict(ws=None)),
+])
+def test_grad_clip_refuses(want, case):
+    a = dict(out=None, sumsq=None, max_norm=1.0, eps=0.0, norm=None, flags=None, ws=WS, n=1 << 30)
+    a.update(case)
+    refused(fg.load().gift_grad_clip(tensors(GOOD), a["out"], 1, a["sumsq"], a["max_norm"], a["eps"], a["norm"], a["flags"],
+                                     a["ws"], a["n"], None), want)
+
+
+def test_grad_sizes():
+    assert fg.gift_grad_workspace_bytes(0) == 0 and fg.gift_grad_workspace_bytes((1 << 16) + 1) == 0
+    assert 0 < fg.gift_grad_workspace_bytes(1) < fg.gift_grad_workspace_bytes(1000)
+    with pytest.raises(ValueError):
+        fg.TensorGroup([torch.zeros(4)])
