@@ -1,5 +1,5 @@
 // The norm of many gradients together, and clipping by it (gift_grad_* of
-// include/gift.h).  The tensors are cut into tiles of 32 KB, the tiles dealt to
+// include/gift.h).  The tensors are cut into tiles of 16 KB, the tiles dealt to
 // the workgroups in contiguous runs.
 //
 //   k_grad_square  the run's sum of squares in fp64 (no square of an fp32 value
@@ -7,19 +7,26 @@
 //   k_grad_norm    the partials added in a fixed order: sum and norm
 //   k_grad_scale   every workgroup adds the partials itself, in the same order,
 //                  so that clipping takes two launches; then scales its run
+//
+// Bound by memory.  778 M fp32 elements (3.1 GB, 219 tensors) into other buffers:
+// 546 us for the squares (5.7 TB/s) and 1200 us for the scaling (5.2; a copy of
+// 4 GB runs at 4.9), of the two launches that put the descriptors into memory 5
+// each; 12.8 M elements of 9 tensors, which stay in the memory-side cache, 9.4
+// and 17 us.
 #include "device.hpp"
 #include "host.hpp"
 #include "mx.hpp"
+#include "product.hpp"
 #include "step.hpp"
 
 namespace gift {
 
 namespace {
 
-constexpr int kThreads = 256, kVecs = 8;                       // 16-byte vectors of a thread and tile
+constexpr int kThreads = 256, kVecs = 4;                       // 16-byte vectors of a thread and tile
 constexpr int64_t kTileBytes = (int64_t)kThreads * kVecs * 16;
 constexpr int kMostRuns = 2048;
-constexpr int kInline = 64;                                    // descriptors in a launch's arguments
+constexpr int kInline = 120;                                   // descriptors in a launch's arguments (4 KB)
 
 struct GradTensor {
   const void* in;
@@ -45,6 +52,7 @@ struct GradArgs {
   bool in_place;
   GradTensor d[kInline];
 };
+static_assert(sizeof(GradArgs) <= 4096 && kInline <= 128, "a launch's arguments, k_grad_put's threads");
 
 struct GradPut {
   GradTensor* to;
@@ -52,35 +60,57 @@ struct GradPut {
   GradTensor d[kInline];
 };
 
-__global__ __launch_bounds__(kInline) void k_grad_put(GradPut q) {
+__global__ __launch_bounds__(128) void k_grad_put(GradPut q) {
   if ((int)threadIdx.x < q.n) q.to[threadIdx.x] = q.d[threadIdx.x];
 }
 
-// f(tensor, its tile) for the tiles of a run, backwards for the second pass
-template <bool kBack, class F>
+// A descriptor in scalar registers, so that a tile's loads take their base from
+// there; pointers read from memory say nothing of their address space, and as
+// global ones they need no flat access.
+template <bool kTable>
+__device__ __forceinline__ GradTensor descriptor(const GradArgs& a, int i) {
+  if constexpr (!kTable) return a.d[i];
+  const GradTensor& d = a.table[i];
+  GradTensor t;
+  t.in = reinterpret_cast<const void*>(uniform64(reinterpret_cast<uint64_t>(d.in)));
+  t.out = reinterpret_cast<void*>(uniform64(reinterpret_cast<uint64_t>(d.out)));
+  t.n = (int64_t)uniform64((uint64_t)d.n);
+  t.dtype = __builtin_amdgcn_readfirstlane(d.dtype);
+  t.tile = __builtin_amdgcn_readfirstlane(d.tile);
+  return t;
+}
+
+// f(tensor, its tile) for the tiles of a run, backwards for the second pass: what
+// the first one read last is in the memory-side cache
+template <bool kTable, bool kBack, class F>
 __device__ __forceinline__ void each_tile(const GradArgs& a, int run, F f) {
-  const GradTensor* d = a.table ? a.table : a.d;
   const int begin = run * a.per, end = min(a.tiles, begin + a.per);
   if (begin >= end) return;
   const int first = kBack ? end - 1 : begin;
-  int lo = 0, hi = a.n - 1;   // the last tensor that begins at or before the tile
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (d[mid].tile <= first) lo = mid;
-    else hi = mid - 1;
+  // the last tensor that begins at or before the tile: 64 of them looked at at a
+  // time, a load's latency each
+  int lo = 0;
+  const int lane = threadIdx.x & 63;
+  const GradTensor* d = kTable ? a.table : a.d;
+  for (int step = a.n > 64 * 64 ? 64 * 64 : a.n > 64 ? 64 : 1;; step /= 64) {
+    const int i = lo + lane * step;
+    lo += (__popcll(__ballot(i < a.n && d[min(i, a.n - 1)].tile <= first)) - 1) * step;
+    if (step == 1) break;
   }
-  GradTensor t = d[lo];
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  GradTensor t = descriptor<kTable>(a, lo);
   if constexpr (kBack) {
     for (int i = end - 1; i >= begin; --i) {
-      while (i < t.tile) t = d[--lo];
+      while (i < t.tile) t = descriptor<kTable>(a, --lo);
       f(t, i - t.tile);
     }
   } else {
-    int next = lo + 1 < a.n ? d[lo + 1].tile : a.tiles;
+    GradTensor u = descriptor<kTable>(a, min(lo + 1, a.n - 1));
     for (int i = begin; i < end; ++i) {
-      while (i >= next) {
-        t = d[++lo];
-        next = lo + 1 < a.n ? d[lo + 1].tile : a.tiles;
+      while (lo + 1 < a.n && i >= u.tile) {
+        t = u;
+        ++lo;
+        u = descriptor<kTable>(a, min(lo + 1, a.n - 1));
       }
       f(t, i - t.tile);
     }
@@ -112,19 +142,37 @@ struct Lane {
   }
 };
 
-// sum of squares of a tile; the elements past its whole vectors go to the first
+template <class T>
+using global_p = __attribute__((address_space(1))) T*;
+
+// A tile's vectors, all loads in flight at once; of a tensor's last tile those
+// that it has, zeros else.
+template <class T>
+__device__ __forceinline__ void load_tile(const T* base, int vecs, uint4 (&q)[kVecs]) {
+  constexpr int kE = Lane<T>::kE;
+  const auto p = (global_p<const any16<T>>)reinterpret_cast<uintptr_t>(base);
+  auto at = [&](int v) {
+    return __builtin_bit_cast(uint4, *(global_p<const any16<T>>)((global_p<const T>)p + v * kE));
+  };
+  const int t = threadIdx.x;
+  if (vecs == kVecs * kThreads) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) q[i] = at(t + i * kThreads);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) q[i] = t + i * kThreads < vecs ? at(t + i * kThreads) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// sum of squares of a tile, its loads unconditional where it is whole: one branch
+// a vector makes each wait for the one before (880 -> 546 us); the elements past its whole vectors go to the first
 // threads
 template <class T>
-__device__ __forceinline__ double tile_square(const T* p, int64_t n) {
+__device__ __forceinline__ double tile_square(const T* p, int n) {
   constexpr int kE = Lane<T>::kE;
-  const int t = threadIdx.x;
-  const int vecs = (int)(n / kE);
+  const int t = threadIdx.x, vecs = n / kE;
   uint4 q[kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    q[i] = make_uint4(0, 0, 0, 0);
-    if (t + i * kThreads < vecs) q[i] = ld16(p + (int64_t)(t + i * kThreads) * kE);
-  }
+  load_tile(p, vecs, q);
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -140,36 +188,38 @@ __device__ __forceinline__ double tile_square(const T* p, int64_t n) {
   return s;
 }
 
+// Results go around the caches: into other buffers that keeps more of what is
+// read in them (92 M bf16 elements 132 -> 109 us with the squares), in place it
+// makes no difference.
 template <class T>
-__device__ __forceinline__ void tile_scale(const T* p, T* o, int64_t n, float c) {
+__device__ __forceinline__ void tile_scale(const T* p, T* o, int n, float c) {
   constexpr int kE = Lane<T>::kE;
-  const int t = threadIdx.x;
-  const int vecs = (int)(n / kE);
+  const int t = threadIdx.x, vecs = n / kE;
+  const auto to = (global_p<T>)reinterpret_cast<uintptr_t>(o);
   uint4 q[kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i)
-    if (t + i * kThreads < vecs) q[i] = ld16(p + (int64_t)(t + i * kThreads) * kE);
+  load_tile(p, vecs, q);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    if (t + i * kThreads >= vecs) continue;
     float v[kE];
     Lane<T>::open(q[i], v);
     T r[kE];
 #pragma unroll
     for (int j = 0; j < kE; ++j) r[j] = (T)(v[j] * c);
-    uint4 w;
+    any16<T> w;
     __builtin_memcpy(&w, r, 16);
-    st16(o + (int64_t)(t + i * kThreads) * kE, w);
+    if (t + i * kThreads < vecs) __builtin_nontemporal_store(w, (global_p<any16<T>>)(to + (t + i * kThreads) * kE));
   }
-  if (vecs * kE + t < n) o[vecs * kE + t] = (T)((float)p[vecs * kE + t] * c);
+  if (vecs * kE + t < n) to[vecs * kE + t] = (T)((float)p[vecs * kE + t] * c);
 }
 
 constexpr int64_t tile_elems(int32_t dtype) { return kTileBytes / (dtype == GIFT_DTYPE_BF16 ? 2 : 4); }
 
+template <bool kTable>
 __global__ __launch_bounds__(kThreads) void k_grad_square(GradArgs a) {
   double s = 0.0;
-  each_tile<false>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
-    const int64_t at = tile * tile_elems(t.dtype), n = min(t.n - at, tile_elems(t.dtype));
+  each_tile<kTable, false>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
+    const int64_t at = tile * tile_elems(t.dtype);
+    const int n = (int)min(t.n - at, tile_elems(t.dtype));
     if (t.dtype == GIFT_DTYPE_BF16) s += tile_square(static_cast<const __bf16*>(t.in) + at, n);
     else s += tile_square(static_cast<const float*>(t.in) + at, n);
   });
@@ -200,12 +250,14 @@ __device__ __forceinline__ double grad_sum(const GradArgs& a) {
 
 __global__ __launch_bounds__(kThreads) void k_grad_norm(GradArgs a) { grad_sum(a); }
 
+template <bool kTable>
 __global__ __launch_bounds__(kThreads) void k_grad_scale(GradArgs a) {
   const double q = grad_sum(a), f = (double)a.max_norm / (sqrt(q) + (double)a.eps);
   const float c = f >= 1.0 || q == 0.0 ? 1.f : (float)f;
   if (c == 1.f && a.in_place) return;
-  each_tile<true>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
-    const int64_t at = tile * tile_elems(t.dtype), n = min(t.n - at, tile_elems(t.dtype));
+  each_tile<kTable, true>(a, blockIdx.x, [&](const GradTensor& t, int tile) {
+    const int64_t at = tile * tile_elems(t.dtype);
+    const int n = (int)min(t.n - at, tile_elems(t.dtype));
     if (t.dtype == GIFT_DTYPE_BF16)
       tile_scale(static_cast<const __bf16*>(t.in) + at, static_cast<__bf16*>(t.out) + at, n, c);
     else tile_scale(static_cast<const float*>(t.in) + at, static_cast<float*>(t.out) + at, n, c);
@@ -257,14 +309,18 @@ hipError_t launch_grad(const gift_tensor* t, const gift_tensor* out, int n, cons
     q.d[q.n++] = d;
     if (q.n == kInline || i + 1 == n) {
       q.to = table + (i + 1 - q.n);
-      k_grad_put<<<dim3(1), dim3(kInline), 0, s>>>(q);
+      k_grad_put<<<dim3(1), dim3(128), 0, s>>>(q);
       q.n = 0;
     }
   }
   a.table = table;
   const dim3 grid((uint32_t)a.runs), block(kThreads);
-  if (!given) k_grad_square<<<grid, block, 0, s>>>(a);
-  if (scale) k_grad_scale<<<grid, block, 0, s>>>(a);
+  if (!given) {
+    if (table) k_grad_square<true><<<grid, block, 0, s>>>(a);
+    else k_grad_square<false><<<grid, block, 0, s>>>(a);
+  }
+  if (scale && table) k_grad_scale<true><<<grid, block, 0, s>>>(a);
+  else if (scale) k_grad_scale<false><<<grid, block, 0, s>>>(a);
   else k_grad_norm<<<dim3(1), block, 0, s>>>(a);
   return hipGetLastError();
 }
