@@ -22,83 +22,89 @@ namespace gift {
 
 namespace {
 
-// 8 elements of T as they lie in memory
-template <class T>
-struct Raw {
-  uint4 q[8 * sizeof(T) / 16];
+// A row's columns: kNV vectors of 8 a lane, over the whole vectors of the row,
+// and with kTail one column more, of those behind them (fewer than 8, a lane
+// each).  A lane's values are kE floats in that order.
+template <int kL, int kNV, bool kTail>
+struct Cols {
+  static constexpr int kE = kNV * 8 + (kTail ? 1 : 0);
+  int d, whole, l;
+  __device__ __forceinline__ Cols(int width, int lane) : d(width), whole(kTail ? width & ~7 : width), l(lane) {}
+  __device__ __forceinline__ int col(int e) const {
+    return e < kNV * 8 ? ((e >> 3) * kL + l) * 8 + (e & 7) : whole + l;
+  }
+  __device__ __forceinline__ bool in(int e) const { return e < kNV * 8 ? ((e >> 3) * kL + l) * 8 < whole : whole + l < d; }
 };
 
-// A lane's 8 columns at `at` of a row of d: the row's last vector is loaded to
-// end with the row and moved into place (unpack8); columns past the row read its
-// last ones.
-template <class T, bool kTail>
-__device__ __forceinline__ Raw<T> fetch8(const T* row, int at, int d) {
-  Raw<T> r;
-  if (kTail && d < 8) {
-    T e[8];
+// a lane's part of a row of T as it lies in memory
+template <class T, int kNV>
+struct Raw {
+  uint4 q[kNV][sizeof(T) / 2];
+  T last;
+};
+
+// Loads go to addresses clamped into the row; what they bring past a lane's
+// columns is dropped by widen().
+template <class T, int kL, int kNV, bool kTail>
+__device__ __forceinline__ Raw<T, kNV> fetch(const Cols<kL, kNV, kTail>& c, const T* row) {
+  Raw<T, kNV> r;
+  if (!kTail || c.whole) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = row[min(j, d - 1)];
-    __builtin_memcpy(&r, e, sizeof(r));
-    return r;
+    for (int v = 0; v < kNV; ++v)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        r.q[v][i] = ld16(row + min((v * kL + c.l) * 8, c.whole - 8) + i * kVecOf<T>);
   }
-  const T* p = row + min(at, d - 8);
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = ld16(p + i * kVecOf<T>);
+  if constexpr (kTail) r.last = row[min(c.whole + c.l, c.d - 1)];
   return r;
 }
 
-template <class T>
-__device__ __forceinline__ void widen8(const Raw<T>& r, float (&o)[8]) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    float v[kVecOf<T>];
-    unpack<T>(r.q[i], v);
-#pragma unroll
-    for (int j = 0; j < kVecOf<T>; ++j) o[i * kVecOf<T> + j] = v[j];
-  }
-}
-
 // -> the lane's values, `fill` past the row
-template <class T, bool kTail>
-__device__ __forceinline__ void unpack8(const Raw<T>& r, int at, int d, bool live, float fill, float (&o)[8]) {
-  widen8(r, o);
-  const bool in = live && at < d;
-  if (kTail && in && at + 8 > d) {
-    if (d >= 8) shift(o, at + 8 - d, fill);
+template <class T, int kL, int kNV, bool kTail, int kE>
+__device__ __forceinline__ void widen(const Cols<kL, kNV, kTail>& c, const Raw<T, kNV>& r, bool live, float fill,
+                                      float (&o)[kE]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = at + j < d ? o[j] : fill;
-  }
+  for (int v = 0; v < kNV; ++v)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = in ? o[j] : fill;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      float f[kVecOf<T>];
+      unpack<T>(r.q[v][i], f);
+#pragma unroll
+      for (int j = 0; j < kVecOf<T>; ++j) o[v * 8 + i * kVecOf<T> + j] = f[j];
+    }
+  if constexpr (kTail) o[kNV * 8] = (float)r.last;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = live && c.in(e) ? o[e] : fill;
 }
 
 // the lane's values of a d-vector that may be NULL (then `none`), zeros past it
-template <bool kTail>
-__device__ __forceinline__ void vector8(const float* p, int at, int d, float none, float (&o)[8]) {
+template <int kL, int kNV, bool kTail, int kE>
+__device__ __forceinline__ void vector(const Cols<kL, kNV, kTail>& c, const float* p, float none, float (&o)[kE]) {
   if (p) {
-    unpack8<float, kTail>(fetch8<float, kTail>(p, at, d), at, d, true, 0.f, o);
+    widen(c, fetch<float>(c, p), true, 0.f, o);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = at + j < d ? none : 0.f;
+    for (int e = 0; e < kE; ++e) o[e] = c.in(e) ? none : 0.f;
   }
 }
 
-template <class T, bool kTail>
-__device__ __forceinline__ void store8(T* row, int at, int d, const float (&v)[8]) {
-  if (at >= d) return;
-  if (kTail && at + 8 > d) {
+template <bool kNt, class T, int kL, int kNV, bool kTail, int kE>
+__device__ __forceinline__ void store(const Cols<kL, kNV, kTail>& c, T* row, const float (&v)[kE]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (at + j < d) row[at + j] = (T)v[j];
-    return;
+  for (int n = 0; n < kNV; ++n) {
+    const int at = (n * kL + c.l) * 8;
+    if (at >= c.whole) continue;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      float o[kVecOf<T>];
+#pragma unroll
+      for (int j = 0; j < kVecOf<T>; ++j) o[j] = v[n * 8 + i * kVecOf<T> + j];
+      if constexpr (kNt) st16_nt(row + at + i * kVecOf<T>, pack<T>(o));
+      else st16(row + at + i * kVecOf<T>, pack<T>(o));
+    }
   }
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    float o[kVecOf<T>];
-#pragma unroll
-    for (int j = 0; j < kVecOf<T>; ++j) o[j] = v[i * kVecOf<T> + j];
-    st16(row + at + i * kVecOf<T>, pack<T>(o));
-  }
+  if constexpr (kTail)
+    if (c.whole + c.l < c.d) row[c.whole + c.l] = (T)v[kNV * 8];
 }
 
 struct BlockFwd {
@@ -112,68 +118,57 @@ struct BlockFwd {
 
 // mean and 1 / sqrt(mean square + eps) of a row held by its lanes, zeros past it;
 // v becomes v - mean
-template <int kL, int kNV, bool kTail>
-__device__ __forceinline__ void row_stats(float (&v)[kNV][8], int l, int d, bool layer, float eps, float (*buf)[waves_of(kL)],
-                                          float& mean, float& rstd) {
+template <int kL, int kNV, bool kTail, int kE>
+__device__ __forceinline__ void row_stats(const Cols<kL, kNV, kTail>& c, float (&v)[kE], bool layer, float eps,
+                                          float (*buf)[waves_of(kL)], float& mean, float& rstd) {
   mean = 0.f;
   if (layer) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
+    for (int e = 0; e < kE; ++e) s += v[e];
+    mean = group_sum<kL>(s, buf[0]) / (float)c.d;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[i][j];
-    mean = group_sum<kL>(s, buf[0]) / (float)d;
-#pragma unroll
-    for (int i = 0; i < kNV; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((i * kL + l) * 8 + (kTail ? j : 0) < d) v[i][j] -= mean;
+    for (int e = 0; e < kE; ++e)
+      if (c.in(e)) v[e] -= mean;
   }
   float q = 0.f;
 #pragma unroll
-  for (int i = 0; i < kNV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q = __builtin_fmaf(v[i][j], v[i][j], q);
-  rstd = 1.0f / sqrtf(group_sum<kL>(q, buf[1]) / (float)d + eps);
+  for (int e = 0; e < kE; ++e) q = __builtin_fmaf(v[e], v[e], q);
+  rstd = 1.0f / sqrtf(group_sum<kL>(q, buf[1]) / (float)c.d + eps);
 }
 
+// Bound by memory: 16384 x 4096 bf16 with post, gate and weights 110 us, 537 MB
+// at 4.9 TB/s (a copy of 4 GB: 4.9); an fp32 stream beside bf16 145 us (5.5),
+// fp32 200 (5.4).  256 lanes of 16 columns: 128 of 32 took 135 us, 512 of 8 113.
 template <class TY, class TH, int kL, int kNV, bool kTail>
 __global__ __launch_bounds__(group_threads(kL)) void k_block_fwd(BlockFwd a) {
   constexpr int kGroups = group_threads(kL) / kL;
+  using C = Cols<kL, kNV, kTail>;
+  constexpr int kE = C::kE;
   __shared__ float buf[kGroups][4][waves_of(kL)];
-  const int grp = threadIdx.x / kL, l = threadIdx.x % kL, d = (int)a.p.d;
+  const int grp = threadIdx.x / kL, l = threadIdx.x % kL;
+  const C c((int)a.p.d, l);
   const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kGroups + grp, rows = a.p.rows;
   const bool live = row < rows;  // a dead group still meets the barriers
-  const int64_t at_row = (live ? row : rows - 1) * d;
+  const int64_t at = (live ? row : rows - 1) * a.p.d;
   const bool layer = a.p.kind == GIFT_NORM_LAYER;
-  Raw<TY> ry[kNV];
-  Raw<TH> rh[kNV];
-#pragma unroll
-  for (int i = 0; i < kNV; ++i) {
-    ry[i] = fetch8<TY, kTail>(static_cast<const TY*>(a.Y) + at_row, (i * kL + l) * 8, d);
-    rh[i] = fetch8<TH, kTail>(static_cast<const TH*>(a.H) + at_row, (i * kL + l) * 8, d);
-  }
-  float y[kNV][8], h[kNV][8];
-#pragma unroll
-  for (int i = 0; i < kNV; ++i) unpack8<TY, kTail>(ry[i], (i * kL + l) * 8, d, true, 0.f, y[i]);
+  const Raw<TY, kNV> ry = fetch(c, static_cast<const TY*>(a.Y) + at);
+  const Raw<TH, kNV> rh = fetch(c, static_cast<const TH*>(a.H) + at);
+  float y[kE], h[kE], w[kE], b[kE];
+  widen(c, ry, true, 0.f, y);
   float pm = 0.f, pr = 1.f, m, r;
-  if (a.p.post) row_stats<kL, kNV, kTail>(y, l, d, layer, a.p.eps, buf[grp], pm, pr);
-  const float* gate = a.p.gate ? a.p.gate + (live ? row : rows - 1) / a.p.gate_rows * d : nullptr;
+  if (a.p.post) {
+    row_stats(c, y, layer, a.p.eps, buf[grp], pm, pr);
+    vector(c, a.p.post_weight, 1.f, w);
+    vector(c, a.p.post_bias, 0.f, b);
 #pragma unroll
-  for (int i = 0; i < kNV; ++i) {
-    const int at = (i * kL + l) * 8;
-    unpack8<TH, kTail>(rh[i], at, d, true, 0.f, h[i]);
-    float w[8], b[8], g[8];
-    vector8<kTail>(a.p.post_weight, at, d, 1.f, w);
-    vector8<kTail>(a.p.post_bias, at, d, 0.f, b);
-    vector8<kTail>(gate, at, d, 1.f, g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float n = a.p.post ? __builtin_fmaf(y[i][j] * pr, w[j], b[j]) : y[i][j];
-      y[i][j] = h[i][j] = __builtin_fmaf(g[j], n, a.p.scale * h[i][j]);
-    }
+    for (int e = 0; e < kE; ++e) y[e] = __builtin_fmaf(y[e] * pr, w[e], b[e]);
   }
-  row_stats<kL, kNV, kTail>(y, l, d, layer, a.p.eps, buf[grp] + 2, m, r);
+  widen(c, rh, true, 0.f, h);
+  vector(c, a.p.gate ? a.p.gate + (live ? row : rows - 1) / a.p.gate_rows * a.p.d : nullptr, 1.f, w);
+#pragma unroll
+  for (int e = 0; e < kE; ++e) y[e] = h[e] = __builtin_fmaf(w[e], y[e], a.p.scale * h[e]);
+  row_stats(c, y, layer, a.p.eps, buf[grp] + 2, m, r);
   if (!live) return;
   if (l == 0) {
     a.stats[row] = pm;
@@ -181,21 +176,12 @@ __global__ __launch_bounds__(group_threads(kL)) void k_block_fwd(BlockFwd a) {
     a.stats[2 * rows + row] = m;
     a.stats[3 * rows + row] = r;
   }
-  // stored behind the sums' barriers: a row's last vector may have been read
-  // from columns that another lane writes
-  TH* h2 = static_cast<TH*>(a.H2) + at_row;
-  TY* x = static_cast<TY*>(a.X) + at_row;
+  store<!kTail>(c, static_cast<TH*>(a.H2) + at, h);
+  vector(c, a.p.weight, 1.f, w);
+  vector(c, a.p.bias, 0.f, b);
 #pragma unroll
-  for (int i = 0; i < kNV; ++i) {
-    const int at = (i * kL + l) * 8;
-    store8<TH, kTail>(h2, at, d, h[i]);
-    float w[8], b[8];
-    vector8<kTail>(a.p.weight, at, d, 1.f, w);
-    vector8<kTail>(a.p.bias, at, d, 0.f, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[i][j] = __builtin_fmaf(y[i][j] * r, w[j], b[j]);
-    store8<TY, kTail>(x, at, d, y[i]);
-  }
+  for (int e = 0; e < kE; ++e) y[e] = __builtin_fmaf(y[e] * r, w[e], b[e]);
+  store<!kTail>(c, static_cast<TY*>(a.X) + at, y);
 }
 
 struct BlockBwd {
@@ -221,64 +207,96 @@ struct BlockBwd {
 // the bias leave once a run, A and B once a gate: the rows of run r that gate g
 // serves leave them in row r + g, which moves by one where a run or a gate ends;
 // where both end at once a row between them holds zeros.
+//
+// The next row is fetched ahead, except where 1024 lanes leave too few registers
+// for that.  Bound by memory: 16384 x 4096 bf16 with gate and weights 168 us, 806
+// MB at 4.8 TB/s, of it 8 for the sums; with the vectors read from memory in each
+// row 200, with 512 lanes of 8 columns 262.  Few rows are bound by the chain of a
+// run: 1000 x 1536 fp32 16.6 us, in runs of 2 and of 8 rows 20.
 template <class TY, class TH, int kL, int kNV, bool kTail, bool kBias>
 __global__ __launch_bounds__(group_threads(kL)) void k_block_bwd(BlockBwd a) {
-  constexpr int kGroups = group_threads(kL) / kL, kW = waves_of(kL);
-  constexpr int kCols = kL * kNV * 8;
+  constexpr int kGroups = group_threads(kL) / kL, kW = waves_of(kL), kThreads = group_threads(kL);
+  constexpr bool kAhead = kL < 1024;
+  using C = Cols<kL, kNV, kTail>;
+  constexpr int kE = C::kE, kCols = kL * kNV * 8 + (kTail ? 8 : 0);
   __shared__ float buf[2][2][2][kGroups][kW];
   __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? kCols : 1];
+  // the lane's own columns of weight and of gate post_weight: from memory they
+  // would come behind the next row's loads, which complete in order.  Where no
+  // row is fetched ahead they do come from memory, and the lane's sums gw and ga
+  // are kept here instead, for which its registers do not suffice.
+  __shared__ f32x4 mine[2][kNV * 2][kThreads];
+  __shared__ float mine_last[2][kTail ? kThreads : 1];
+  auto keep = [&](int which, const float (&v)[kE]) {
+#pragma unroll
+    for (int i = 0; i < 2 * kNV; ++i)
+      mine[which][i][threadIdx.x] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    if constexpr (kTail) mine_last[which][threadIdx.x] = v[kNV * 8];
+  };
+  auto kept = [&](int which, float (&v)[kE]) {
+#pragma unroll
+    for (int i = 0; i < 2 * kNV; ++i) {
+      const f32x4 q = mine[which][i][threadIdx.x];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = q[j];
+    }
+    if constexpr (kTail) v[kNV * 8] = mine_last[which][threadIdx.x];
+  };
   const int grp = threadIdx.x / kL, l = threadIdx.x % kL, d = (int)a.p.d;
+  const C c(d, l);
   const int64_t rows = a.p.rows, begin = (int64_t)blockIdx.x * a.run, end = min(rows, begin + a.run);
   const bool layer = a.p.kind == GIFT_NORM_LAYER, post = a.p.post;
   const float inv_d = 1.0f / (float)d;
-  float gw[kNV][8], gb[kNV][8], ga[kNV][8], gt[kNV][8];
-  auto clear = [&](float (&v)[kNV][8]) {
+  float gw[kAhead ? kE : 1], gb[kE], ga[kAhead ? kE : 1], gt[kE];
+  auto clear = [&](auto& v) {
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
+    for (float& x : v) x = 0.f;
+  };
+  // sum `which` (0: gw, 1: ga, in registers or kept) += x y; what it holds
+  auto grow = [&](int which, float (&in)[kAhead ? kE : 1], const float (&x)[kE], const float (&y)[kE]) {
+    if constexpr (kAhead) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      for (int e = 0; e < kE; ++e) in[e] = __builtin_fmaf(x[e], y[e], in[e]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kNV; ++i) {
+        f32x4 q = mine[which][i][threadIdx.x];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __builtin_fmaf(x[4 * i + j], y[4 * i + j], q[j]);
+        mine[which][i][threadIdx.x] = q;
+      }
+      if constexpr (kTail) {
+        float& q = mine_last[which][threadIdx.x];
+        q = __builtin_fmaf(x[kNV * 8], y[kNV * 8], q);
+      }
+    }
+  };
+  auto zero = [&](int which, float (&in)[kAhead ? kE : 1]) {
+    clear(in);
+    if constexpr (!kAhead) {
+      float z[kE];
+      clear(z);
+      keep(which, z);
+    }
   };
   // the groups' sums, added in group order, to a row of `out`
-  auto leave = [&](float* out, int64_t at_row, const float (&v)[kNV][8]) {
+  auto leave = [&](float* out, int64_t at_row, const float (&v)[kE]) {
     float* o = out + at_row * d;
     if constexpr (kGroups > 1) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kNV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sums[grp][(i * kL + l) * 8 + j] = v[i][j];
+      for (int e = 0; e < kE; ++e)
+        if (c.in(e)) sums[grp][c.col(e)] = v[e];
       __syncthreads();
-      for (int c = threadIdx.x; c < d; c += group_threads(kL)) {
-        float s = sums[0][c];
+      for (int x = threadIdx.x; x < d; x += kThreads) {
+        float s = sums[0][x];
 #pragma unroll
-        for (int k = 1; k < kGroups; ++k) s += sums[k][c];
-        o[c] = s;
+        for (int k = 1; k < kGroups; ++k) s += sums[k][x];
+        o[x] = s;
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < kNV; ++i) store8<float, kTail>(o, (i * kL + l) * 8, d, v[i]);
+      store<false>(c, o, v);
     }
-  };
-  clear(gw);
-  clear(gb);
-  // rows are fetched one ahead, from addresses clamped into the run
-  Raw<TY> nx[kNV], ny[kNV];
-  Raw<TH> ng[kNV], nh[kNV];
-  float npm, npr, nm, nr;
-  auto fetch = [&](int64_t row) {
-    row = min(row, end - 1);
-#pragma unroll
-    for (int i = 0; i < kNV; ++i) {
-      const int at = (i * kL + l) * 8;
-      nx[i] = fetch8<TY, kTail>(static_cast<const TY*>(a.dX) + row * d, at, d);
-      nh[i] = fetch8<TH, kTail>(static_cast<const TH*>(a.H2) + row * d, at, d);
-      ny[i] = fetch8<TY, kTail>(static_cast<const TY*>(a.Y) + row * d, at, d);
-      if (a.dH2) ng[i] = fetch8<TH, kTail>(static_cast<const TH*>(a.dH2) + row * d, at, d);
-    }
-    npm = a.stats[row];
-    npr = a.stats[rows + row];
-    nm = a.stats[2 * rows + row];
-    nr = a.stats[3 * rows + row];
   };
   // sums over a row's lanes of two values
   auto both = [&](float& s1, float& s2, float (&b)[2][kGroups][kW]) {
@@ -302,98 +320,133 @@ __global__ __launch_bounds__(group_threads(kL)) void k_block_bwd(BlockBwd a) {
     s1 *= inv_d;
     s2 *= inv_d;
   };
-  fetch(begin + grp);
+  auto leave_sum = [&](float* out, int64_t at_row, int which, const float (&in)[kAhead ? kE : 1]) {
+    if constexpr (kAhead) {
+      leave(out, at_row, in);
+    } else {
+      float v[kE];
+      kept(which, v);
+      leave(out, at_row, v);
+    }
+  };
+  if constexpr (kAhead) {
+    float w[kE];
+    vector(c, a.p.weight, 1.f, w);
+    keep(0, w);
+  }
+  zero(0, gw);
+  clear(gb);
+  // rows come from addresses clamped into the run
+  Raw<TY, kNV> nx, ny;
+  Raw<TH, kNV> ng, nh;
+  float npm, npr, nm, nr;
+  auto load = [&](int64_t row) {
+    row = min(row, end - 1);
+    nx = fetch(c, static_cast<const TY*>(a.dX) + row * d);
+    nh = fetch(c, static_cast<const TH*>(a.H2) + row * d);
+    if (a.dH2) ng = fetch(c, static_cast<const TH*>(a.dH2) + row * d);
+    ny = fetch(c, static_cast<const TY*>(a.Y) + row * d);
+    npm = a.stats[row];
+    npr = a.stats[rows + row];
+    nm = a.stats[2 * rows + row];
+    nr = a.stats[3 * rows + row];
+  };
+  if constexpr (kAhead) load(begin + grp);
   int phase = 0;
   for (int64_t from = begin; from < end;) {
     const int64_t g = from / a.p.gate_rows, to = min(end, (g + 1) * a.p.gate_rows);
-    const float* gate = a.p.gate ? a.p.gate + g * d : nullptr;
-    clear(ga);
+    zero(1, ga);
     clear(gt);
+    auto gated = [&](float (&k)[kE]) {
+      float w[kE];
+      vector(c, a.p.gate ? a.p.gate + g * d : nullptr, 1.f, k);
+      vector(c, post ? a.p.post_weight : nullptr, 1.f, w);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) k[e] *= w[e];
+    };
+    if constexpr (kAhead) {
+      float k[kE];
+      gated(k);
+      keep(1, k);
+    }
     for (int64_t base = from; base < to; base += kGroups, phase ^= 1) {
       const int64_t row = base + grp;
       const bool live = row < to;
+      if constexpr (!kAhead) load(row);
       // a dead row adds nothing, whatever the row that was fetched for it holds
       const float m = live ? nm : 0.f, r = live ? nr : 0.f;
       const float pm = live && post ? npm : 0.f, pr = live && post ? npr : 0.f;
-      float dx[kNV][8], u[kNV][8], t[kNV][8], v[kNV][8];
-#pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int at = (i * kL + l) * 8;
-        unpack8<TY, kTail>(nx[i], at, d, live, 0.f, dx[i]);
-        unpack8<TH, kTail>(nh[i], at, d, live, m, u[i]);
-        unpack8<TY, kTail>(ny[i], at, d, live, pm, v[i]);
-        if (a.dH2) {
-          unpack8<TH, kTail>(ng[i], at, d, live, 0.f, t[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) t[i][j] = 0.f;
-        }
+      float dx[kE], u[kE], t[kE], v[kE], w[kE];
+      widen(c, nx, live, 0.f, dx);
+      widen(c, nh, live, m, u);
+      if constexpr (kAhead) {
+        widen(c, ny, live, pm, v);
+        if (a.dH2) widen(c, ng, live, 0.f, t);
+        else clear(t);
+        // the next row of the group: in this gate's rows, or the first of the next
+        if (base + kGroups < to || to < end) load(base + kGroups < to ? row + kGroups : to + grp);
       }
-      // the next row of the group: in this gate's rows, or the first of the next
-      const int64_t next = base + kGroups < to ? row + kGroups : to + grp;
-      if (base + kGroups < to || to < end) fetch(next);
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        float w[8];
-        vector8<kTail>(a.p.weight, (i * kL + l) * 8, d, 1.f, w);
+      for (int e = 0; e < kE; ++e) u[e] = (u[e] - m) * r;
+      grow(0, gw, dx, u);
+      if constexpr (kAhead) kept(0, w);
+      else vector(c, a.p.weight, 1.f, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[i][j] = (u[i][j] - m) * r;
-          gw[i][j] = __builtin_fmaf(dx[i][j], u[i][j], gw[i][j]);
-          if constexpr (kBias) gb[i][j] += dx[i][j];
-          dx[i][j] *= w[j];
-          s2 = __builtin_fmaf(dx[i][j], u[i][j], s2);
-          s1 += dx[i][j];
-        }
+      for (int e = 0; e < kE; ++e) {
+        if constexpr (kBias) gb[e] += dx[e];
+        dx[e] *= w[e];
+        s2 = __builtin_fmaf(dx[e], u[e], s2);
+        s1 += dx[e];
       }
       both(s1, s2, buf[0][phase]);
+      if constexpr (!kAhead) {
+        if (a.dH2) widen(c, ng, live, 0.f, t);
+        else clear(t);
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        if (live && c.in(e)) t[e] = __builtin_fmaf(r, __builtin_fmaf(-u[e], s2, dx[e]) - s1, t[e]);
+        dx[e] = a.p.scale * t[e];
+      }
+      if (live && a.dH) store<!kTail>(c, static_cast<TH*>(a.dH) + row * d, dx);
+      if constexpr (!kAhead) widen(c, ny, live, pm, v);
       float s3 = 0.f, s4 = 0.f;
-      TH* dh = static_cast<TH*>(a.dH) + row * d;
+      if (post)
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        const int at = (i * kL + l) * 8;
-        float w[8], k[8];
-        vector8<kTail>(gate, at, d, 1.f, k);
-        vector8<kTail>(a.p.post_weight, at, d, 1.f, w);
+        for (int e = 0; e < kE; ++e) v[e] = (v[e] - pm) * pr;
+      grow(1, ga, t, v);
+      if constexpr (kAhead) kept(1, w);
+      else gated(w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (live && at + (kTail ? j : 0) < d) t[i][j] = __builtin_fmaf(r, __builtin_fmaf(-u[i][j], s2, dx[i][j]) - s1, t[i][j]);
-          if (post) v[i][j] = (v[i][j] - pm) * pr;
-          ga[i][j] = __builtin_fmaf(t[i][j], v[i][j], ga[i][j]);
-          if constexpr (kBias) gt[i][j] += t[i][j];
-          u[i][j] = a.p.scale * t[i][j];
-          t[i][j] *= k[j] * (post ? w[j] : 1.f);
-          s4 = __builtin_fmaf(t[i][j], v[i][j], s4);
-          s3 += t[i][j];
-        }
-        if (live && a.dH) store8<TH, kTail>(dh, at, d, u[i]);
+      for (int e = 0; e < kE; ++e) {
+        if constexpr (kBias) gt[e] += t[e];
+        t[e] *= w[e];
+        s4 = __builtin_fmaf(t[e], v[e], s4);
+        s3 += t[e];
       }
       if (!a.dY) continue;
-      TY* dy = static_cast<TY*>(a.dY) + row * d;
-      if (post) both(s3, s4, buf[1][phase]);
+      if (post) {
+        both(s3, s4, buf[1][phase]);
 #pragma unroll
-      for (int i = 0; i < kNV; ++i) {
-        if (post)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) t[i][j] = pr * (__builtin_fmaf(-v[i][j], s4, t[i][j]) - s3);
-        if (live) store8<TY, kTail>(dy, (i * kL + l) * 8, d, t[i]);
+        for (int e = 0; e < kE; ++e) t[e] = pr * (__builtin_fmaf(-v[e], s4, t[e]) - s3);
       }
+      if (live) store<!kTail>(c, static_cast<TY*>(a.dY) + row * d, t);
     }
     const int64_t seg = blockIdx.x + g;
-    if (a.sa) leave(a.sa, seg, ga);
+    if (a.sa) leave_sum(a.sa, seg, 1, ga);
     if (kBias && a.st) leave(a.st, seg, gt);
     if (a.gate_of && threadIdx.x == 0) a.gate_of[seg] = (int)g;
     if (from == begin && begin && begin == g * a.p.gate_rows) {
       // the row between two ends
-      clear(ga);
-      if (a.sa) leave(a.sa, seg - 1, ga);
-      if (kBias && a.st) leave(a.st, seg - 1, ga);
+      clear(gt);
+      if (a.sa) leave(a.sa, seg - 1, gt);
+      if (kBias && a.st) leave(a.st, seg - 1, gt);
       if (a.gate_of && threadIdx.x == 0) a.gate_of[seg - 1] = (int)g;
     }
     from = to;
   }
-  if (a.sw) leave(a.sw, blockIdx.x, gw);
+  if (a.sw) leave_sum(a.sw, blockIdx.x, 0, gw);
   if (kBias && a.sb) leave(a.sb, blockIdx.x, gb);
 }
 
