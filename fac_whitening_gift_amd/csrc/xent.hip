@@ -70,7 +70,7 @@ struct XeGemm {
   uint8_t* P;        // packed D: rows tokens, k vocabulary; NULL: not wanted
   int64_t p_steps;
   uint8_t* Pt;       // packed ratio D^T: rows vocabulary, k tokens; NULL: not wanted
-  int64_t t_steps;   // k steps over the tokens
+  int64_t t_steps;   // k steps over the tokens; a tile's tokens past them are not stored
   int parts;         // of ratio D^T: 1, or 2 (what the first rounding left behind it)
   // the rest
   void* C;
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
             lo[h][j][e] = bf16_pair(a - __uint_as_float(p << 16), b - __uint_as_float(p & 0xffff0000u));
           }
       }
-      if (!g.Pt) continue;
+      if (!g.Pt || m0 / kXeStep + i2 >= g.t_steps) continue;
       for (int part = 0; part < g.parts; ++part) {
         asm volatile("" ::: "memory");
 #pragma unroll
@@ -659,54 +659,58 @@ __global__ __launch_bounds__(256) void k_xe_reduce(XeGemm g, const float* slots)
 
 // ---------------------------------------------------------------------------
 // Few rows (a token scored, a small batch): a wave owns 16 vocabulary columns
-// and all of d, straight from memory into the matrix operands.
+// and all of d, W straight from memory into the matrix operands.  X comes packed,
+// but for one row: a fragment of 16 rows that lie apart costs four times the
+// cache lookups (32 rows of 4096 over 32000 123 us with X as rows).
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 64, kFewWaves = 8;
 
 template <int FM>
-__global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, XeMatrix W, const int64_t* targets, float2* part,
-                                                           float* picked) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, const uint8_t* packed, XeMatrix W,
+                                                           const int64_t* targets, float2* part, float* picked) {
   constexpr int kU = FM == 4 ? 4 : 8;  // k steps in flight
   __shared__ float2 sums[kFewWaves][16 * FM];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, rl = lane & 15, gq = lane >> 4;
   const int64_t v0 = ((int64_t)blockIdx.x * kFewWaves + w) * 16;
-  const int64_t d = X.cols;
+  const int d = (int)X.cols, whole = d / kXeStep;
   f32x4 acc[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (v0 < W.rows) {
     const uint16_t* wp = W.p + min(v0 + rl, W.rows - 1) * W.ld + 8 * gq;
-    const uint16_t* xp[FM];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) xp[i] = X.p + min((int64_t)16 * i + rl, X.rows - 1) * X.ld + 8 * gq;
-    const int whole = (int)(d / kXeStep);
-    int s = 0;
-    for (; s + kU <= whole; s += kU) {
+    const uint16_t* xp = X.p + 8 * gq;
+    const uint8_t* xq = packed + lane * 16;
+    auto x_at = [&](int s, int i) {
+      return packed ? *reinterpret_cast<const uint4*>(xq + (int64_t)s * kPanelStep + i * kFrag) : ld16(xp + s * kXeStep);
+    };
+    for (int s = 0; s < whole; s += kU) {
       uint4 b[kU], a[kU][FM];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        b[u] = ld16(wp + (s + u) * kXeStep);
+        const int at = min(s + u, whole - 1);
+        b[u] = ld16(wp + at * kXeStep);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) a[u][i] = ld16(xp[i] + (s + u) * kXeStep);
+        for (int i = 0; i < FM; ++i) a[u][i] = x_at(at, i);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u)
+        if (s + u < whole)
 #pragma unroll
-        for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b[u], a[u][i], acc[i]);
+          for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b[u], a[u][i], acc[i]);
     }
-    for (; s * kXeStep < d; ++s) {
-      auto load = [&](const uint16_t* p) {
-        const int64_t n = d - (int64_t)s * kXeStep - 8 * gq;  // elements left
-        if (n >= 8) return ld16(p + s * kXeStep);
+    if (whole * kXeStep < d) {
+      const int n = d - whole * kXeStep - 8 * gq;  // elements left
+      auto last = [&](const uint16_t* p) {
+        if (n >= 8) return ld16(p + whole * kXeStep);
         uint16_t e[8] = {};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (j < n) e[j] = p[s * kXeStep + j];
+          if (j < n) e[j] = p[whole * kXeStep + j];
         return __builtin_bit_cast(uint4, *reinterpret_cast<i16x8*>(e));
       };
-      const uint4 b = load(wp);
+      const uint4 b = last(wp);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b, load(xp[i]), acc[i]);
+      for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b, packed ? x_at(whole, i) : last(xp), acc[i]);
     }
   }
   const int64_t left = W.rows - v0 - 4 * gq;
@@ -785,10 +789,15 @@ XeOperand row_operand(const XeMatrix& a, int64_t first, int64_t rows, bool is_pa
 // taking a twelfth longer for the same work (16384 x 32000 x 4096 without an
 // epilogue 2.89 and 3.15 ms, 16384 x 4096 x 16128 1.45 and 1.57).
 bool big_tiles(int64_t M, int64_t N) {
+  if (M <= Half::kRows) return false;
   const int64_t tn = up_div(N, kTn);
   const int64_t big = up_div(up_div(M, Big::kRows) * tn, 256), half = up_div(up_div(M, Half::kRows) * tn, 512);
   return 12 * big <= 13 * half;
 }
+
+// As above for dX and dW: short sums are bound by their results, which the
+// second workgroup of a CU forms beside the first one's stores.
+bool big_tiles(int64_t M, int64_t N, int64_t steps) { return steps >= 24 && big_tiles(M, N); }
 
 // Tokens that D is written for: whole tiles of them.
 int64_t padded(int64_t rows, int64_t piece) {
@@ -817,7 +826,7 @@ void launch_gemm(const XeGemm& g, hipStream_t s) {
 // Ways to split a sum of `steps` k steps: enough workgroups to fill the chip,
 // at least 8 steps each.
 int splits(int64_t M, int64_t N, int64_t steps) {
-  const bool big = big_tiles(M, N);
+  const bool big = big_tiles(M, N, steps);
   const int64_t tiles = up_div(M, big ? Big::kRows : Half::kRows) * up_div(N, kTn);
   int64_t n = (big ? 256 : 512) / tiles;
   if (n > steps / 8) n = steps / 8;
@@ -853,6 +862,7 @@ XeFwdWs forward_plan(int64_t rows, int64_t d, int64_t vocab, Carve& c) {
   r.picked = c.take<float>(rows * 4);
   if (rows <= kFewRows) {
     r.part = c.take<float2>(up_div(vocab, 16 * kFewWaves) * rows * 8);
+    if (rows > 1) r.x = c.take<uint8_t>(operand_bytes(rows, up_div(d, kXeStep)));
     return r;
   }
   r.part = c.take<float2>(up_div(vocab, kTn) * chunk_rows(rows, vocab) * 8);
@@ -864,7 +874,7 @@ XeFwdWs forward_plan(int64_t rows, int64_t d, int64_t vocab, Carve& c) {
 struct XeBwdPlan {
   int64_t piece;     // vocabulary columns at a time
   int n_piece;
-  int64_t tall;      // tokens that D is written for
+  int64_t tokens;    // k steps over the tokens
   int parts;         // of the dW operand
   int dx_split, dw_split;
   float* scale;
@@ -880,14 +890,14 @@ XeBwdPlan backward_plan(int64_t rows, int64_t d, int64_t vocab, bool dx, bool dw
   r.n_piece = (int)up_div(wide, most);
   r.piece = up_div(up_div(wide, r.n_piece), kTn) * kTn;
   r.n_piece = (int)up_div(wide, r.piece);
-  r.tall = padded(rows, r.piece);
-  const int64_t tall = r.tall, tokens = tall / kXeStep;
+  r.tokens = up_div(rows, kXeStep);
+  const int64_t tokens = r.tokens;
   r.parts = dw_dtype == GIFT_DTYPE_F32 ? 2 : 1;
   r.scale = c.take<float>(4);
   r.x = c.take<uint8_t>(operand_bytes(rows, k));
   r.w = c.take<uint8_t>(operand_bytes(r.piece, k));
   if (dx) {
-    r.P = c.take<uint8_t>(operand_bytes(tall, r.piece / kXeStep));
+    r.P = c.take<uint8_t>(operand_bytes(padded(rows, r.piece), r.piece / kXeStep));
     r.Wt = c.take<uint8_t>(operand_bytes(d, r.piece / kXeStep));
     r.dx_split = splits(rows, d, r.piece / kXeStep);
     if (r.dx_split > 1 || r.n_piece > 1) r.dx_slots = c.take<float>((size_t)r.dx_split * rows * d * 4);
@@ -933,9 +943,10 @@ hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64
   if (rows <= kFewRows) {
     const int64_t groups = up_div(vocab, 16 * kFewWaves);
     const dim3 grid((uint32_t)groups), block(64 * kFewWaves);
-    if (rows <= 16) k_xe_few<1><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
-    else if (rows <= 32) k_xe_few<2><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
-    else k_xe_few<4><<<grid, block, 0, s>>>(X, W, targets, p.part, p.picked);
+    if (rows > 1) pack_rows(X, 0, rows, p.x, s);
+    if (rows <= 16) k_xe_few<1><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
+    else if (rows <= 32) k_xe_few<2><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
+    else k_xe_few<4><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
     hipError_t e = done();
     if (e != hipSuccess) return e;
     join(0, rows, groups);
@@ -977,7 +988,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
   Carve c{static_cast<uint8_t*>(ws), 0};
   const int64_t rows = X.rows, d = X.cols, vocab = W.rows;
   const XeBwdPlan p = backward_plan(rows, d, vocab, o.dX, o.dW, o.dw_dtype, c);
-  const int64_t tokens = p.tall / kXeStep, k = up_div(d, kXeStep);
+  const int64_t tokens = p.tokens, k = up_div(d, kXeStep);
   const bool big = big_tiles(rows, p.piece);
   const float* scale = o.dW && dloss ? p.scale : nullptr;
   const bool pw = packed(W, rows), px = packed(X, vocab);
@@ -1017,7 +1028,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     if (e != hipSuccess) return e;
     if (o.dX) {
       XeGemm h{};
-      sized(h, rows, d, steps, p.dx_split, big_tiles(rows, d));
+      sized(h, rows, d, steps, p.dx_split, big_tiles(rows, d, p.piece / kXeStep));
       h.A = as_packed(p.P, rows, steps);
       h.B = as_packed(p.Wt, d, steps);
       if (p.dx_slots && (p.dx_split > 1 || i + 1 < p.n_piece)) {
@@ -1042,7 +1053,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     }
     if (o.dW) {
       XeGemm h{};
-      sized(h, n, d, tokens * p.parts, p.dw_split, big_tiles(p.piece, d));
+      sized(h, n, d, tokens * p.parts, p.dw_split, big_tiles(p.piece, d, tokens * p.parts));
       h.wrap = (int)tokens;
       h.A = as_packed(p.Pt, n, tokens * p.parts);
       h.B = as_packed(p.Xt, d, tokens);
