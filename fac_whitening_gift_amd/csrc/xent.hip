@@ -57,7 +57,7 @@ struct XeGemm {
   int per_split;     // k steps of a split
   int n_split;
   int tm, tn;
-  bool big;          // 256 x 256 tiles
+  int tile;          // kBig ..
   // kXeLse, kXeGrad: rows are tokens, columns vocabulary
   const int64_t* targets;
   int64_t col0;      // vocabulary index of column 0
@@ -126,6 +126,9 @@ struct XeTile {
 };
 using Big = XeTile<2, 2, 8, 8, 4>;    // 256 x 256, one workgroup a CU
 using Half = XeTile<1, 4, 8, 4, 3>;   // 128 x 256, two
+using Flat = XeTile<1, 4, 4, 2, 6>;   // 64 x 128, two: for up to 64 rows, many copies ahead
+using Low = XeTile<1, 4, 8, 2, 4>;    // 128 x 128, two: for up to 128
+enum { kBig, kHalf, kFlat, kLow };
 
 template <int kOut, class Tile>
 __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_gemm(XeGemm g) {
@@ -249,9 +252,8 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
         if constexpr ((k + 1) * kVm / kSide > c) copy(std::integral_constant<int, c>{});
         else read(std::integral_constant<int, k - c>{}, fr[1 - p], o);
       });
-      constexpr int i = gr / (FB / 4), j0 = gr % (FB / 4) * 4;
       static_for<4>([&](auto J) {
-        constexpr int j = j0 + decltype(J)::value;
+        constexpr int n = gr * 4 + decltype(J)::value, i = n / FB, j = n % FB;
         acc[i][j] = xe_mfma(r.f[j], r.f[FB + i], acc[i][j]);
       });
       __builtin_amdgcn_sched_barrier(0);
@@ -391,8 +393,9 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
             return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(uintptr_t)at);
           };
           const i16x8 v = __builtin_shufflevector(tr(from + 32 * j), tr(from + 32 * j + 16 * kRow), 0, 1, 2, 3, 4, 5, 6, 7);
-          uint8_t* to = g.Pt + ((n0 / kXePanel + j / 4) * (g.t_steps * g.parts) + part * g.t_steps + m0 / kXeStep + i2) *
-                                   kPanelStep + j % 4 * kFrag + lane * 16;
+          const int64_t f = n0 / 16 + j;  // fragment along the vocabulary
+          uint8_t* to = g.Pt + (f / 4 * (g.t_steps * g.parts) + part * g.t_steps + m0 / kXeStep + i2) * kPanelStep +
+                        f % 4 * kFrag + lane * 16;
           *reinterpret_cast<uint4*>(to) = __builtin_bit_cast(uint4, v);
         }
         asm volatile("" ::: "memory");
@@ -658,37 +661,44 @@ __global__ __launch_bounds__(256) void k_xe_reduce(XeGemm g, const float* slots)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (a token scored, a small batch): a wave owns 16 vocabulary columns
-// and all of d, W straight from memory into the matrix operands.  X comes packed,
-// but for one row: a fragment of 16 rows that lie apart costs four times the
-// cache lookups (32 rows of 4096 over 32000 123 us with X as rows).
+// Few rows without tiles: a wave owns 32 vocabulary columns and all of d, W
+// straight from memory into the matrix operands, wherever its rows start.  X
+// comes packed, but for one row: a fragment of 16 rows that lie apart costs four
+// times the cache lookups.  Columns, and the order of every sum, are those of the
+// Flat tiles, so the result does not depend on how W lies.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 64, kFewWaves = 8;
+constexpr int kFewRows = 64, kFewWaves = 4, kFewCols = 32;
+static_assert(kFewWaves * kFewCols == Flat::kCols && kFewCols == Flat::FB * 16, "the sums of the Flat tiles");
 
 template <int FM>
 __global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, const uint8_t* packed, XeMatrix W,
                                                            const int64_t* targets, float2* part, float* picked) {
-  constexpr int kU = FM == 4 ? 4 : 8;  // k steps in flight
+  constexpr int kU = FM == 4 ? 4 : 8, FB = Flat::FB;  // k steps in flight, fragments of columns
   __shared__ float2 sums[kFewWaves][16 * FM];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, rl = lane & 15, gq = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * kFewWaves + w) * 16;
+  const int64_t v0 = ((int64_t)blockIdx.x * kFewWaves + w) * kFewCols;
   const int d = (int)X.cols, whole = d / kXeStep;
-  f32x4 acc[FM];
+  f32x4 acc[FM][FB];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (v0 < W.rows) {
-    const uint16_t* wp = W.p + min(v0 + rl, W.rows - 1) * W.ld + 8 * gq;
+    const uint16_t* wp[FB];
+#pragma unroll
+    for (int j = 0; j < FB; ++j) wp[j] = W.p + min(v0 + 16 * j + rl, W.rows - 1) * W.ld + 8 * gq;
     const uint16_t* xp = X.p + 8 * gq;
     const uint8_t* xq = packed + lane * 16;
     auto x_at = [&](int s, int i) {
       return packed ? *reinterpret_cast<const uint4*>(xq + (int64_t)s * kPanelStep + i * kFrag) : ld16(xp + s * kXeStep);
     };
     for (int s = 0; s < whole; s += kU) {
-      uint4 b[kU], a[kU][FM];
+      uint4 b[kU][FB], a[kU][FM];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int at = min(s + u, whole - 1);
-        b[u] = ld16(wp + at * kXeStep);
+#pragma unroll
+        for (int j = 0; j < FB; ++j) b[u][j] = ld16(wp[j] + at * kXeStep);
 #pragma unroll
         for (int i = 0; i < FM; ++i) a[u][i] = x_at(at, i);
       }
@@ -696,7 +706,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, const uin
       for (int u = 0; u < kU; ++u)
         if (s + u < whole)
 #pragma unroll
-          for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b[u], a[u][i], acc[i]);
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FB; ++j) acc[i][j] = xe_mfma(b[u][j], a[u][i], acc[i][j]);
     }
     if (whole * kXeStep < d) {
       const int n = d - whole * kXeStep - 8 * gq;  // elements left
@@ -708,9 +720,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, const uin
           if (j < n) e[j] = p[whole * kXeStep + j];
         return __builtin_bit_cast(uint4, *reinterpret_cast<i16x8*>(e));
       };
-      const uint4 b = last(wp);
+      uint4 b[FB];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) acc[i] = xe_mfma(b, packed ? x_at(whole, i) : last(xp), acc[i]);
+      for (int j = 0; j < FB; ++j) b[j] = last(wp[j]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const uint4 a = packed ? x_at(whole, i) : last(xp);
+#pragma unroll
+        for (int j = 0; j < FB; ++j) acc[i][j] = xe_mfma(b[j], a, acc[i][j]);
+      }
     }
   }
   const int64_t left = W.rows - v0 - 4 * gq;
@@ -720,17 +738,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_xe_few(XeMatrix X, const uin
     const int64_t t = m < X.rows ? targets[m] : -1;
     float top = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (e >= left) acc[i][e] = -__builtin_inff();
-      else if (t >= 0 && v0 + 4 * gq + e == t) picked[m] = acc[i][e];
-      top = fmaxf(top, acc[i][e]);
-    }
+    for (int j = 0; j < FB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (16 * j + e >= left) acc[i][j][e] = -__builtin_inff();
+        else if (t >= 0 && v0 + 4 * gq + 16 * j + e == t) picked[m] = acc[i][j][e];
+        top = fmaxf(top, acc[i][j][e]);
+      }
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const float from = top == -__builtin_inff() ? 0.f : top;
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((acc[i][e] - from) * kLog2e);
+    for (int j = 0; j < FB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - from) * kLog2e);
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
     if (gq == 0) sums[w][m] = make_float2(top, sum);
@@ -772,8 +794,15 @@ XeOperand as_packed(const uint8_t* p, int64_t rows, int64_t steps) {
 }
 
 // Whether a matrix is packed along its columns for so many rows of the other
-// operand: packing reads and writes it once, copies of rows take longer per use.
-bool packed(const XeMatrix& a, int64_t uses) { return !readable(a) || uses >= 2600; }
+// operand: packing reads and writes it once, copies of rows take longer per use
+// (16384 x 4096 over 32000 as rows 3.99 ms, packed 3.20 and 0.18).  A few rows stay
+// in the caches either way.
+bool packed(const XeMatrix& a, int64_t uses) { return !readable(a) || (uses >= 2600 && a.rows > Low::kRows); }
+// Whether the forward pass takes W straight from memory: few rows where W would
+// have to be packed first (64 x 394 over 42848 24 us, packed 39).  Where its rows
+// can be copied, the Flat tiles are as fast or faster (1 x 4096 over 32000 63 us,
+// 69; over 131072 178 and 222).
+bool few(int64_t rows, bool w_readable) { return !w_readable && rows <= kFewRows; }
 
 void pack_rows(const XeMatrix& a, int64_t first, int64_t rows, uint8_t* out, hipStream_t s) {
   const int64_t steps = up_div(a.cols, kXeStep);
@@ -799,28 +828,36 @@ bool big_tiles(int64_t M, int64_t N) {
 // second workgroup of a CU forms beside the first one's stores.
 bool big_tiles(int64_t M, int64_t N, int64_t steps) { return steps >= 24 && big_tiles(M, N); }
 
-// Tokens that D is written for: whole tiles of them.
-int64_t padded(int64_t rows, int64_t piece) {
-  const int64_t tile = big_tiles(rows, piece) ? Big::kRows : Half::kRows;
-  return up_div(rows, tile) * tile;
+// The tile of the products with W along d: with few rows, smaller ones, so that
+// all of the chip reads W (32 rows of 4096 over 32000: see k_xe_gemm).
+int w_tile(int64_t M, int64_t N, bool grad) {
+  if (M <= Flat::kRows) return kFlat;
+  if (M <= Low::kRows) return kLow;
+  return grad && big_tiles(M, N) ? kBig : kHalf;
 }
+int rows_of(int tile) { return tile == kBig ? Big::kRows : tile == kFlat ? Flat::kRows : Half::kRows; }
+int cols_of(int tile) { return tile == kFlat || tile == kLow ? Flat::kCols : Big::kCols; }
 
-void sized(XeGemm& g, int64_t M, int64_t N, int64_t steps, int split, bool big) {
+void sized(XeGemm& g, int64_t M, int64_t N, int64_t steps, int split, int tile) {
   g.M = M;
   g.N = N;
   g.steps = (int)steps;
   g.wrap = (int)steps;
   g.per_split = (int)up_div(steps, split);
   g.n_split = (int)up_div(steps, g.per_split);
-  g.big = big;
-  g.tm = (int)up_div(M, g.big ? Big::kRows : Half::kRows);
-  g.tn = (int)up_div(N, kTn);
+  g.tile = tile;
+  g.tm = (int)up_div(M, rows_of(tile));
+  g.tn = (int)up_div(N, cols_of(tile));
 }
 template <int kOut>
 void launch_gemm(const XeGemm& g, hipStream_t s) {
   const dim3 grid((uint32_t)(g.tm * g.tn * g.n_split)), block(256);
-  if (g.big) k_xe_gemm<kOut, Big><<<grid, block, 0, s>>>(g);
-  else k_xe_gemm<kOut, Half><<<grid, block, 0, s>>>(g);
+  if (g.tile == kBig) k_xe_gemm<kOut, Big><<<grid, block, 0, s>>>(g);
+  else if (g.tile == kHalf) k_xe_gemm<kOut, Half><<<grid, block, 0, s>>>(g);
+  else if constexpr (kOut == kXeLse || kOut == kXeGrad) {
+    if (g.tile == kFlat) k_xe_gemm<kOut, Flat><<<grid, block, 0, s>>>(g);
+    else k_xe_gemm<kOut, Low><<<grid, block, 0, s>>>(g);
+  }
 }
 
 // Ways to split a sum of `steps` k steps: enough workgroups to fill the chip,
@@ -858,14 +895,10 @@ struct XeFwdWs {
   uint8_t* w;
 };
 XeFwdWs forward_plan(int64_t rows, int64_t d, int64_t vocab, Carve& c) {
+  // enough for either form: the sizes do not say how W lies
   XeFwdWs r{};
   r.picked = c.take<float>(rows * 4);
-  if (rows <= kFewRows) {
-    r.part = c.take<float2>(up_div(vocab, 16 * kFewWaves) * rows * 8);
-    if (rows > 1) r.x = c.take<uint8_t>(operand_bytes(rows, up_div(d, kXeStep)));
-    return r;
-  }
-  r.part = c.take<float2>(up_div(vocab, kTn) * chunk_rows(rows, vocab) * 8);
+  r.part = c.take<float2>(up_div(vocab, rows <= Low::kRows ? Flat::kCols : Half::kCols) * chunk_rows(rows, vocab) * 8);
   r.x = c.take<uint8_t>(operand_bytes(rows, up_div(d, kXeStep)));
   r.w = c.take<uint8_t>(operand_bytes(vocab, up_div(d, kXeStep)));
   return r;
@@ -875,7 +908,11 @@ struct XeBwdPlan {
   int64_t piece;     // vocabulary columns at a time
   int n_piece;
   int64_t tokens;    // k steps over the tokens
+  int tile;          // of the products that form D
+  // k steps over n columns of the vocabulary: whole tiles
+  int64_t steps_of(int64_t n) const { return up_div(n, cols_of(tile)) * cols_of(tile) / kXeStep; }
   int parts;         // of the dW operand
+  int64_t dx_steps;  // of the first piece, the longest
   int dx_split, dw_split;
   float* scale;
   uint8_t *P, *Pt, *Wt, *Xt, *x, *w;
@@ -890,6 +927,7 @@ XeBwdPlan backward_plan(int64_t rows, int64_t d, int64_t vocab, bool dx, bool dw
   r.n_piece = (int)up_div(wide, most);
   r.piece = up_div(up_div(wide, r.n_piece), kTn) * kTn;
   r.n_piece = (int)up_div(wide, r.piece);
+  r.tile = w_tile(rows, r.piece, true);
   r.tokens = up_div(rows, kXeStep);
   const int64_t tokens = r.tokens;
   r.parts = dw_dtype == GIFT_DTYPE_F32 ? 2 : 1;
@@ -897,9 +935,10 @@ XeBwdPlan backward_plan(int64_t rows, int64_t d, int64_t vocab, bool dx, bool dw
   r.x = c.take<uint8_t>(operand_bytes(rows, k));
   r.w = c.take<uint8_t>(operand_bytes(r.piece, k));
   if (dx) {
-    r.P = c.take<uint8_t>(operand_bytes(padded(rows, r.piece), r.piece / kXeStep));
+    r.P = c.take<uint8_t>(operand_bytes(up_div(rows, rows_of(r.tile)) * rows_of(r.tile), r.piece / kXeStep));
     r.Wt = c.take<uint8_t>(operand_bytes(d, r.piece / kXeStep));
-    r.dx_split = splits(rows, d, r.piece / kXeStep);
+    r.dx_steps = r.steps_of(vocab < r.piece ? vocab : r.piece);
+    r.dx_split = splits(rows, d, r.dx_steps);
     if (r.dx_split > 1 || r.n_piece > 1) r.dx_slots = c.take<float>((size_t)r.dx_split * rows * d * 4);
   }
   if (dw) {
@@ -940,13 +979,14 @@ hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64
     else if (n <= 4096) run(k_xe_loss<4>, 4);
     else run(k_xe_loss<16>, 16);
   };
-  if (rows <= kFewRows) {
-    const int64_t groups = up_div(vocab, 16 * kFewWaves);
+  if (few(rows, readable(W))) {
+    const int64_t groups = up_div(vocab, kFewCols * kFewWaves);
     const dim3 grid((uint32_t)groups), block(64 * kFewWaves);
-    if (rows > 1) pack_rows(X, 0, rows, p.x, s);
-    if (rows <= 16) k_xe_few<1><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
-    else if (rows <= 32) k_xe_few<2><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
-    else k_xe_few<4><<<grid, block, 0, s>>>(X, p.x, W, targets, p.part, p.picked);
+    const uint8_t* x = rows > 1 ? p.x : nullptr;
+    if (x) pack_rows(X, 0, rows, p.x, s);
+    if (rows <= 16) k_xe_few<1><<<grid, block, 0, s>>>(X, x, W, targets, p.part, p.picked);
+    else if (rows <= 32) k_xe_few<2><<<grid, block, 0, s>>>(X, x, W, targets, p.part, p.picked);
+    else k_xe_few<4><<<grid, block, 0, s>>>(X, x, W, targets, p.part, p.picked);
     hipError_t e = done();
     if (e != hipSuccess) return e;
     join(0, rows, groups);
@@ -960,7 +1000,7 @@ hipError_t launch_xent_forward(const XeMatrix& X, const XeMatrix& W, const int64
   for (int64_t first = 0; first < rows; first += chunk) {
     const int64_t n = rows - first < chunk ? rows - first : chunk;
     XeGemm g{};
-    sized(g, n, vocab, up_div(X.cols, kXeStep), 1, false);
+    sized(g, n, vocab, up_div(X.cols, kXeStep), 1, w_tile(n, vocab, false));
     g.A = x;
     g.A.rows = n;
     g.A.p += x.pitch ? first * x.pitch : first / kXePanel * x.steps * kPanelStep;
@@ -989,7 +1029,6 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
   const int64_t rows = X.rows, d = X.cols, vocab = W.rows;
   const XeBwdPlan p = backward_plan(rows, d, vocab, o.dX, o.dW, o.dw_dtype, c);
   const int64_t tokens = p.tokens, k = up_div(d, kXeStep);
-  const bool big = big_tiles(rows, p.piece);
   const float* scale = o.dW && dloss ? p.scale : nullptr;
   const bool pw = packed(W, rows), px = packed(X, vocab);
   // an operand along the matrix's rows, and beside it the one along its columns
@@ -1005,9 +1044,9 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
   if (e != hipSuccess) return e;
   for (int i = 0; i < p.n_piece; ++i) {
     const int64_t first = i * p.piece, n = vocab - first < p.piece ? vocab - first : p.piece;
-    const int64_t steps = up_div(n, kTn) * kTn / kXeStep;  // k steps over the piece
+    const int64_t steps = p.steps_of(n);  // k steps over the piece
     XeGemm g{};
-    sized(g, rows, n, k, 1, big);
+    sized(g, rows, n, k, 1, p.tile);
     g.A = x;
     if (o.dX) transposed(XePack{W, first, first + n, nullptr, vocab, p.Wt, steps, pw ? p.w : nullptr, nullptr, nullptr});
     else if (pw) pack_rows(W, first, n, p.w, s);
@@ -1028,7 +1067,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     if (e != hipSuccess) return e;
     if (o.dX) {
       XeGemm h{};
-      sized(h, rows, d, steps, p.dx_split, big_tiles(rows, d, p.piece / kXeStep));
+      sized(h, rows, d, steps, p.dx_split, big_tiles(rows, d, p.dx_steps) ? kBig : kHalf);
       h.A = as_packed(p.P, rows, steps);
       h.B = as_packed(p.Wt, d, steps);
       if (p.dx_slots && (p.dx_split > 1 || i + 1 < p.n_piece)) {
@@ -1053,7 +1092,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
     }
     if (o.dW) {
       XeGemm h{};
-      sized(h, n, d, tokens * p.parts, p.dw_split, big_tiles(p.piece, d, tokens * p.parts));
+      sized(h, n, d, tokens * p.parts, p.dw_split, big_tiles(p.piece, d, tokens * p.parts) ? kBig : kHalf);
       h.wrap = (int)tokens;
       h.A = as_packed(p.Pt, n, tokens * p.parts);
       h.B = as_packed(p.Xt, d, tokens);
@@ -1084,7 +1123,7 @@ hipError_t launch_xent_backward(const XeMatrix& X, const XeMatrix& W, const int6
   }
   if (o.dX && p.dx_split > 1) {
     XeGemm h{};
-    sized(h, rows, d, p.piece / kXeStep, p.dx_split, false);
+    sized(h, rows, d, p.dx_steps, p.dx_split, kHalf);
     h.C = o.dX;
     h.ldc = o.ld_dx;
     h.by_row = true;
