@@ -1119,8 +1119,8 @@ def gift_block_norm_backward(dx, dh, y, h_out, stats, weight=None, bias=None, po
 
 
 class TensorGroup:
-    """Contiguous device tensors (fp32 or bf16, on one device) that are worked on
-    together, their descriptors made once: the gradients of a model, which stay
+    """Contiguous device tensors (fp32 or bf16, on one device, no element in two of
+    them) that are worked on together, their descriptors made once: the gradients of a model, which stay
     where they are from step to step."""
 
     __slots__ = ("tensors", "device", "_array")
@@ -1140,6 +1140,9 @@ class TensorGroup:
             if not t.is_contiguous():
                 raise ValueError("tensor %d must be contiguous" % i)
             self._array[i] = _Tensor(t.data_ptr(), t.numel(), code)
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self.tensors if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("two of the tensors share elements")
 
     def __len__(self):
         return len(self.tensors)

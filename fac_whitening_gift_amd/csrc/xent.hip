@@ -118,7 +118,21 @@ __device__ __forceinline__ f32x4 sums_at(const XeGemm& g, int64_t m, int64_t n) 
   return v;
 }
 
-// A workgroup's tile: WR x WC waves of FA x FB fragments.
+// A workgroup's tile: WR x WC waves of FA x FB fragments.  A step copies both
+// operands' fragments into one of kStages stages of LDS, spread among the MFMAs of
+// the step kStages before it, as are the reads of the next step's fragments.
+//
+// Large products are bound by power: Big runs 1.45 to 1.56 PFLOP/s (16384 x 4096 x
+// 16128 1.39 to 1.45 ms) with the matrix units busy 82% of the cycles at the 1.75
+// GHz that the clock falls to; these MFMAs alone, from registers, on the same
+// values reach 1.93 to 1.98, the library's product 1.37 to 1.63.  Its waves of 128 x
+// 128 read two thirds of the LDS bytes of Half's 128 x 64 (1.57 ms); three to five
+// stages, bands of 2 to 6 tile rows and other orders of the MFMAs are alike, 2 x 2
+// blocks of them take 7% more, 32 x 32 x 16 MFMAs reach 1.76.  Half hides what
+// follows a tile: the logits' maxima and sums 16384 x 32000 x 4096 in 3.1 ms, Big
+// 3.5.  D takes 3.6 ms in Big, 3.9 in Half: its results, 6 bytes a logit for an fp32
+// dW (3.1 GB), leave at the memory's rate behind each round of tiles.  Flat and Low
+// have all CUs read W for few rows (32 x 4096 over 32000 77 us, Half 111).
 template <int kWR, int kWC, int kFA, int kFB, int kS>
 struct XeTile {
   static constexpr int WR = kWR, WC = kWC, FA = kFA, FB = kFB, kStages = kS;
@@ -126,8 +140,8 @@ struct XeTile {
 };
 using Big = XeTile<2, 2, 8, 8, 4>;    // 256 x 256, one workgroup a CU
 using Half = XeTile<1, 4, 8, 4, 3>;   // 128 x 256, two
-using Flat = XeTile<1, 4, 4, 2, 6>;   // 64 x 128, two: for up to 64 rows, many copies ahead
-using Low = XeTile<1, 4, 8, 2, 4>;    // 128 x 128, two: for up to 128
+using Flat = XeTile<1, 4, 4, 2, 6>;   // 64 x 128, two: up to 64 rows (8 or 12 stages: 3 and 8% more)
+using Low = XeTile<1, 4, 8, 2, 4>;    // 128 x 128, two: up to 128 rows
 enum { kBig, kHalf, kFlat, kLow };
 
 template <int kOut, class Tile>
@@ -279,7 +293,7 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
   const int left = (int)min(g.vocab - g.col0 - n0 - 4 * gq, (int64_t)kTn);
   auto column = [&](int64_t target) {
     const int64_t c = target - g.col0 - n0 - 4 * gq;
-    return target < g.vocab && c >= 0 && c < FB * 16 && (c & 12) == 0 ? (int)c : -1;
+    return target >= 0 && target < g.vocab && c >= 0 && c < FB * 16 && (c & 12) == 0 ? (int)c : -1;
   };
   if constexpr (kOut == kXeLse) {
     float2* sums = reinterpret_cast<float2*>(lds);  // [wave column][row]
@@ -829,7 +843,7 @@ bool big_tiles(int64_t M, int64_t N) {
 bool big_tiles(int64_t M, int64_t N, int64_t steps) { return steps >= 24 && big_tiles(M, N); }
 
 // The tile of the products with W along d: with few rows, smaller ones, so that
-// all of the chip reads W (32 rows of 4096 over 32000: see k_xe_gemm).
+// all of the chip reads W.
 int w_tile(int64_t M, int64_t N, bool grad) {
   if (M <= Flat::kRows) return kFlat;
   if (M <= Low::kRows) return kLow;

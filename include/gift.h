@@ -527,8 +527,9 @@ size_t gift_norm_backward_workspace_bytes(int64_t rows, int64_t d);
  * the row's loss NaN or infinite.  dev_flags (optional): NONFINITE where the
  * loss of a row that counts is, TARGET where a target lies past the
  * vocabulary.
- * 1 <= rows, vocab <= 2^20, 1 <= d <= 2^16.  Up to 64 rows read W once,
- * straight from memory (the serving form).
+ * 1 <= rows, vocab <= 2^20, 1 <= d <= 2^16.  The result does not depend on
+ * the leading dimensions and alignment.  A few rows (scoring, a token) read
+ * W once where it lies.
  */
 gift_status gift_xent_forward(const void *X, int64_t rows, int64_t d, int64_t ldx,
                               const void *W, int64_t vocab, int64_t ldw,
@@ -625,14 +626,15 @@ size_t gift_block_norm_backward_workspace_bytes(int64_t rows, int64_t d, int64_t
  * order that depends on the tensors' sizes and types alone.  dev_flags
  * (optional): NONFINITE where the sum is NaN or infinite.  The tensors are a
  * HOST array, dense, element aligned; one may be empty (its data is not read).
- * At most 2^16 tensors, 2^45 bytes.
+ * At most 2^16 tensors, 2^45 bytes.  A tensor named twice counts twice.
  *
  * gift_grad_clip -- every element times c = min(1, max_norm / (norm + eps)),
  * one rounding to its type.  sumsq: the sum of squares to go by, device fp64
  * (gift_grad_norm's, summed over the ranks of a data-parallel job); NULL: the
  * tensors' own.  out: n tensors of the same sizes and types to write, which
- * must not overlap the tensors but may be they; NULL: in place, where nothing
- * is written if c is 1.  norm (optional): as above.  A sum that is NaN makes
+ * must not overlap each other or the tensors, but may be they; NULL: in place,
+ * where the tensors must not overlap each other and nothing is written if c
+ * is 1.  norm (optional): as above.  A sum that is NaN makes
  * every element NaN, an infinite one gives c = 0 (0, and NaN for what was
  * infinite).
  */

@@ -191,3 +191,12 @@ def test_refuses():
     for bad in (-1.0, float("nan"), float("inf")):
         with pytest.raises(fg.GiftError):
             fg.gift_grad_clip([x], bad)
+
+
+def test_refuses_shared_elements():
+    """Scaled in place, an element of two tensors would be scaled twice, or race."""
+    x = torch.zeros(100, device=DEV)
+    for bad in ([x, x], [x[:60], x[59:]], [x[50:], x[:51]]):
+        with pytest.raises(ValueError, match="share elements"):
+            fg.gift_grad_clip(bad, 1.0)
+    assert float(fg.gift_grad_norm([x[:50], x[50:], x[:0]])) == 0.0

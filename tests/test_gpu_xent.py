@@ -260,3 +260,172 @@ def test_refuses():
         fg.gift_xent_backward(x, w, t, lse, dx=torch.zeros(4, 64, device=DEV))
     with pytest.raises(fg.GiftError):
         fg.gift_xent_backward(x, w, t, lse, dx=False, dw=False)
+
+
+def _lse_on_device(X, W, T):
+    """lse and loss in fp64 on the device, W a piece at a time, and how far off
+    they may be: _check_forward's bound."""
+    x, n, top, es, picked = X.double(), [], 0.0, 0.0, torch.zeros(X.shape[0], dtype=torch.float64, device=DEV)
+    for i in range(0, W.shape[0], 65536):
+        w = W[i:i + 65536].double()
+        s = torch.mm(x, w.t())
+        n.append(torch.logsumexp(s, 1))
+        top = torch.clamp(s.abs().amax(1), min=top)
+        es = torch.clamp(torch.mm(x.abs(), w.abs().t()).amax(1) * (2 * X.shape[1] * 2.0 ** -23), min=es)
+        here = (T >= i) & (T < i + w.shape[0])
+        picked = torch.where(here, s.gather(1, torch.where(here, T - i, 0)[:, None])[:, 0], picked)
+    z = torch.logsumexp(torch.stack(n, 1), 1)
+    e = es + 4 * (50 + W.shape[0] / 1024) * U + 2 * U * (1 + np.log(W.shape[0])) * 4 + 4 * U * (z.abs() + top)
+    return z, z - picked, e, e + es
+
+
+def _reference_on_device(X, W, T, z, G, chunk):
+    """dX, dW and the sums of magnitudes that bound their errors, in fp64 on the
+    device, `chunk` tokens at a time."""
+    w = W.double()
+    dx, dxa = (torch.empty(X.shape, dtype=torch.float64, device=DEV) for _ in range(2))
+    dw, dwa = (torch.zeros(W.shape, dtype=torch.float64, device=DEV) for _ in range(2))
+    for i in range(0, X.shape[0], chunk):
+        x, t, g = X[i:i + chunk].double(), T[i:i + chunk], G[i:i + chunk].double()
+        s = torch.mm(x, w.t())
+        es = 2 * X.shape[1] * 2.0 ** -23 * torch.mm(x.abs(), w.abs().t())
+        a = s - z[i:i + chunk, None].double()
+        D = a.exp()
+        ed = D * (es + 3 * U * a.abs() + 4 * U) + U
+        live = (t >= 0) & (t < W.shape[0])
+        rows = live.nonzero()[:, 0]
+        D[rows, t[rows]] -= 1.0
+        g = torch.where(live, g, torch.zeros_like(g))[:, None]
+        dx[i:i + chunk] = g * torch.mm(D, w)
+        dxa[i:i + chunk] = g.abs() * torch.mm(ed + (HALF + 2 * W.shape[0] * 2.0 ** -23) * (D.abs() + ed), w.abs())
+        dw += torch.mm((g * D).t(), x)
+        dwa += torch.mm((g.abs() * (ed + (HALF * HALF + 4 * X.shape[0] * 2.0 ** -23 + 3 * U) * (D.abs() + ed))).t(), x.abs())
+    return dx, dxa, dw, dwa
+
+
+@pytest.mark.parametrize("rows,d,vocab", [(40000, 64, 14001), (30000, 100, 9500)])
+def test_pieces_of_the_vocabulary(rows, d, vocab):
+    """More logits than a piece holds: dX grows over the pieces, the last one
+    shorter."""
+    say("xent pieces %d x %d over %d" % (rows, d, vocab))
+    X, W, T, G = (v.to(DEV) for v in _draw(rows, d, vocab))
+    loss, lse = fg.gift_xent_forward(X, W, T)
+    for i in range(0, rows, 5000):
+        z, l, ez, el = _lse_on_device(X[i:i + 5000], W, T[i:i + 5000])
+        assert bool(((lse[i:i + 5000].double() - z).abs() <= ez).all())
+        live = T[i:i + 5000] >= 0
+        assert bool(((loss[i:i + 5000].double() - l).abs() <= el)[live].all())
+    dx, dw = fg.gift_xent_backward(X, W, T, lse, G)
+    rx, ex, rw, ew = _reference_on_device(X, W, T, lse, G, 5000)
+    ex = ex + (HALF + U) * (rx.abs() + ex)
+    ew = ew + 3 * U * (rw.abs() + ew)
+    assert bool(((dx.double() - rx).abs() <= ex).all()) and bool(((dw.double() - rw).abs() <= ew).all())
+    # the same bits again, and into what a workspace full of NaN gives
+    ws = torch.full((fg.gift_xent_backward_workspace_bytes(rows, d, vocab),), 255, dtype=torch.uint8, device=DEV)
+    again = fg.gift_xent_backward(X, W, T, lse, G, ws=ws)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+@pytest.mark.parametrize("rows,d,vocab", [(1, 97, 300), (20, 64, 500), (100, 96, 3000), (130, 64, 257), (600, 128, 700)])
+def test_contents_of_the_workspace_do_not_matter(rows, d, vocab):
+    say("xent workspace %d x %d over %d" % (rows, d, vocab))
+    X, W, T, G = (v.to(DEV) for v in _draw(rows, d, vocab))
+    want = fg.gift_xent_forward(X, W, T)
+    for dtype in (torch.float32, BF16):
+        ref = fg.gift_xent_backward(X, W, T, want[1], G, dtype=dtype)
+        for fill in (255, 0x7f, 0):
+            ws = torch.full((fg.gift_xent_forward_workspace_bytes(rows, d, vocab),), fill, dtype=torch.uint8, device=DEV)
+            got = fg.gift_xent_forward(X, W, T, ws=ws)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            ws = torch.full((fg.gift_xent_backward_workspace_bytes(rows, d, vocab, dtype=dtype),), fill, dtype=torch.uint8,
+                            device=DEV)
+            got = fg.gift_xent_backward(X, W, T, want[1], G, dtype=dtype, ws=ws)
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_chunks_of_the_rows():
+    """More rows than one launch of the forward pass takes: the first ones, those
+    where the launches meet, and the last."""
+    say("xent chunks of rows")
+    rows, d, vocab = 70000, 32, 131072
+    X = torch.randn(rows, d, device=DEV).to(BF16)
+    W = torch.randn(vocab, d, device=DEV).to(BF16)
+    T = torch.randint(0, vocab, (rows,), device=DEV)
+    loss, lse = fg.gift_xent_forward(X, W, T)
+    for a, b in ((0, 300), (65400, 65700), (rows - 200, rows)):
+        z, l, ez, el = _lse_on_device(X[a:b], W, T[a:b])
+        assert bool(((lse[a:b].double() - z).abs() <= ez).all()) and bool(((loss[a:b].double() - l).abs() <= el).all())
+
+
+def test_offsets_past_32_bits():
+    """X, then W of more than 2^31 elements: rows at both ends and in the middle."""
+    say("xent large offsets, rows")
+    rows, d, vocab = 600000, 4096, 70
+    X = torch.empty(rows, d, dtype=BF16, device=DEV).normal_()
+    W = (torch.randn(vocab, d, device=DEV) / 64).to(BF16)
+    T = torch.randint(0, vocab, (rows,), device=DEV)
+    loss, lse = fg.gift_xent_forward(X, W, T)
+    dx, dw = fg.gift_xent_backward(X, W, T, lse)
+    pick = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device=DEV)
+    x, w, t = X[pick].cpu(), W.cpu(), T[pick].cpu()
+    _check_forward(x, w, t, (loss[pick], lse[pick]))
+    _check_backward(x, w, t, lse[pick], None, dx[pick], None)
+    assert bool(torch.isfinite(dw).all())
+    del X, dx
+    say("xent large offsets, vocabulary")
+    rows, d, vocab = 70, 2080, 1 << 20
+    W = torch.empty(vocab, d, dtype=BF16, device=DEV).normal_().mul_(0.02)
+    X = torch.randn(rows, d, device=DEV).to(BF16)
+    T = torch.randint(0, vocab, (rows,), device=DEV)
+    T[0], T[1] = vocab - 1, 0
+    loss, lse = fg.gift_xent_forward(X, W, T)
+    z, l, ez, el = _lse_on_device(X, W, T)
+    assert bool(((lse.double() - z).abs() <= ez).all()) and bool(((loss.double() - l).abs() <= el).all())
+    dx, dw = fg.gift_xent_backward(X, W, T, lse)
+    rows_of_w = torch.tensor([0, 1, vocab // 2, vocab - 2, vocab - 1], device=DEV)
+    part = W[rows_of_w].contiguous()
+    a = torch.mm(X.double(), part.double().t()) - lse[:, None].double()
+    es = 2 * d * 2.0 ** -23 * torch.mm(X.double().abs(), part.double().abs().t())
+    hit = (T[:, None] == rows_of_w).double()
+    D, ed = a.exp() - hit, a.exp() * (es + 3 * U * a.abs() + 4 * U) + U
+    want = torch.mm(D.t(), X.double())
+    tol = torch.mm((ed + (HALF * HALF + 4 * rows * 2.0 ** -23 + 3 * U) * (D.abs() + ed)).t(), X.double().abs())
+    assert bool(((dw[rows_of_w].double() - want).abs() <= tol + 3 * U * (want.abs() + tol)).all())
+
+
+def test_two_streams_and_two_graphs():
+    """Two at once on two streams with workspaces of their own, and two captured
+    graphs that share one and run one after the other."""
+    say("xent two streams, two graphs")
+    sets = [[v.to(DEV) for v in _draw(300, 96, 2000, seed=i)] for i in range(2)]
+
+    def step(i, ws=None, stream=None):
+        x, w, t, g = sets[i]
+        loss, lse = fg.gift_xent_forward(x, w, t, ws=ws, stream=stream)
+        return (loss,) + fg.gift_xent_backward(x, w, t, lse, g, ws=ws, stream=stream)
+    want = [[v.clone() for v in step(i)] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i in range(2):
+            got[i].append(step(i, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i in range(2) for g in got[i] for a, b in zip(g, want[i]))
+    need = max(fg.gift_xent_forward_workspace_bytes(300, 96, 2000), fg.gift_xent_backward_workspace_bytes(300, 96, 2000))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(i, ws=ws))
+        graphs.append(graph)
+    for rep in range(3):
+        for o in outs:
+            for v in o:
+                v.fill_(float("nan"))
+        ws.fill_(255)
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for i in range(2) for a, b in zip(outs[i], want[i])), rep
