@@ -295,12 +295,17 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
     const int64_t c = target - g.col0 - n0 - 4 * gq;
     return target >= 0 && target < g.vocab && c >= 0 && c < FB * 16 && (c & 12) == 0 ? (int)c : -1;
   };
+  // The rows' words are loaded for all of a tile's rows at once: one row fragment
+  // at a time waits for its own.
   if constexpr (kOut == kXeLse) {
     float2* sums = reinterpret_cast<float2*>(lds);  // [wave column][row]
+    int64_t target[FA];
+#pragma unroll
+    for (int i = 0; i < FA; ++i) target[i] = g.targets[min(m0 + 16 * i + rl, g.M - 1)];
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
       const int64_t m = m0 + 16 * i + rl;
-      const int at = m < g.M ? column(g.targets[m]) : -1;
+      const int at = m < g.M ? column(target[i]) : -1;
       if (__any(at >= 0 || left < FB * 16)) {
 #pragma unroll
         for (int j = 0; j < FB; ++j)
@@ -344,45 +349,67 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
     char* stage = lds + w * 32 * kRow;
     const uint32_t stage0 = lds0 + (uint32_t)(w * 32 * kRow);
     const float scale = g.Pt && g.scale ? *g.scale : 1.f;
+    int at[FA];
+    float lse[FA], ratio[FA];
+    uint32_t live = 0;
+    {
+      int64_t target[FA];
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int64_t m = min(m0 + 16 * i + rl, g.M - 1);
+        target[i] = g.targets[m];
+        lse[i] = g.lse[m];
+        ratio[i] = g.dloss ? g.dloss[m] : scale;
+      }
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        at[i] = column(target[i]);
+        if (target[i] >= 0 && target[i] < g.vocab && m0 + 16 * i + rl < g.M) live |= 1u << i;
+        ratio[i] = live >> i & 1 ? ratio[i] / scale : 1.f;
+      }
+    }
+    // of this wave's P and D^T: steps and panels from here are constant but for
+    // one stride each
+    uint8_t* const p0 = g.P + (m0 / kXePanel * g.p_steps + n0 / kXeStep) * kPanelStep + lane * 16;
+    const int64_t p_panel = g.p_steps * kPanelStep, t_panel = g.t_steps * g.parts * kPanelStep;
+    uint8_t* const t0 = g.Pt + n0 / kXePanel * t_panel + m0 / kXeStep * kPanelStep + lane * 16;
+    const int t_first = (int)(n0 / 16) % 4;  // fragment of its panel
+    const int64_t t_part = g.t_steps * kPanelStep;
 #pragma unroll
     for (int i2 = 0; i2 < FA / 2; ++i2) {
       uint32_t hi[2][FB][2], lo[2][FB][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = 2 * i2 + h;
-        const int64_t m = m0 + 16 * i + rl;
-        const int64_t t = m < g.M ? g.targets[m] : -1;
-        const bool live = t >= 0 && t < g.vocab;
-        const int at = column(t);
-        const float lse = live ? g.lse[m] : 0.f, ratio = live && g.dloss ? g.dloss[m] / scale : 1.f;
+        float x[FB][4];
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - lse) * kLog2e);
+          for (int e = 0; e < 4; ++e) x[j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - lse[i]) * kLog2e);
         // targets, rows left out and columns past the vocabulary are rare
-        if (__any(at >= 0 || !live || left < FB * 16)) {
+        const bool in = live >> i & 1;
+        if (__any(at[i] >= 0 || !in || left < FB * 16)) {
 #pragma unroll
           for (int j = 0; j < FB; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (16 * j + e == at) acc[i][j][e] -= 1.f;
-              if (!live || 16 * j + e >= left) acc[i][j][e] = 0.f;
+              if (16 * j + e == at[i]) x[j][e] -= 1.f;
+              if (!in || 16 * j + e >= left) x[j][e] = 0.f;
             }
         }
         if (g.P) {
-          uint8_t* to = g.P + ((m0 + 16 * i) / kXePanel * g.p_steps + n0 / kXeStep) * kPanelStep +
-                        i % 4 * kFrag + lane * 16;
+          uint8_t* to = p0 + i / 4 * p_panel + i % 4 * kFrag;
 #pragma unroll
           for (int j = 0; j < FB; j += 2)
             *reinterpret_cast<uint4*>(to + j / 2 * kPanelStep) =
-                make_uint4(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]),
-                           bf16_pair(acc[i][j + 1][0], acc[i][j + 1][1]), bf16_pair(acc[i][j + 1][2], acc[i][j + 1][3]));
+                make_uint4(bf16_pair(x[j][0], x[j][1]), bf16_pair(x[j][2], x[j][3]), bf16_pair(x[j + 1][0], x[j + 1][1]),
+                           bf16_pair(x[j + 1][2], x[j + 1][3]));
         }
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float a = acc[i][j][2 * e] * ratio, b = acc[i][j][2 * e + 1] * ratio;
+            const float a = x[j][2 * e] * ratio[i], b = x[j][2 * e + 1] * ratio[i];
             const uint32_t p = bf16_pair(a, b);
             hi[h][j][e] = p;
             lo[h][j][e] = bf16_pair(a - __uint_as_float(p << 16), b - __uint_as_float(p & 0xffff0000u));
@@ -407,9 +434,7 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
             return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(uintptr_t)at);
           };
           const i16x8 v = __builtin_shufflevector(tr(from + 32 * j), tr(from + 32 * j + 16 * kRow), 0, 1, 2, 3, 4, 5, 6, 7);
-          const int64_t f = n0 / 16 + j;  // fragment along the vocabulary
-          uint8_t* to = g.Pt + (f / 4 * (g.t_steps * g.parts) + part * g.t_steps + m0 / kXeStep + i2) * kPanelStep +
-                        f % 4 * kFrag + lane * 16;
+          uint8_t* to = t0 + j / 4 * t_panel + part * t_part + i2 * kPanelStep + (t_first + j % 4) * kFrag;
           *reinterpret_cast<uint4*>(to) = __builtin_bit_cast(uint4, v);
         }
         asm volatile("" ::: "memory");
@@ -426,11 +451,17 @@ __global__ __launch_bounds__(256, Tile::FA * Tile::FB > 32 ? 1 : 2) void k_xe_ge
     const int sr = lane / kLanes, sc = lane % kLanes;
     T* C = static_cast<T*>(g.C) + (int64_t)split * g.M * g.N + (m0 + sr) * g.ldc + n0 + sc * kE;
     const float all = !g.by_row && g.scale ? *g.scale : 1.f;
+    float factor[FA];
+    uint32_t dead = 0;
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
-      float f = all;
-      bool out = false;
-      if (g.by_row) out = !row_factor(g.targets, g.dloss, g.vocab, min(m0 + 16 * i + rl, g.M - 1), f);
+      factor[i] = all;
+      if (g.by_row && !row_factor(g.targets, g.dloss, g.vocab, min(m0 + 16 * i + rl, g.M - 1), factor[i])) dead |= 1u << i;
+    }
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      const float f = factor[i];
+      const bool out = dead >> i & 1;
 #pragma unroll
       for (int j = 0; j < FB; ++j) {
         f32x4 v = acc[i][j];
