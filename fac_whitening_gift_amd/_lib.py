@@ -959,6 +959,8 @@ def gift_xent_forward(x, w, targets, loss=None, lse=None, flags=None, ws=None, s
 
 
 def gift_xent_backward_workspace_bytes(rows, d, vocab, dx=True, dw=True, dtype=torch.float32):
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be bf16 or fp32, got %s" % dtype)
     return int(load().gift_xent_backward_workspace_bytes(rows, d, vocab, 1 if dx else 0, 1 if dw else 0,
                                                          _DTYPES[dtype]))
 

@@ -44,7 +44,8 @@ def _check(tensors, max_norm, eps, norm, out, sumsq=None):
 
 LISTS = [[(1,)], [(3, 5), (7,), (1,)], [(0,), (4,), (0, 3), (5,)], [(8192,), (8193,), (8191,)], [(16384,), (16385,)],
          [(300, 257)] * 3 + [(1000,)] * 5, [(i + 1,) for i in range(64)], [(2 * i,) for i in range(65)],
-         [(17, 31)] * 200, [(3,)] * 1000, [(2000, 3001)]]
+         [(17, 31)] * 200, [(3,)] * 1000, [(2000, 3001)], [(5,), (9000,)] * 2600, [(0,), (0, 4)], [(100,)] * 120 + [(0,)],
+         [(100,)] * 121]
 
 
 @pytest.mark.parametrize("types", [(F32,), (BF16,), (F32, BF16)])

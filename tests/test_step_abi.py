@@ -34,6 +34,9 @@ def test_xent_sizes():
     n, v = 1 << 17, 131072
     assert fg.gift_xent_forward_workspace_bytes(n, 4096, v) < 4 * n * v / 16
     assert fg.gift_xent_backward_workspace_bytes(n, 4096, v) < 4 * n * v / 4
+    for dtype in (torch.float16, torch.float64, None):
+        with pytest.raises(ValueError, match="dtype"):
+            fg.gift_xent_backward_workspace_bytes(5, 64, 100, dtype=dtype)
 
 
 @pytest.mark.parametrize("want,case", [
