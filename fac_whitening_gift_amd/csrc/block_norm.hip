@@ -137,9 +137,10 @@ __device__ __forceinline__ void row_stats(const Cols<kL, kNV, kTail>& c, float (
   rstd = 1.0f / sqrtf(group_sum<kL>(q, buf[1]) / (float)c.d + eps);
 }
 
-// Bound by memory: 16384 x 4096 bf16 with post, gate and weights 110 us, 537 MB
-// at 4.9 TB/s (a copy of 4 GB: 4.9); an fp32 stream beside bf16 145 us (5.5),
-// fp32 200 (5.4).  256 lanes of 16 columns: 128 of 32 took 135 us, 512 of 8 113.
+// Bound by memory: 16384 x 4096 bf16 with post, gate and weights 102 us, 537 MB
+// at 5.3 TB/s (a copy of 4 GB: 4.9); an fp32 stream beside bf16 145 us (5.5),
+// fp32 198 (5.4); 16384 x 4095 bf16 144.  256 lanes of 16 columns: 128 of 32 took
+// 135 us, 512 of 8 113.
 template <class TY, class TH, int kL, int kNV, bool kTail>
 __global__ __launch_bounds__(group_threads(kL)) void k_block_fwd(BlockFwd a) {
   constexpr int kGroups = group_threads(kL) / kL;
@@ -210,9 +211,12 @@ struct BlockBwd {
 //
 // The next row is fetched ahead, except where 1024 lanes leave too few registers
 // for that.  Bound by memory: 16384 x 4096 bf16 with gate and weights 168 us, 806
-// MB at 4.8 TB/s, of it 8 for the sums; with the vectors read from memory in each
-// row 200, with 512 lanes of 8 columns 262.  Few rows are bound by the chain of a
-// run: 1000 x 1536 fp32 16.6 us, in runs of 2 and of 8 rows 20.
+// MB at 4.8 TB/s, and 8 for the sums of its runs; with the vectors read from memory
+// in each row 200, with 512 lanes of 8 columns 262; 16384 x 4095 192.  Rows above
+// 8192 columns, whose lanes have 128 registers each, 4096 x 16384 bf16 315 us
+// without biases (2.6 TB/s), with them 650 (spilled; with their other sums in
+// registers too 484 and 781).  Few rows are bound by the chain of a run: 1000 x 1536
+// fp32 16.4 us, in runs of 2 and of 8 rows 20.
 template <class TY, class TH, int kL, int kNV, bool kTail, bool kBias>
 __global__ __launch_bounds__(group_threads(kL)) void k_block_bwd(BlockBwd a) {
   constexpr int kGroups = group_threads(kL) / kL, kW = waves_of(kL), kThreads = group_threads(kL);

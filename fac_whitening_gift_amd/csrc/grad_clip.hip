@@ -9,10 +9,9 @@
 //                  so that clipping takes two launches; then scales its run
 //
 // Bound by memory.  778 M fp32 elements (3.1 GB, 219 tensors) into other buffers:
-// 546 us for the squares (5.7 TB/s) and 1200 us for the scaling (5.2; a copy of
-// 4 GB runs at 4.9), of the two launches that put the descriptors into memory 5
-// each; 12.8 M elements of 9 tensors, which stay in the memory-side cache, 9.4
-// and 17 us.
+// 514 us for the squares (6.1 TB/s), 1231 for the scaling (5.1; a copy of 4 GB runs
+// at 4.9), 9 for the two launches that put the descriptors into memory; 12.8 M
+// elements of 9 tensors, which stay in the memory-side cache, 10.6 and 17 us.
 #include "device.hpp"
 #include "host.hpp"
 #include "mx.hpp"
