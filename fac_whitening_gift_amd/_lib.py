@@ -1122,8 +1122,8 @@ def gift_block_norm_backward(dx, dh, y, h_out, stats, weight=None, bias=None, po
 
 class TensorGroup:
     """Contiguous device tensors (fp32 or bf16, on one device, no element in two of
-    them) that are worked on together, their descriptors made once: the gradients of a model, which stay
-    where they are from step to step."""
+    them) that are worked on together, their descriptors made once: the gradients
+    of a model, which stay where they are from step to step."""
 
     __slots__ = ("tensors", "device", "_array")
 
@@ -1183,8 +1183,9 @@ def gift_grad_norm(tensors, norm=None, sumsq=None, flags=None, ws=None, stream=N
 
 def gift_grad_clip(tensors, max_norm, eps=1e-6, out=None, sumsq=None, norm=None, flags=None, ws=None, stream=None):
     """Scale tensors (a list, or a TensorGroup) by min(1, max_norm / (norm +
-    eps)), in place or into out (as many of the same sizes and types).  sumsq:
-    one fp64 element to go by instead of the tensors' own sum of squares.
+    eps)), in place or into out (as many of the same sizes and types, each the
+    tensor itself or apart from all of them).  sumsq: one fp64 element to go by
+    instead of the tensors' own sum of squares.
     -> norm (1 fp32 element)."""
     group = _group(tensors)
     dev = group.device

@@ -164,8 +164,8 @@ __device__ __forceinline__ void load_tile(const T* base, int vecs, uint4 (&q)[kV
 }
 
 // sum of squares of a tile, its loads unconditional where it is whole: one branch
-// a vector makes each wait for the one before (880 -> 546 us); the elements past its whole vectors go to the first
-// threads
+// a vector makes each wait for the one before (880 -> 546 us); the elements past
+// its whole vectors go to the first threads
 template <class T>
 __device__ __forceinline__ double tile_square(const T* p, int n) {
   constexpr int kE = Lane<T>::kE;

@@ -906,14 +906,15 @@ void launch_gemm(const XeGemm& g, hipStream_t s) {
 }
 
 // Ways to split a sum of `steps` k steps: enough workgroups to fill the chip,
-// at least 8 steps each.
+// at least 8 steps each.  As many as splits of equal length make, so that fewer
+// steps (a last piece) never make more.
 int splits(int64_t M, int64_t N, int64_t steps) {
   const bool big = big_tiles(M, N, steps);
   const int64_t tiles = up_div(M, big ? Big::kRows : Half::kRows) * up_div(N, kTn);
   int64_t n = (big ? 256 : 512) / tiles;
   if (n > steps / 8) n = steps / 8;
   if (n > 32) n = 32;
-  return n < 1 ? 1 : (int)n;
+  return n < 1 ? 1 : (int)up_div(steps, up_div(steps, n));
 }
 
 // rows of a forward launch: their parts of the sums stay within 256 MB
